@@ -220,6 +220,122 @@ moe_status moe_dense_forward(int64_t N, int32_t D, int32_t dff, int32_t dtype, f
                              const void* gate, const void* up, const void* down, void* y, void* workspace,
                              size_t ws_bytes, void* stream);
 
+/* ---- The operators around the experts --------------------------------------------------------------
+ *
+ * For models that hold more than the fused layer: the norms, gate and residual on both sides of a block,
+ * the experts' products as separate calls (other activations, adapters, training), the combine of their
+ * rows, and experts with 4-bit weights. They work on the same lists as the layer (moe_route,
+ * moe_dispatch). The conventions at the top hold: 16-byte aligned contiguous device pointers, the
+ * caller's stream and workspace, errors found on the host before any launch, no atomics (the same inputs
+ * give the same bits). Calls that write gradients overwrite them.
+ */
+
+/* Norms before and after a block, fused with the block's gate and the residual scale:
+ *   h_out = residual_scale * h + gate * (o / rms(o)) * w_post,   u = (h_out / rms(h_out)) * w_pre,
+ *   rms(v) = sqrt(mean(v^2) + eps) over the D features of a row.
+ * One call closes a block (o is its output) and opens the next (u is its input). Parts that are absent:
+ *   o == NULL      the norm before a block alone: u from h. w_post, gate and h_out are NULL, residual_scale
+ *                  is not used.
+ *   w_pre == NULL  the end of a block alone: h_out. u is NULL.
+ *   w_post == NULL o enters as it is, without a norm.   gate == NULL: 1.
+ *   h, o, h_out, u [N, D] of dtype; w_post, w_pre [D] of dtype
+ *   gate    [ceil(N / gate_rows), D] of dtype: row n uses gate row n / gate_rows (gate_rows >= N: one row
+ *           for all; 1: a row per token; a sequence's length: one per sequence)
+ * Float32 arithmetic; h_out and u are each rounded once, u from the unrounded h_out. h_out may be h
+ * (in place); no other overlap. D: a multiple of 64, at most 16384. N = 0 launches nothing. */
+moe_status moe_block_norm(int64_t N, int32_t D, int32_t dtype, float eps, float residual_scale, const void* h,
+                          const void* o, const void* w_post, const void* gate, int64_t gate_rows, const void* w_pre,
+                          void* h_out, void* u, void* stream);
+
+/* Gradients of moe_block_norm, from the tensors of the forward call (nothing else is kept):
+ *   h_out   [N, D]: the forward's h_out, or its h when o == NULL (not read, and may be NULL, without w_pre)
+ *   dh_out, du: the gradients of h_out and u. dh_out may be NULL (zero) when du is given; du is NULL
+ *           without w_pre. With o == NULL, dh_out is what reaches h beside the norm.
+ *   dh [N, D], d_o [N, D] (NULL without o) of dtype, written
+ *   dw_post [D], dgate [ceil(N / gate_rows), D], dw_pre [D] float32, written, or NULL where not wanted:
+ *           sums over rows in a fixed order
+ *   workspace: at least moe_block_norm_workspace_size(N, D, dtype, gate ? gate_rows : 0) bytes (may be NULL
+ *           when no sum is wanted). The size never falls as N grows.
+ * dh may be dh_out (in place); no other overlap. residual_scale has no gradient. N = 0 writes zeros to
+ * dw_post and dw_pre. */
+size_t moe_block_norm_workspace_size(int64_t N, int32_t D, int32_t dtype, int64_t gate_rows);
+moe_status moe_block_norm_backward(int64_t N, int32_t D, int32_t dtype, float eps, float residual_scale,
+                                   const void* h_out, const void* o, const void* w_post, const void* gate,
+                                   int64_t gate_rows, const void* w_pre, const void* dh_out, const void* du, void* dh,
+                                   void* d_o, float* dw_post, float* dgate, float* dw_pre, void* workspace,
+                                   size_t ws_bytes, void* stream);
+
+/* The combine as a call of its own ("MoE Forward", eq. y_n, for expert rows that are not weighted yet):
+ *   y[n] = alpha * sum over the slots s of topk_w[n, s] * rows[inv_row[n, s]]  +  shared[n]
+ *   rows [R, D], shared [N, D] or NULL, y [N, D] of dtype; inv_row [N, k] int32 as moe_dispatch writes it;
+ *   topk_w [N, k] float32 or NULL (all 1: the gradient of a gathered token is the sum of its rows').
+ * Slots whose entry is outside [0, R) add nothing. Float32 sums in slot order, one rounding. y may be
+ * shared (in place) but not rows. k: 1..32; D: a multiple of 64. N = 0 launches nothing. */
+moe_status moe_combine(int64_t N, int32_t k, int32_t D, int32_t dtype, const void* rows, int64_t R,
+                       const int32_t* inv_row, const float* topk_w, const void* shared, float alpha, void* y,
+                       void* stream);
+
+/* Gradients of moe_combine:
+ *   drows[inv_row[n, s]] = alpha * topk_w[n, s] * dy[n]   (of dtype)
+ *   dtopk_w[n, s]        = alpha * <dy[n], rows[inv_row[n, s]]>   (float32; 0 for an empty slot)
+ * The entries of inv_row inside [0, R) are distinct, as moe_dispatch writes them; rows that no slot names
+ * are left as they were. dtopk_w may be NULL (not wanted; rows may then be NULL too) and is NULL without
+ * topk_w. The gradient of shared is dy. drows overlaps neither dy nor rows. */
+moe_status moe_combine_backward(int64_t N, int32_t k, int32_t D, int32_t dtype, const void* dy, const void* rows,
+                                int64_t R, const int32_t* inv_row, const float* topk_w, float alpha, void* drows,
+                                float* dtopk_w, void* stream);
+
+/* A bias-free linear map per expert over rows grouped by expert, ragged sizes, and its gradients. Expert e
+ * has the rows r in [offsets[e], offsets[e + 1]):
+ *   moe_grouped_linear        y[r]  = W[e] x[src(r)]
+ *   moe_grouped_linear_dgrad  dx[r] = W[e]^T dy[r]
+ *   moe_grouped_linear_wgrad  dW[e] = sum over the expert's rows of dy[r] x[src(r)]^T   (0 without rows)
+ *   W, dW [E, out, in], y, dy [R, out], dx [R, in] of dtype
+ *   x       [x_rows, in] of dtype; src(r) = row_index[r] / index_div with row_index [R] int32 (moe_dispatch's
+ *           sorted_pair with index_div = k gathers tokens), or r when row_index is NULL (x_rows >= R)
+ *   offsets [E + 1] int32 on the device, ascending, as moe_dispatch writes them. Rows outside
+ *           [offsets[0], offsets[E]) belong to no expert: no output row of theirs is written.
+ *   workspace: at least moe_grouped_workspace_size(E, R, dtype) bytes (wgrad without row_index: may be NULL).
+ *           The size never falls as R grows.
+ * dx holds one row per grouped row: the gradient of a gathered token is moe_combine of its rows with
+ * topk_w == NULL. Offsets and indices are read on the device and kept in range there: offsets outside [0, R]
+ * or out of order and indices outside [0, x_rows * index_div) give unspecified values, never an access
+ * outside the buffers. Float32 sums over the whole reduction, one rounding. E: 1..512; in and out:
+ * multiples of 64, in * out below 2^31; bf16: gathered x below 4 GiB. R = 0 launches nothing (wgrad: writes
+ * zeros). No overlap between an output and an input. */
+size_t moe_grouped_workspace_size(int32_t E, int64_t R, int32_t dtype);
+moe_status moe_grouped_linear(int32_t E, int64_t R, int32_t in, int32_t out, int32_t dtype, const void* x,
+                              int64_t x_rows, const int32_t* row_index, int32_t index_div, const void* w,
+                              const int32_t* offsets, void* y, void* workspace, size_t ws_bytes, void* stream);
+moe_status moe_grouped_linear_dgrad(int32_t E, int64_t R, int32_t in, int32_t out, int32_t dtype, const void* dy,
+                                    const void* w, const int32_t* offsets, void* dx, void* workspace, size_t ws_bytes,
+                                    void* stream);
+moe_status moe_grouped_linear_wgrad(int32_t E, int64_t R, int32_t in, int32_t out, int32_t dtype, const void* dy,
+                                    const void* x, int64_t x_rows, const int32_t* row_index, int32_t index_div,
+                                    const int32_t* offsets, void* dw, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
+/* moe_grouped_linear with 4-bit weights and one scale per group of a weight row:
+ *   W[e, m, i] = (q[e, m, i] - 8) * scales[e, m, i / group],   q in 0..15
+ *   wq      [E, out, in / 2] uint8: two values a byte, even i in the low four bits
+ *   scales  [E, out, in / group] bf16, finite; group 32, 64 or 128, dividing in
+ *   x, y    bf16; x, x_rows, row_index, index_div, offsets, rows as for moe_grouped_linear. With E = 1 offsets
+ *           may be NULL: all R rows (a plain 4-bit linear map).
+ *   swiglu  1: the rows of W are [0, out / 2) gate and [out / 2, out) up, and y [R, out / 2] is
+ *           SiLU(W_gate x) * W_up x, clamped by swiglu_limit > 0 as in moe_config (out a multiple of 128).
+ *           0: y [R, out], swiglu_limit 0.
+ * Float32 sums; no weight and no partial sum is rounded to fewer bits. Sums of |x| over one group have to stay
+ * below 2^120 (the products carry an offset of 136). No workspace. x does not overlap y. R = 0 launches nothing. */
+moe_status moe_qlinear(int32_t E, int64_t R, int32_t in, int32_t out, int32_t group, const void* x, int64_t x_rows,
+                       const int32_t* row_index, int32_t index_div, const void* wq, const void* scales,
+                       const int32_t* offsets, int32_t swiglu, float swiglu_limit, void* y, void* stream);
+
+/* Weights for moe_qlinear from w [rows, in] of dtype (rows = E * out): scale = bf16(max|w| / 7) over each
+ * group, q = 8 + the nearest integer (ties to even) of the float32 quotient w / scale, kept in 0..15; a
+ * group of zeros has scale 0 and q = 8. */
+moe_status moe_quantize(int32_t dtype, int64_t rows, int32_t in, int32_t group, const void* w, void* wq, void* scales,
+                        void* stream);
+
 /* Static string naming a status. */
 const char* moe_status_str(moe_status status);
 

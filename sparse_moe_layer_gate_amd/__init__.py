@@ -21,7 +21,9 @@ MOE_ROUTE_SCORES_IN, MOE_ROUTE_SCORES_OUT, MOE_ROUTE_PREPARED = 1, 2, 4
 EXPORTED = ["moe_check_config", "moe_workspace_size", "moe_dispatch_workspace_size", "moe_router_prepared_size",
             "moe_router_prepare", "moe_route", "moe_dispatch", "moe_forward", "moe_forward_routed",
             "moe_forward_noalloc", "moe_noalloc_scratch_bytes", "moe_dense_workspace_size", "moe_dense_forward",
-            "moe_status_str", "moe_profile_begin",
+            "moe_block_norm", "moe_block_norm_backward", "moe_block_norm_workspace_size", "moe_combine",
+            "moe_combine_backward", "moe_grouped_workspace_size", "moe_grouped_linear", "moe_grouped_linear_dgrad",
+            "moe_grouped_linear_wgrad", "moe_qlinear", "moe_quantize", "moe_status_str", "moe_profile_begin",
             "moe_profile_begin_mask", "moe_profile_end", "moe_stage_name", "moe_stage_count"]
 
 
@@ -92,6 +94,25 @@ def lib():
         L.moe_dense_forward.argtypes = [i64, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp, ctypes.c_size_t,
                                         vp]
         L.moe_forward.restype = ctypes.c_int
+        f32, sz = ctypes.c_float, ctypes.c_size_t
+        L.moe_block_norm_workspace_size.argtypes = [i64, i32, i32, i64]
+        L.moe_block_norm_workspace_size.restype = sz
+        L.moe_block_norm.argtypes = [i64, i32, i32, f32, f32, vp, vp, vp, vp, i64, vp, vp, vp, vp]
+        L.moe_block_norm_backward.argtypes = [i64, i32, i32, f32, f32, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp,
+                                              vp, vp, sz, vp]
+        L.moe_combine.argtypes = [i64, i32, i32, i32, vp, i64, vp, vp, vp, f32, vp, vp]
+        L.moe_combine_backward.argtypes = [i64, i32, i32, i32, vp, vp, i64, vp, vp, f32, vp, vp, vp]
+        L.moe_grouped_workspace_size.argtypes = [i32, i64, i32]
+        L.moe_grouped_workspace_size.restype = sz
+        L.moe_grouped_linear.argtypes = [i32, i64, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp, vp, sz, vp]
+        L.moe_grouped_linear_dgrad.argtypes = [i32, i64, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_grouped_linear_wgrad.argtypes = [i32, i64, i32, i32, i32, vp, vp, i64, vp, i32, vp, vp, vp, sz, vp]
+        L.moe_qlinear.argtypes = [i32, i64, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp, i32, f32, vp, vp]
+        L.moe_quantize.argtypes = [i32, i64, i32, i32, vp, vp, vp, vp]
+        for fn in (L.moe_block_norm, L.moe_block_norm_backward, L.moe_combine, L.moe_combine_backward,
+                   L.moe_grouped_linear, L.moe_grouped_linear_dgrad, L.moe_grouped_linear_wgrad, L.moe_qlinear,
+                   L.moe_quantize):
+            fn.restype = ctypes.c_int
         L.moe_status_str.argtypes = [ctypes.c_int]
         L.moe_status_str.restype = ctypes.c_char_p
         L.moe_profile_begin.argtypes = []
@@ -341,6 +362,213 @@ def moe_dense_forward(N: int, x, gate, up, down, y, workspace, limit: float = 0.
         _ptr(down, "down", adt, (D, dff)), _ptr(y, "y", adt, (N, D)),
         _ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     _check(st, "moe_dense_forward")
+
+
+# ---- the operators around the experts ----
+def _tensor_dtype(t, name) -> int:
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a device tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return MOE_F32 if t.dtype == torch.float32 else MOE_BF16
+
+
+def _same_device(what, *tensors):
+    """The tensors' one device, made the current one for the launch (and its current stream the default)."""
+    import torch
+
+    devices = {t.device for t in tensors if t is not None}
+    if any(d.type != "cuda" for d in devices):
+        raise TypeError(f"{what}: every tensor must be a device tensor")
+    if len(devices) != 1:
+        raise ValueError(f"{what}: tensors on more than one device: {sorted(map(str, devices))}")
+    return torch.cuda.device(devices.pop())
+
+
+def _ws(workspace):
+    import torch
+
+    return (_ptr(workspace, "workspace", torch.uint8, required=False), 0 if workspace is None else workspace.numel())
+
+
+def moe_block_norm_workspace_size(N: int, D: int, dtype="bf16", gate_rows: int = 0) -> int:
+    """Bytes of workspace of moe_block_norm_backward (gate_rows 0: no gate)."""
+    return int(lib().moe_block_norm_workspace_size(int(N), int(D), _dtype_code(dtype), int(gate_rows)))
+
+
+def moe_block_norm(N: int, h, o, w_post, gate, gate_rows, w_pre, h_out, u, residual_scale: float = 1.0,
+                   eps: float = 1e-5, stream=None):
+    """h_out = residual_scale h + gate (o / rms(o)) w_post and u = (h_out / rms(h_out)) w_pre. Without o (None)
+    u is the norm of h; without w_pre only h_out is written; w_post and gate may be None. Row n uses row
+    n // gate_rows of gate [ceil(N / gate_rows), D]."""
+    dt = _tensor_dtype(h, "h")
+    t, D, T = h.dtype, h.shape[-1], int(gate_rows or 0)
+    groups = (N + T - 1) // T if T > 0 else 0
+    with _same_device("moe_block_norm", h, o, w_post, gate, w_pre, h_out, u):
+        st = lib().moe_block_norm(
+            int(N), int(D), dt, float(eps), float(residual_scale),
+            _ptr(h, "h", t, (N, D)), _ptr(o, "o", t, (N, D), required=False),
+            _ptr(w_post, "w_post", t, (D,), required=False),
+            _ptr(gate, "gate", t, (groups, D), required=False), T,
+            _ptr(w_pre, "w_pre", t, (D,), required=False),
+            _ptr(h_out, "h_out", t, (N, D), required=False), _ptr(u, "u", t, (N, D), required=False),
+            _stream(stream))
+    _check(st, "moe_block_norm")
+
+
+def moe_block_norm_backward(N: int, h_out, o, w_post, gate, gate_rows, w_pre, dh_out, du, dh, d_o, dw_post, dgate,
+                            dw_pre, workspace, residual_scale: float = 1.0, eps: float = 1e-5, stream=None):
+    """Gradients of moe_block_norm from its tensors (h_out: the forward's h when o is None) and the gradients
+    dh_out (or None) and du. Writes dh, d_o and, where given, the float32 sums dw_post, dgate, dw_pre;
+    workspace: moe_block_norm_workspace_size(N, D, dtype, gate_rows) bytes, or None without sums."""
+    import torch
+
+    dt = _tensor_dtype(dh, "dh")
+    t, f, D, T = dh.dtype, torch.float32, dh.shape[-1], int(gate_rows or 0)
+    groups = (N + T - 1) // T if T > 0 else 0
+    ws, ws_bytes = _ws(workspace)
+    with _same_device("moe_block_norm_backward", h_out, o, w_post, gate, w_pre, dh_out, du, dh, d_o, dw_post, dgate,
+                      dw_pre, workspace):
+        st = lib().moe_block_norm_backward(
+            int(N), int(D), dt, float(eps), float(residual_scale),
+            _ptr(h_out, "h_out", t, (N, D), required=False), _ptr(o, "o", t, (N, D), required=False),
+            _ptr(w_post, "w_post", t, (D,), required=False),
+            _ptr(gate, "gate", t, (groups, D), required=False), T,
+            _ptr(w_pre, "w_pre", t, (D,), required=False),
+            _ptr(dh_out, "dh_out", t, (N, D), required=False), _ptr(du, "du", t, (N, D), required=False),
+            _ptr(dh, "dh", t, (N, D)), _ptr(d_o, "d_o", t, (N, D), required=False),
+            _ptr(dw_post, "dw_post", f, (D,), required=False), _ptr(dgate, "dgate", f, (groups, D), required=False),
+            _ptr(dw_pre, "dw_pre", f, (D,), required=False), ws, ws_bytes, _stream(stream))
+    _check(st, "moe_block_norm_backward")
+
+
+def moe_combine(N: int, k: int, rows, inv_row, topk_w, shared, y, alpha: float = 1.0, stream=None):
+    """y[n] = alpha sum_s topk_w[n, s] rows[inv_row[n, s]] + shared[n]; topk_w None: ones, shared None: nothing
+    added. inv_row (N * k int32) as moe_dispatch writes it; entries outside rows are empty slots."""
+    import torch
+
+    dt = _tensor_dtype(rows, "rows")
+    t, (R, D) = rows.dtype, rows.shape
+    with _same_device("moe_combine", rows, inv_row, topk_w, shared, y):
+        st = lib().moe_combine(
+            int(N), int(k), int(D), dt, _ptr(rows, "rows", t), int(R),
+            _ptr(inv_row, "inv_row", torch.int32, (N * k,)),
+            _ptr(topk_w, "topk_w", torch.float32, (N, k), required=False),
+            _ptr(shared, "shared", t, (N, D), required=False), float(alpha), _ptr(y, "y", t, (N, D)),
+            _stream(stream))
+    _check(st, "moe_combine")
+
+
+def moe_combine_backward(N: int, k: int, dy, rows, inv_row, topk_w, drows, dtopk_w, alpha: float = 1.0, stream=None):
+    """drows[inv_row[n, s]] = alpha topk_w[n, s] dy[n] and dtopk_w[n, s] = alpha <dy[n], rows[inv_row[n, s]]>.
+    dtopk_w (and with it rows) may be None; rows that no slot names keep what they held in drows."""
+    import torch
+
+    dt = _tensor_dtype(drows, "drows")
+    t, (R, D) = drows.dtype, drows.shape
+    with _same_device("moe_combine_backward", dy, rows, inv_row, topk_w, drows, dtopk_w):
+        st = lib().moe_combine_backward(
+            int(N), int(k), int(D), dt, _ptr(dy, "dy", t, (N, D)), _ptr(rows, "rows", t, (R, D), required=False),
+            int(R), _ptr(inv_row, "inv_row", torch.int32, (N * k,)),
+            _ptr(topk_w, "topk_w", torch.float32, (N, k), required=False), float(alpha), _ptr(drows, "drows", t),
+            _ptr(dtopk_w, "dtopk_w", torch.float32, (N, k), required=False), _stream(stream))
+    _check(st, "moe_combine_backward")
+
+
+def moe_grouped_workspace_size(E: int, R: int, dtype="bf16") -> int:
+    return int(lib().moe_grouped_workspace_size(int(E), int(R), _dtype_code(dtype)))
+
+
+def moe_grouped_linear(x, w, offsets, y, workspace, row_index=None, index_div: int = 1, stream=None):
+    """y[r] = w[e] x[src(r)] for the rows r in [offsets[e], offsets[e + 1]); w [E, out, in], y [R, out].
+    src(r) = row_index[r] // index_div (moe_dispatch's sorted_pair and k), or r without row_index."""
+    import torch
+
+    dt = _tensor_dtype(x, "x")
+    t, (E, M, K), R = x.dtype, w.shape, y.shape[0]
+    ws, ws_bytes = _ws(workspace)
+    with _same_device("moe_grouped_linear", x, w, offsets, y, workspace, row_index):
+        st = lib().moe_grouped_linear(
+            int(E), int(R), int(K), int(M), dt, _ptr(x, "x", t, (x.shape[0], K)), int(x.shape[0]),
+            _ptr(row_index, "row_index", torch.int32, (R,), required=False), int(index_div), _ptr(w, "w", t),
+            _ptr(offsets, "offsets", torch.int32, (E + 1,)), _ptr(y, "y", t, (R, M)), ws, ws_bytes,
+            _stream(stream))
+    _check(st, "moe_grouped_linear")
+
+
+def moe_grouped_linear_dgrad(dy, w, offsets, dx, workspace, stream=None):
+    """dx[r] = w[e]^T dy[r], one row per grouped row."""
+    import torch
+
+    dt = _tensor_dtype(dy, "dy")
+    t, (E, M, K), R = dy.dtype, w.shape, dx.shape[0]
+    ws, ws_bytes = _ws(workspace)
+    with _same_device("moe_grouped_linear_dgrad", dy, w, offsets, dx, workspace):
+        st = lib().moe_grouped_linear_dgrad(
+            int(E), int(R), int(K), int(M), dt, _ptr(dy, "dy", t, (R, M)), _ptr(w, "w", t),
+            _ptr(offsets, "offsets", torch.int32, (E + 1,)), _ptr(dx, "dx", t, (R, K)), ws, ws_bytes,
+            _stream(stream))
+    _check(st, "moe_grouped_linear_dgrad")
+
+
+def moe_grouped_linear_wgrad(dy, x, offsets, dw, workspace, row_index=None, index_div: int = 1, stream=None):
+    """dw[e] = sum of dy[r] x[src(r)]^T over the rows of expert e (zeros without rows)."""
+    import torch
+
+    dt = _tensor_dtype(dy, "dy")
+    t, (E, M, K), R = dy.dtype, dw.shape, dy.shape[0]
+    ws, ws_bytes = _ws(workspace)
+    with _same_device("moe_grouped_linear_wgrad", dy, x, offsets, dw, workspace, row_index):
+        st = lib().moe_grouped_linear_wgrad(
+            int(E), int(R), int(K), int(M), dt, _ptr(dy, "dy", t, (R, M)), _ptr(x, "x", t, (x.shape[0], K)),
+            int(x.shape[0]), _ptr(row_index, "row_index", torch.int32, (R,), required=False), int(index_div),
+            _ptr(offsets, "offsets", torch.int32, (E + 1,)), _ptr(dw, "dw", t), ws, ws_bytes, _stream(stream))
+    _check(st, "moe_grouped_linear_wgrad")
+
+
+def moe_qlinear(x, wq, scales, y, offsets=None, row_index=None, index_div: int = 1, swiglu: bool = False,
+                limit: float = 0.0, stream=None):
+    """moe_grouped_linear with 4-bit weights: wq [E, out, in / 2] uint8, scales [E, out, in / group] bf16
+    (moe_quantize). offsets None (E = 1): all rows. swiglu: y [R, out / 2] = SiLU(gate half) * up half."""
+    import torch
+
+    E, M, half = wq.shape
+    K = 2 * half
+    if scales.dim() != 3 or scales.shape[2] < 1 or K % scales.shape[2]:
+        raise ValueError(f"scales must have shape (E, out, in / group), got {tuple(scales.shape)}")
+    groups, R, bf = scales.shape[2], y.shape[0], torch.bfloat16
+    with _same_device("moe_qlinear", x, wq, scales, y, offsets, row_index):
+        st = lib().moe_qlinear(
+            int(E), int(R), int(K), int(M), K // groups, _ptr(x, "x", bf, (x.shape[0], K)), int(x.shape[0]),
+            _ptr(row_index, "row_index", torch.int32, (R,), required=False), int(index_div),
+            _ptr(wq, "wq", torch.uint8), _ptr(scales, "scales", bf, (E, M, groups)),
+            _ptr(offsets, "offsets", torch.int32, (E + 1,), required=False), int(bool(swiglu)), float(limit),
+            _ptr(y, "y", bf, (R, M // 2 if swiglu else M)), _stream(stream))
+    _check(st, "moe_qlinear")
+
+
+def moe_quantize(w, group: int, wq=None, scales=None, stream=None):
+    """(wq, scales) of w [..., in] for moe_qlinear: uint8 [..., in / 2] and bf16 [..., in / group], allocated here
+    when None."""
+    import torch
+
+    dt = _tensor_dtype(w, "w")
+    K, lead = w.shape[-1], tuple(w.shape[:-1])
+    if group < 1 or K % group:
+        raise ValueError(f"group {group} does not divide {K}")
+    if wq is None:
+        wq = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=w.device)
+    if scales is None:
+        scales = torch.empty(lead + (K // group,), dtype=torch.bfloat16, device=w.device)
+    rows = w.numel() // K if K else 0
+    with _same_device("moe_quantize", w, wq, scales):
+        st = lib().moe_quantize(dt, rows, int(K), int(group), _ptr(w, "w"),
+                                _ptr(wq, "wq", torch.uint8, lead + (K // 2,)),
+                                _ptr(scales, "scales", torch.bfloat16, lead + (K // group,)), _stream(stream))
+    _check(st, "moe_quantize")
+    return wq, scales
 
 
 def stage_names() -> list:

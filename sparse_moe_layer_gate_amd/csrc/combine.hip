@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "moe_internal.h"
+#include "row_ops.h"
 
 namespace moe {
 namespace {
@@ -23,7 +24,6 @@ template <>
 struct V8<float> {
   float4 a, b;
 };
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 __device__ inline V8<uint16_t> load8(const uint16_t* p) {
   const u32x4 v = __builtin_nontemporal_load((const u32x4*)p);  // each expert row is read once
   return V8<uint16_t>{make_uint4(v.x, v.y, v.z, v.w)};
@@ -93,7 +93,141 @@ __global__ __launch_bounds__(1024) void combine_kernel(const T* __restrict__ Y, 
   }
 }
 
+// moe_combine: the same sum for rows that are not yet weighted, y = alpha sum_s w_s rows[inv_s] + shared.
+// inv_row comes from the caller: an entry outside [0, R) is an empty slot.
+template <typename T>
+__global__ __launch_bounds__(1024) void combine_rows_kernel(const T* __restrict__ rows_in, int64_t R,
+                                                           const int32_t* __restrict__ inv_row,
+                                                           const float* __restrict__ w, const T* __restrict__ shared,
+                                                           int k, int D, float alpha, T* __restrict__ y) {
+  __shared__ int rows[MAX_K];
+  __shared__ float wt[MAX_K];
+  const int64_t n = blockIdx.x;
+  if (threadIdx.x < k) {
+    const int r = inv_row[n * k + threadIdx.x];
+    rows[threadIdx.x] = r >= 0 && r < R ? r : -1;
+    wt[threadIdx.x] = w ? w[n * k + threadIdx.x] : 1.0f;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x * 8; c < D; c += blockDim.x * 8) {
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    Raw8<T> vsh;
+    if (shared) vsh = raw_load8<true>(shared + n * D + c);
+    for (int s0 = 0; s0 < k; s0 += 8) {  // as above: a group's loads first, the sums in slot order
+      Raw8<T> v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int r = s0 + u < k ? rows[s0 + u] : -1;
+        if (r >= 0) v[u] = raw_load8<true>(rows_in + (int64_t)r * D + c);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (s0 + u < k && rows[s0 + u] >= 0) {
+          float f[8];
+          widen8(v[u], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[i] += wt[s0 + u] * f[i];
+        }
+    }
+    float sh[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (shared) widen8(vsh, sh);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[i] = alpha * acc[i] + sh[i];
+    raw_store8(y + n * D + c, acc);
+  }
+}
+
+// Gradients of moe_combine: drows[inv_s] = alpha w_s dy and dw_s = alpha <dy, rows[inv_s]>, one block per
+// token. A token's dy stays in registers over its slots (rows of up to 8192 features); the slots' dot
+// products are summed over the block together, eight at a time. Every row is written by the one slot
+// that names it, so nothing is accumulated in memory.
+template <typename T>
+__global__ __launch_bounds__(1024) void combine_rows_backward_kernel(const T* __restrict__ dy,
+                                                                    const T* __restrict__ rows_in, int64_t R,
+                                                                    const int32_t* __restrict__ inv_row,
+                                                                    const float* __restrict__ w, int k, int D,
+                                                                    float alpha, T* __restrict__ drows,
+                                                                    float* __restrict__ dw) {
+  __shared__ int rows[MAX_K];
+  __shared__ float wt[MAX_K];
+  __shared__ float buf[2][16][8];
+  const int64_t n = blockIdx.x;
+  const int waves = blockDim.x >> 6;
+  if (threadIdx.x < k) {
+    const int r = inv_row[n * k + threadIdx.x];
+    rows[threadIdx.x] = r >= 0 && r < R ? r : -1;
+    wt[threadIdx.x] = alpha * (w ? w[n * k + threadIdx.x] : 1.0f);
+  }
+  __syncthreads();
+  for (int s0 = 0; s0 < k; s0 += 8) {
+    float dot[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int c = threadIdx.x * 8; c < D; c += blockDim.x * 8) {
+      Raw8<T> v[8];
+      if (dw) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int r = s0 + u < k ? rows[s0 + u] : -1;
+          if (r >= 0) v[u] = raw_load8<true>(rows_in + (int64_t)r * D + c);
+        }
+      }
+      float g[8];
+      widen8(raw_load8(dy + n * D + c), g);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int r = s0 + u < k ? rows[s0 + u] : -1;
+        if (r < 0) continue;
+        float f[8];
+        if (dw) {
+          widen8(v[u], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot[u] += g[i] * f[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = wt[s0 + u] * g[i];
+        raw_store8(drows + (int64_t)r * D + c, f);
+      }
+    }
+    if (!dw) continue;
+    block_sums<8>(dot, buf[(s0 >> 3) & 1], waves);
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (s0 + u < k) dw[n * k + s0 + u] = rows[s0 + u] >= 0 ? alpha * dot[u] : 0.f;
+    }
+  }
+}
+
+int combine_threads(int D) {
+  const int threads = (D / 8 + 63) / 64 * 64;
+  return threads > 1024 ? 1024 : threads;
+}
+
 }  // namespace
+
+hipError_t launch_combine_rows(int dtype, const void* rows, int64_t R, const int32_t* inv_row, const float* w,
+                               const void* shared, int64_t N, int k, int D, float alpha, void* y, hipStream_t s) {
+  const dim3 grid((unsigned)N), block(combine_threads(D));
+  if (dtype == MOE_F32)
+    hipLaunchKernelGGL(combine_rows_kernel<float>, grid, block, 0, s, (const float*)rows, R, inv_row, w,
+                       (const float*)shared, k, D, alpha, (float*)y);
+  else
+    hipLaunchKernelGGL(combine_rows_kernel<uint16_t>, grid, block, 0, s, (const uint16_t*)rows, R, inv_row, w,
+                       (const uint16_t*)shared, k, D, alpha, (uint16_t*)y);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_rows_backward(int dtype, const void* dy, const void* rows, int64_t R,
+                                        const int32_t* inv_row, const float* w, int64_t N, int k, int D, float alpha,
+                                        void* drows, float* dw, hipStream_t s) {
+  const dim3 grid((unsigned)N), block(combine_threads(D));
+  if (dtype == MOE_F32)
+    hipLaunchKernelGGL(combine_rows_backward_kernel<float>, grid, block, 0, s, (const float*)dy, (const float*)rows, R,
+                       inv_row, w, k, D, alpha, (float*)drows, dw);
+  else
+    hipLaunchKernelGGL(combine_rows_backward_kernel<uint16_t>, grid, block, 0, s, (const uint16_t*)dy,
+                       (const uint16_t*)rows, R, inv_row, w, k, D, alpha, (uint16_t*)drows, dw);
+  return hipGetLastError();
+}
 
 hipError_t launch_combine(int dtype, const void* Y, const void* Ysh, const int32_t* inv_row, int64_t N, int k, int D,
                           float alpha_out, void* y, hipStream_t s) {

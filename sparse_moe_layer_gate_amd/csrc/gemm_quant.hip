@@ -1,0 +1,332 @@
+// Products with 4-bit weights and one scale per group of a weight row, dense or grouped by expert:
+//
+//   y[r, m] = sum_k x[src(r), k] (q[e, m, k] - 8) s[e, m, k / group]
+//
+// q holds two 4-bit values a byte, even k in the low half; groups of 32, 64 or 128. With few rows per
+// expert the product is a stream of the weights (half a byte each), so the weights go straight from
+// memory to registers in 16-byte pieces of 32 values, several pieces ahead of their use, and are made
+// into matrix operands with one instruction per value:
+//  - 0x4300 | q is the bfloat16 128 + q, exactly, so two values of a word become a pair with one
+//    and-or: (w & 0x000f000f) | 0x43004300 gives values 0 and 4 of the word, w >> 4 values 1 and 5, ...
+//    (the activations are laid out in LDS in that order);
+//  - the products run on the integers 128 + q, v_mfma_f32_16x16x32_bf16 with float32 sums over one
+//    group; the surplus 136 sum(x) is taken out by one more product with the constant -136 (exact in
+//    bfloat16), shared by all weight tiles of the wave; then the group's sum is scaled in float32 and
+//    added. Neither a weight nor a scaled partial sum is ever rounded to bfloat16.
+// A lane's 16 bytes are 32 consecutive k of one weight row. Groups of 128 take them as they are (four
+// matrix steps that each cross the four 32-value pieces); smaller groups first exchange the four words
+// among the four lanes of a row (permlane swaps), so that a step's 32 values are consecutive.
+#include <hip/hip_runtime.h>
+
+#include "moe_internal.h"
+#include "row_ops.h"
+
+namespace moe {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int SEG = 128;           // k per 16-byte piece of the four lanes of a row
+constexpr int NSEG = 4;            // pieces per batch: a wave's loads in flight per weight tile
+constexpr int BATCH = SEG * NSEG;  // k per wave and batch
+
+// TT: 16-row activation tiles per block; KS: waves that split k (the other factor of the four waves splits
+// the weight rows). Each wave holds two 16-row weight tiles: with SWIGLU a gate tile and its up tile.
+template <int TT, int KS>
+struct QTile {
+  static constexpr int ROWS = 16 * TT;
+  static constexpr int WAVE_N = 4 / KS;                 // waves over weight rows
+  static constexpr int LDS_ELEMS = 32768 + 8 * ROWS;    // activations of a chunk, rows padded by 8
+  static constexpr int STEP = KS * BATCH;               // k per batch of the block
+  // k per chunk for a tile of `rows` activation rows: what the LDS holds, no more than the row needs
+  __device__ static int chunk(int rows, int K) {
+    return min(32768 / rows / STEP * STEP, (K + STEP - 1) / STEP * STEP);
+  }
+};
+
+__device__ inline bf16x8 unpack8(uint32_t w) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// The four words of the four lanes of a row, transposed: lane group j receives word j of lane groups 0..3.
+__device__ inline void exchange4(u32x4& d) {
+  auto a = __builtin_amdgcn_permlane32_swap(d[0], d[2], false, false);
+  auto b = __builtin_amdgcn_permlane32_swap(d[1], d[3], false, false);
+  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  auto e = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  d[0] = c[0];
+  d[1] = c[1];
+  d[2] = e[0];
+  d[3] = e[1];
+}
+
+template <int TT, int KS, int G, bool SWIGLU>
+__global__ __launch_bounds__(256) void qlinear_kernel(QuantArgs a) {
+  using T = QTile<TT, KS>;
+  constexpr int RT = 2;                       // weight tiles per wave
+  constexpr int GPS = SEG / G;                // groups per piece
+  constexpr int STEPS = G / 32;               // matrix steps per group
+  __shared__ __attribute__((aligned(16))) uint16_t xs[T::LDS_ELEMS];
+  __shared__ int src_rows[T::ROWS];
+
+  const int expert = blockIdx.y;
+  int64_t row0 = 0, cnt = a.R;
+  if (a.offsets) {
+    row0 = min(max((int64_t)a.offsets[expert], (int64_t)0), a.R);
+    cnt = min(max((int64_t)a.offsets[expert + 1], row0), a.R) - row0;
+  }
+  const int K = a.K;
+  const int half = a.M / 2;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kw = wave % KS, nw = wave / KS;   // this wave's k share and weight rows
+  const int r16 = lane & 15, j = lane >> 4;
+  // output columns of the block, and this wave's two weight tiles
+  constexpr int WCOLS = SWIGLU ? 16 : 32;
+  const int ncols = SWIGLU ? half : a.M;
+  const int col0 = (blockIdx.x * T::WAVE_N + nw) * WCOLS;
+  const uint8_t* wq[RT];
+  const uint16_t* ws[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    int m = SWIGLU ? t * half + min(col0, ncols - WCOLS) : min(col0, ncols - WCOLS) + 16 * t;
+    const int64_t row = (int64_t)expert * a.M + m + r16;
+    wq[t] = a.q + row * (K / 2);
+    ws[t] = a.s + row * (K / G);
+  }
+  const u32x4 neg = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};  // -136 as bfloat16 pairs
+  const bf16x8 minus136 = __builtin_bit_cast(bf16x8, neg);
+
+  for (int64_t tile0 = (int64_t)blockIdx.z * T::ROWS; tile0 < cnt; tile0 += (int64_t)gridDim.z * T::ROWS) {
+    const int rows = (int)min((int64_t)T::ROWS, cnt - tile0);
+    const int kc = T::chunk(rows, K);
+    const int pitch = kc + 8;
+    __syncthreads();  // the previous tile's LDS reads are over
+    if (tid < rows) {
+      int64_t r = row0 + tile0 + tid;
+      if (a.row_index) {
+        r = a.row_index[r] / a.div;
+        r = min(max(r, (int64_t)0), a.x_rows - 1);
+      }
+      src_rows[tid] = (int)r;
+    }
+    f32x4 acc[TT][RT];
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+      for (int t = 0; t < RT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    u32x4 q[RT][NSEG];
+    uint16_t sc[RT][NSEG][GPS];
+    // this wave's batch at k0: 16 bytes per piece and weight tile, and the pieces' scales; past K the last
+    // valid piece again (the activations there are zero)
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int p = 0; p < NSEG; ++p) {
+        const int k = min(k0 + p * SEG + j * 32, K - 32);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          // one row tile per expert: the bytes are used once; more of them share the weights in L2
+          if (TT == 1)
+            q[t][p] = __builtin_nontemporal_load((const u32x4*)(wq[t] + (k >> 1)));
+          else
+            q[t][p] = *(const u32x4*)(wq[t] + (k >> 1));
+#pragma unroll
+          for (int g = 0; g < GPS; ++g) sc[t][p][g] = ws[t][min((k0 + p * SEG) / G + g, K / G - 1)];
+        }
+      }
+    };
+    load(kw * BATCH);
+    for (int c0 = 0; c0 < K; c0 += kc) {
+      __syncthreads();  // src_rows is written; the previous chunk's reads are over
+      // stage rows x kc activations (zeros past K), values 0 4 1 5 2 6 3 7 of every eight
+      const int pieces = kc / 8;
+      for (int c = tid; c < rows * pieces; c += 256) {
+        const int r = c / pieces, kk = (c % pieces) * 8;
+        u32x4 v = {0, 0, 0, 0};
+        if (c0 + kk < K) v = *(const u32x4*)(a.x + (int64_t)src_rows[r] * K + c0 + kk);
+        u32x4 w;
+        w[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100);
+        w[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302);
+        w[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100);
+        w[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302);
+        *(u32x4*)(xs + r * pitch + kk) = w;
+      }
+      __syncthreads();
+      for (int b0 = kw * BATCH; b0 < kc && c0 + b0 < K; b0 += T::STEP) {
+        u32x4 cq[RT][NSEG];
+        uint16_t cs[RT][NSEG][GPS];
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int p = 0; p < NSEG; ++p) {
+            cq[t][p] = q[t][p];
+#pragma unroll
+            for (int g = 0; g < GPS; ++g) cs[t][p][g] = sc[t][p][g];
+          }
+        // the next batch is STEP further on, within the chunk or at the next one's start (chunks are
+        // whole steps); nothing is read past the row
+        if (c0 + b0 + T::STEP < K) load(c0 + b0 + T::STEP);
+#pragma unroll
+        for (int p = 0; p < NSEG; ++p) {
+          if (c0 + b0 + p * SEG >= K) break;
+          if (G < SEG) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) exchange4(cq[t][p]);
+          }
+          const uint16_t* xp = xs + b0 + p * SEG;
+#pragma unroll
+          for (int g = 0; g < GPS; ++g) {
+            f32x4 sum[TT][RT];
+            bf16x8 xf[STEPS][TT];
+#pragma unroll
+            for (int i = 0; i < TT; ++i) {
+              f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int u = 0; u < STEPS; ++u) {
+                const int piece = G < SEG ? 4 * (g * STEPS + u) + j : 4 * j + u;
+                xf[u][i] = *(const bf16x8*)(xp + min(16 * i + r16, rows - 1) * pitch + piece * 8);
+                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], minus136, c, 0, 0, 0);
+              }
+#pragma unroll
+              for (int t = 0; t < RT; ++t) sum[i][t] = c;
+            }
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+#pragma unroll
+              for (int u = 0; u < STEPS; ++u) {
+                const bf16x8 w = unpack8(cq[t][p][g * STEPS + u]);
+#pragma unroll
+                for (int i = 0; i < TT; ++i)
+                  sum[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, sum[i][t], 0, 0, 0);
+              }
+              const float s = bf16_f32(cs[t][p][g]);
+#pragma unroll
+              for (int i = 0; i < TT; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][t][r] += s * sum[i][t][r];
+            }
+          }
+        }
+      }
+    }
+    // the waves that split k: partial sums through LDS, added in wave order by the first of them
+    if (KS > 1) {
+      constexpr int PER = TT * RT * 4;
+      float* red = (float*)xs;  // [4 waves][PER][64 lanes]
+      static_assert(4 * PER * 64 * 4 <= T::LDS_ELEMS * 2, "the partial sums fit the activations' space");
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) red[(wave * PER + (i * RT + t) * 4 + r) * 64 + lane] = acc[i][t][r];
+      __syncthreads();
+      if (kw == 0) {
+#pragma unroll
+        for (int i = 0; i < TT; ++i)
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              float v = acc[i][t][r];
+              for (int w = 1; w < KS; ++w) v += red[((wave + w) * PER + (i * RT + t) * 4 + r) * 64 + lane];
+              acc[i][t][r] = v;
+            }
+      }
+    }
+    if (kw == 0 && col0 < ncols) {
+#pragma unroll
+      for (int i = 0; i < TT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * i + 4 * j + r;
+          if (row >= rows) continue;
+          uint16_t* y = a.y + (row0 + tile0 + row) * ncols + col0 + r16;
+          if (SWIGLU) {
+            y[0] = (uint16_t)bf16_pair(swiglu_bf16(acc[i][0][r], acc[i][1][r], a.limit), 0.f);
+          } else {
+            y[0] = (uint16_t)bf16_pair(acc[i][0][r], 0.f);
+            y[16] = (uint16_t)bf16_pair(acc[i][1][r], 0.f);
+          }
+        }
+    }
+  }
+}
+
+template <int TT, int KS, int G>
+hipError_t launch_q(const QuantArgs& a, hipStream_t s) {
+  using T = QTile<TT, KS>;
+  const int wcols = (a.swiglu ? 16 : 32) * T::WAVE_N, ncols = a.swiglu ? a.M / 2 : a.M;
+  int64_t z = (a.R + (int64_t)a.E * T::ROWS - 1) / ((int64_t)a.E * T::ROWS);  // even load: one tile per block
+  if (z > 65535) z = 65535;
+  const dim3 grid((ncols + wcols - 1) / wcols, a.E, (unsigned)z);
+  if (a.swiglu)
+    hipLaunchKernelGGL((qlinear_kernel<TT, KS, G, true>), grid, dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((qlinear_kernel<TT, KS, G, false>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int TT, int KS>
+hipError_t launch_group(const QuantArgs& a, hipStream_t s) {
+  if (a.group == 32) return launch_q<TT, KS, 32>(a, s);
+  if (a.group == 64) return launch_q<TT, KS, 64>(a, s);
+  return launch_q<TT, KS, 128>(a, s);
+}
+
+// One thread per eight values, group / 8 neighbouring lanes per group: the group's largest magnitude over
+// 7, rounded to bfloat16, is the scale; a value is the nearest integer (ties to even) of its quotient by
+// that scale, kept within [-8, 7]. A group of zeros has the scale 0 and the values 0.
+template <typename T>
+__global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ w, int64_t pieces, int lanes_per_group,
+                                                       uint32_t* __restrict__ q, uint16_t* __restrict__ s) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool live = i < pieces;
+  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (live) widen8(raw_load8(w + i * 8), f);
+  float m = 0.f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) m = fmaxf(m, fabsf(f[u]));
+  for (int off = 1; off < lanes_per_group; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
+  const uint16_t sb = (uint16_t)bf16_pair(m / 7.0f, 0.f);
+  const float sf = bf16_f32(sb);
+  uint32_t word = 0;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const float v = sf > 0.f ? fminf(fmaxf(rintf(f[u] / sf), -8.f), 7.f) : 0.f;
+    word |= (uint32_t)((int)v + 8) << (4 * u);
+  }
+  if (!live) return;
+  q[i] = word;
+  if (i % lanes_per_group == 0) s[i / lanes_per_group] = sb;
+}
+
+}  // namespace
+
+hipError_t launch_qlinear(const QuantArgs& a, hipStream_t s) {
+  if (a.R <= (int64_t)16 * a.E) return launch_group<1, 4>(a, s);
+  return launch_group<4, 1>(a, s);
+}
+
+hipError_t launch_quantize(int dtype, const void* w, int64_t rows, int K, int group, uint8_t* q, uint16_t* s,
+                           hipStream_t st) {
+  const int64_t pieces = rows * (K / 8);
+  const int64_t blocks = (pieces + 255) / 256;
+  if (blocks == 0) return hipSuccess;
+  if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  if (dtype == MOE_F32)
+    hipLaunchKernelGGL(quantize_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, st, (const float*)w, pieces,
+                       group / 8, (uint32_t*)q, s);
+  else
+    hipLaunchKernelGGL(quantize_kernel<uint16_t>, dim3((unsigned)blocks), dim3(256), 0, st, (const uint16_t*)w, pieces,
+                       group / 8, (uint32_t*)q, s);
+  return hipGetLastError();
+}
+
+}  // namespace moe

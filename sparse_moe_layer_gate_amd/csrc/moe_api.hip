@@ -196,15 +196,8 @@ hipEvent_t next_event() {
 
 const char* kStageNames[ST_COUNT_STAGES] = {"router_split", "router_logits", "router_select",  "dispatch_count",
                                             "dispatch_scan", "dispatch_place", "experts_gate_up", "experts_down",
-                                            "combine"};
-
-#define MOE_TRY(stage, expr)                 \
-  do {                                       \
-    prof_before((stage), s);                 \
-    const hipError_t e_ = (expr);            \
-    prof_after((stage), s);                  \
-    if (e_ != hipSuccess) return MOE_ERR_HIP; \
-  } while (0)
+                                            "combine", "block_norm", "grouped_lists", "grouped_linear", "qlinear",
+                                            "quantize"};
 
 // Router. wg is the float32 router weight, or (prepared) the three bf16 pieces of moe_router_prepare;
 // scores is read (MOE_ROUTE_SCORES_IN), written (non-null otherwise) or not kept (null).

@@ -1,0 +1,567 @@
+"""The operators around the experts on the GPU, through the C ABI, against float64 references on the CPU
+(tests/_ops.py, where the bounds are derived)."""
+import pytest
+import torch
+
+import sparse_moe_layer_gate_amd as moe
+import synth
+from tests import _harness as H
+from tests import _ops as O
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+TYPES = {"bf16": BF, "f32": F32}
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+def workspace(n):
+    return torch.empty(max(int(n), 256), dtype=torch.uint8, device="cuda").fill_(0xFF)
+
+
+# ---------------------------------------------------------------- block norms
+NORM_CASES = [
+    # N, D, gate rows (0: no gate), parts
+    (1, 64, 0, "post+pre"), (1, 6144, 1 << 40, "post+pre"), (3, 320, 1, "post+pre"), (37, 512, 5, "post+pre"),
+    (700, 192, 256, "post+pre"), (1500, 64, 700, "post+pre"), (1030, 64, 3, "post+pre"),
+    (5, 8256, 2, "post+pre"), (2, 16384, 2, "post+pre"),
+    (19, 256, 4, "post"), (19, 256, 4, "plain+pre"), (33, 576, 0, "plain"), (19, 256, 0, "pre"), (1100, 128, 0, "pre"),
+]
+
+
+def norm_inputs(N, D, T, parts, dt, seed):
+    g = gen(seed)
+
+    def randn(*shape, scale=1.0, mean=0.0):
+        return (torch.randn(shape, generator=g) * scale + mean).to(dt)
+    post = parts != "pre"
+    t = {"h": randn(N, D, scale=2.0), "o": randn(N, D, scale=0.3) if post else None,
+         "w_post": randn(D, scale=0.2, mean=1.0) if parts.startswith("post") else None,
+         "gate": randn((N + T - 1) // T, D, mean=0.5) if T else None,
+         "w_pre": randn(D, scale=0.2, mean=1.0) if parts.endswith("pre") else None,
+         "dv": randn(N, D), "du": randn(N, D) if parts.endswith("pre") else None}
+    return t
+
+
+def f64(t):
+    return None if t is None else t.double()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,D,T,parts", NORM_CASES)
+def test_block_norm(N, D, T, parts, dtype):
+    dt, a, eps = TYPES[dtype], 0.75, 1e-5
+    print(f"[norm] N={N} D={D} T={T} {parts} {dtype}", flush=True)
+    t = norm_inputs(N, D, T, parts, dt, 1)
+    d = {n: dev(v) for n, v in t.items()}
+    h_out = torch.empty_like(d["h"]) if t["o"] is not None else None
+    u = torch.empty_like(d["h"]) if t["w_pre"] is not None else None
+    moe.moe_block_norm(N, d["h"], d["o"], d["w_post"], d["gate"], T, d["w_pre"], h_out, u, residual_scale=a, eps=eps)
+    torch.cuda.synchronize()
+    args = [f64(t[n]) for n in ("h", "o", "w_post", "gate")] + [T or 1, f64(t["w_pre"]), a, eps]
+    ref, bound = O.norm_forward(*args), O.norm_forward_bound(*args)
+    if h_out is not None:
+        O.check("h_out", h_out, ref[0], bound[0])
+    if u is not None:
+        O.check("u", u, ref[1], bound[1])
+    if h_out is not None:  # in place, the same bits
+        again = d["h"].clone()
+        u2 = torch.empty_like(u) if u is not None else None
+        moe.moe_block_norm(N, again, d["o"], d["w_post"], d["gate"], T, d["w_pre"], again, u2, residual_scale=a, eps=eps)
+        assert torch.equal(again, h_out) and (u is None or torch.equal(u, u2))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,D,T,parts", NORM_CASES)
+def test_block_norm_backward(N, D, T, parts, dtype):
+    dt, a, eps = TYPES[dtype], 0.75, 1e-5
+    print(f"[norm bwd] N={N} D={D} T={T} {parts} {dtype}", flush=True)
+    t = norm_inputs(N, D, T, parts, dt, 2)
+    d = {n: dev(v) for n, v in t.items()}
+    post, pre = t["o"] is not None, t["w_pre"] is not None
+    f = dict(dtype=F32, device="cuda")
+    dh = torch.empty_like(d["h"])
+    do = torch.empty_like(d["h"]) if post else None
+    dwp = torch.empty(D, **f) if t["w_post"] is not None else None
+    dg = torch.empty(t["gate"].shape, **f) if T else None
+    dw = torch.empty(D, **f) if pre else None
+    ws = workspace(moe.moe_block_norm_workspace_size(N, D, dtype, T))
+
+    def run(dv, dh):
+        moe.moe_block_norm_backward(N, d["h"] if pre else None, d["o"], d["w_post"], d["gate"], T, d["w_pre"], dv,
+                                    d["du"], dh, do, dwp, dg, dw, ws, residual_scale=a, eps=eps)
+        torch.cuda.synchronize()
+    run(d["dv"], dh)
+    got = (dh, do, dwp, dg, dw)
+    refs, bounds = O.norm_backward(f64(t["h"]), f64(t["o"]), f64(t["w_post"]), f64(t["gate"]), T or 1, f64(t["w_pre"]),
+                                   f64(t["dv"]), f64(t["du"]), a, eps)
+    for name, x, r, b in zip(("dh", "do", "dw_post", "dgate", "dw_pre"), got, refs, bounds):
+        assert (x is None) == (r is None), name
+        if x is not None:
+            O.check(name, x, r, b)
+    keep = [None if x is None else x.clone() for x in got]
+    inplace = d["dv"].clone()
+    run(inplace, inplace)  # dh over dh_out; the sums the same bits again
+    assert torch.equal(inplace, keep[0])
+    assert all(x is None or torch.equal(x, y) for x, y in zip(got[1:], keep[1:]))
+    if pre:  # no gradient of h_out
+        run(None, dh)
+        refs, bounds = O.norm_backward(f64(t["h"]), f64(t["o"]), f64(t["w_post"]), f64(t["gate"]), T or 1,
+                                       f64(t["w_pre"]), None, f64(t["du"]), a, eps)
+        O.check("dh without dh_out", dh, refs[0], bounds[0])
+
+
+def test_block_norm_gradient_against_differences():
+    """<gradient, direction> against central differences of the float64 forward formula."""
+    N, D, T, a, eps, e = 6, 128, 3, 0.9, 1e-5, 1e-4
+    t = {n: v for n, v in norm_inputs(N, D, T, "post+pre", F32, 3).items()}
+    names = ("h", "o", "w_post", "gate", "w_pre")
+    g = gen(4)
+
+    def loss(p):
+        v, u = O.norm_forward(p["h"], p["o"], p["w_post"], p["gate"], T, p["w_pre"], a, eps)
+        return float((v * t["dv"].double()).sum() + (u * t["du"].double()).sum())
+    base = {n: t[n].double() for n in names}
+    v, _ = O.norm_forward(base["h"], base["o"], base["w_post"], base["gate"], T, base["w_pre"], a, eps)
+    h_out = v.float().cuda()  # the forward's h_out, rounded to float32: 2^-24 of it beside the difference's own error
+    outs = [torch.empty_like(h_out), torch.empty_like(h_out)]
+    sums = [torch.empty(D, device="cuda"), torch.empty((2, D), device="cuda"), torch.empty(D, device="cuda")]
+    moe.moe_block_norm_backward(N, h_out, dev(t["o"]), dev(t["w_post"]), dev(t["gate"]), T, dev(t["w_pre"]),
+                                dev(t["dv"]), dev(t["du"]), *outs, *sums,
+                                workspace(moe.moe_block_norm_workspace_size(N, D, "f32", T)), residual_scale=a, eps=eps)
+    grads = dict(zip(("h", "o", "w_post", "gate", "w_pre"), [outs[0], outs[1], sums[0], sums[1], sums[2]]))
+    for n in names:
+        r = torch.randn(base[n].shape, generator=g, dtype=torch.float64)
+        num = (loss({**base, n: base[n] + e * r}) - loss({**base, n: base[n] - e * r})) / (2 * e)
+        ana = float((grads[n].cpu().double() * r).sum())
+        scale = float((grads[n].cpu().double() * r).abs().sum())
+        print(f"  {n}: {ana:.8g} against {num:.8g}", flush=True)
+        # differences: e^2 of third derivatives (order one here) and 1e-16 / e; gradient: float32 steps
+        assert abs(ana - num) <= 3e-5 * scale + 1e-6
+
+
+def test_block_norm_without_rows():
+    ws = workspace(0)
+    z = torch.empty((0, 64), dtype=BF, device="cuda")
+    w = torch.ones(64, dtype=BF, device="cuda")
+    dwp, dw = torch.full((64,), 7.0, device="cuda"), torch.full((64,), 7.0, device="cuda")
+    moe.moe_block_norm(0, z, z, w, None, 0, w, z, z)
+    moe.moe_block_norm_backward(0, z, z, w, None, 0, w, z, z, z, z, dwp, None, dw, ws)
+    assert not dwp.any() and not dw.any()
+
+
+# ---------------------------------------------------------------- combine
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,k,D,empty", [(1, 1, 64, 0.0), (1, 8, 6144, 0.0), (33, 4, 320, 0.3), (5, 32, 128, 0.5),
+                                         (257, 2, 8256, 0.1), (40, 9, 256, 1.0)])
+def test_combine_and_gradients(N, k, D, empty, dtype):
+    dt, alpha = TYPES[dtype], 2.5
+    print(f"[combine] N={N} k={k} D={D} empty={empty} {dtype}", flush=True)
+    g = gen(5)
+    _, offsets, _, inv = O.lists(g, N, k, 64, empty)
+    R = N * k
+    rows, shared, dy = (torch.randn((n, D), generator=g).to(dt) for n in (R, N, N))
+    w = torch.rand((N, k), generator=g)
+    y = torch.empty((N, D), dtype=dt, device="cuda")
+    drows = torch.full((R, D), 3.0, dtype=dt, device="cuda")
+    dw = torch.empty((N, k), device="cuda")
+    d = [dev(x) for x in (rows, inv, w, shared, dy)]
+    for ww, ss in ((w, shared), (None, None), (w, None)):
+        moe.moe_combine(N, k, d[0], d[1], dev(ww), dev(ss), y, alpha=alpha)
+        O.check("y", y, *O.combine(rows.double(), inv, f64(ww), f64(ss), alpha, N, k))
+    y.copy_(d[3])
+    moe.moe_combine(N, k, d[0], d[1], d[2], y, y, alpha=alpha)  # in place over shared
+    O.check("y in place", y, *O.combine(rows.double(), inv, f64(w), f64(shared), alpha, N, k))
+    moe.moe_combine_backward(N, k, d[4], d[0], d[1], d[2], drows, dw, alpha=alpha)
+    torch.cuda.synchronize()
+    used = int(offsets[-1])
+    ref = torch.zeros((R, D), dtype=torch.float64)
+    rw = torch.zeros((N, k), dtype=torch.float64)
+    mag = rw.clone()
+    for n in range(N):
+        for s in range(k):
+            r = int(inv[n * k + s])
+            if r >= 0:
+                ref[r] = alpha * w[n, s].double() * dy[n].double()
+                prod = dy[n].double() * rows[r].double()
+                rw[n, s], mag[n, s] = alpha * prod.sum(), alpha * prod.abs().sum()
+    O.check("drows", drows[:used], ref[:used], 3 * O.U32 * ref[:used].abs())
+    O.check("dw", dw, rw, (D + 3) * O.U32 * mag)
+    assert (drows[used:] == 3.0).all()  # rows that no slot names
+    again = torch.zeros_like(drows)
+    moe.moe_combine_backward(N, k, d[4], None, d[1], None, again, None, alpha=alpha)
+    ref = (alpha * dy.double())[_token_of(inv, k, used)]
+    O.check("drows unweighted", again[:used], ref, 3 * O.U32 * ref.abs())
+
+
+def _token_of(inv, k, used):
+    tok = torch.zeros(used, dtype=torch.long)
+    for i, r in enumerate(inv.tolist()):
+        if r >= 0:
+            tok[r] = i // k
+    return tok
+
+
+# ---------------------------------------------------------------- grouped products
+GROUPED = [  # N, k, E, K, M, share of empty slots
+    (1, 1, 1, 64, 64, 0.0), (1, 4, 16, 256, 192, 0.0), (3, 2, 512, 64, 128, 0.0), (65, 2, 4, 320, 576, 0.2),
+    (300, 2, 3, 128, 320, 0.1), (700, 1, 2, 192, 64, 0.0), (40, 8, 16, 448, 832, 0.3), (9, 1, 5, 128, 64, 1.0),
+    (2000, 1, 2, 64, 256, 0.0), (130, 4, 60, 512, 256, 0.0),
+]
+
+
+def grouped_setup(N, k, E, K, M, empty, dt, gather, seed=6):
+    """Integer-valued operands: every sum is exact in float32 (|sum| <= 9 * 2000 and a K or M of at most 832),
+    so an output is the exact value rounded once."""
+    g = gen(seed)
+    _, offsets, pair, _ = O.lists(g, N, k, E, empty)
+    R = N * k
+    x = O.ints(g, (N if gather else R, K), -3, 3, dt)
+    w = O.ints(g, (E, M, K), -3, 3, dt)
+    dy = O.ints(g, (R, M), -3, 3, dt)
+    src = (pair // k).long() if gather else torch.arange(R)
+    return offsets, pair, src, x, w, dy
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("N,k,E,K,M,empty", GROUPED)
+def test_grouped_linear_and_gradients(N, k, E, K, M, empty, gather, dtype):
+    dt, R = TYPES[dtype], N * k
+    print(f"[grouped] N={N} k={k} E={E} K={K} M={M} empty={empty} gather={gather} {dtype}", flush=True)
+    offsets, pair, src, x, w, dy = grouped_setup(N, k, E, K, M, empty, dt, gather)
+    used = int(offsets[-1])
+    ws = workspace(moe.moe_grouped_workspace_size(E, R, dtype))
+    o, xd, wd, dyd = dev(offsets), dev(x), dev(w), dev(dy)
+    index = dict(row_index=dev(pair), index_div=k) if gather else {}
+    y = torch.full((R, M), 7.0, dtype=dt, device="cuda")
+    moe.moe_grouped_linear(xd, wd, o, y, ws, **index)
+    torch.cuda.synchronize()
+    print("  fwd done", flush=True)
+    assert torch.equal(y[:used].cpu(), O.grouped(x.double(), w.double(), offsets, src, R)[:used].to(dt))
+    assert (y[used:] == 7.0).all()  # rows behind the last expert's
+    dx = torch.full((R, K), 7.0, dtype=dt, device="cuda")
+    moe.moe_grouped_linear_dgrad(dyd, wd, o, dx, ws)
+    torch.cuda.synchronize()
+    print("  dgrad done", flush=True)
+    assert torch.equal(dx[:used].cpu(), O.grouped_dgrad(dy.double(), w.double(), offsets)[:used].to(dt))
+    assert (dx[used:] == 7.0).all()
+    dw = torch.full((E, M, K), 7.0, dtype=dt, device="cuda")
+    moe.moe_grouped_linear_wgrad(dyd, xd, o, dw, ws, **index)
+    torch.cuda.synchronize()
+    print("  wgrad done", flush=True)
+    assert torch.equal(dw.cpu(), O.grouped_wgrad(dy.double(), x.double(), offsets, src, E).to(dt))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_grouped_float_values(dtype):
+    """Ordinary values: within the bound of a float32 sum and one rounding."""
+    dt, N, k, E, K, M = TYPES[dtype], 150, 2, 3, 576, 320
+    g = gen(8)
+    _, offsets, pair, _ = O.lists(g, N, k, E)
+    R, src = N * k, (pair // k).long()
+    x, dy = torch.randn((N, K), generator=g).to(dt), torch.randn((R, M), generator=g).to(dt)
+    w = (torch.randn((E, M, K), generator=g) * K ** -0.5).to(dt)
+    ws = workspace(moe.moe_grouped_workspace_size(E, R, dtype))
+    y, dx, dw = (torch.empty(s, dtype=dt, device="cuda") for s in ((R, M), (R, K), (E, M, K)))
+    o, p = dev(offsets), dev(pair)
+    moe.moe_grouped_linear(dev(x), dev(w), o, y, ws, row_index=p, index_div=k)
+    moe.moe_grouped_linear_dgrad(dev(dy), dev(w), o, dx, ws)
+    moe.moe_grouped_linear_wgrad(dev(dy), dev(x), o, dw, ws, row_index=p, index_div=k)
+    x, w, dy = x.double(), w.double(), dy.double()
+    O.check("y", y, O.grouped(x, w, offsets, src, R), (K + 1) * O.U32 * O.grouped(x.abs(), w.abs(), offsets, src, R))
+    O.check("dx", dx, O.grouped_dgrad(dy, w, offsets), (M + 1) * O.U32 * O.grouped_dgrad(dy.abs(), w.abs(), offsets))
+    O.check("dw", dw, O.grouped_wgrad(dy, x, offsets, src, E),
+            (R + 1) * O.U32 * O.grouped_wgrad(dy.abs(), x.abs(), offsets, src, E))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_grouped_ranges_inside_the_rows(dtype):
+    """Offsets that start behind row 0 and end before R; a NaN row next to an expert's rows stays out of its
+    sums and outputs; out-of-range indices are clamped."""
+    dt, E, R, K, M = TYPES[dtype], 3, 300, 128, 192
+    g = gen(9)
+    offsets = torch.tensor([5, 5, 138, 291], dtype=torch.int32)
+    x, w, dy = O.ints(g, (R, K), -3, 3, dt), O.ints(g, (E, M, K), -3, 3, dt), O.ints(g, (R, M), -3, 3, dt)
+    for t in (x, dy):
+        t[:5] = float("nan")
+        t[291:] = float("nan")
+    ws = workspace(moe.moe_grouped_workspace_size(E, R, dtype))
+    y, dx, dw = (torch.full(s, 7.0, dtype=dt, device="cuda") for s in ((R, M), (R, K), (E, M, K)))
+    o, src = dev(offsets), torch.arange(R)
+    moe.moe_grouped_linear(dev(x), dev(w), o, y, ws)
+    moe.moe_grouped_linear_dgrad(dev(dy), dev(w), o, dx, ws)
+    moe.moe_grouped_linear_wgrad(dev(dy), dev(x), o, dw, ws)
+    xd, wd, dyd = x.double(), w.double(), dy.double()
+    for got, ref in ((y, O.grouped(xd, wd, offsets, src, R)), (dx, O.grouped_dgrad(dyd, wd, offsets))):
+        assert torch.equal(got[5:291].cpu(), ref[5:291].to(dt))
+        assert (got[:5] == 7.0).all() and (got[291:] == 7.0).all()
+    assert torch.equal(dw.cpu(), O.grouped_wgrad(dyd, xd, offsets, src, E).to(dt))
+    index = torch.arange(R, dtype=torch.int32)
+    index[10], index[20] = -9, 1 << 30
+    clean = x.clone()
+    clean[:5], clean[291:] = 1.0, 2.0
+    moe.moe_grouped_linear(dev(clean), dev(w), o, y, ws, row_index=dev(index))
+    ref = O.grouped(clean.double(), wd, offsets, index.long().clamp(0, R - 1), R)
+    assert torch.equal(y[5:291].cpu(), ref[5:291].to(dt))
+
+
+# ---------------------------------------------------------------- 4-bit weights
+def swiglu64(y, limit):
+    g, u = y.chunk(2, -1)
+    if limit:
+        g, u = g.clamp(max=limit), u.clamp(-limit, limit)
+    return g * torch.sigmoid(g) * u
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("N,k,E,K,M", [(1, 1, 1, 128, 64), (1, 1, 1, 5120, 128), (17, 1, 1, 384, 192), (70, 1, 1, 640, 320),
+                                       (3, 2, 512, 256, 64), (33, 4, 16, 896, 256), (500, 1, 3, 256, 128),
+                                       (16, 1, 1, 6144, 64), (5, 1, 1, 12288, 64)])
+def test_qlinear_exact(N, k, E, K, M, group):
+    """Integer activations and power-of-two scales: float32 holds every sum exactly, so the output is the exact
+    value rounded once."""
+    print(f"[qlinear] N={N} k={k} E={E} K={K} M={M} group={group}", flush=True)
+    g = gen(10)
+    _, offsets, pair, _ = O.lists(g, N, k, E, 0.2 if k > 1 else 0.0)
+    R, used = N * k, int(offsets[-1])
+    x = O.ints(g, (N, K), -3, 3)
+    q = torch.randint(0, 256, (E, M, K // 2), generator=g, dtype=torch.uint8)
+    s = (2.0 ** torch.randint(-2, 2, (E, M, K // group), generator=g)).to(BF)
+    y = torch.full((R, M), 7.0, dtype=BF, device="cuda")
+    kw = dict(offsets=dev(offsets), row_index=dev(pair), index_div=k) if E > 1 or k > 1 else {}
+    moe.moe_qlinear(dev(x), dev(q), dev(s), y, **kw)
+    torch.cuda.synchronize()
+    src = (pair // k).long() if kw else torch.arange(R)
+    ref = O.grouped(x.double(), O.dequantize(q, s), offsets, src, R)
+    assert torch.equal(y[:used].cpu(), ref[:used].to(BF))
+    assert (y[used:] == 7.0).all()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("swiglu,limit", [(False, 0.0), (True, 0.0), (True, 1.5)])
+@pytest.mark.parametrize("N,E", [(1, 1), (9, 1), (130, 1), (40, 8)])
+def test_qlinear_float_values(N, E, swiglu, limit, group):
+    """Ordinary values. Bound of the product: every float32 step of the offset form (products of 128 + q and
+    -136, at most 280 |x| s a value; group sums of 2 group terms, then K / group scaled sums)."""
+    K, M, k = 768, 256, 1
+    g = gen(11)
+    _, offsets, pair, _ = O.lists(g, N, k, E)
+    x = torch.randn((N, K), generator=g).to(BF)
+    w = torch.randn((E, M, K), generator=g) * K ** -0.5
+    q, s = moe.moe_quantize(dev(w), group)
+    y = torch.empty((N, M // 2 if swiglu else M), dtype=BF, device="cuda")
+    kw = dict(offsets=dev(offsets), row_index=dev(pair)) if E > 1 else {}
+    moe.moe_qlinear(dev(x), q, s, y, swiglu=swiglu, limit=limit, **kw)
+    wd, src = O.dequantize(q.cpu(), s.cpu()), pair.long()
+    scale = s.cpu().double().repeat_interleave(group, 2)
+    ref = O.grouped(x.double(), wd, offsets, src, N)
+    bound = (2 * group + K / group + 4) * O.U32 * 280 * O.grouped(x.double().abs(), scale, offsets, src, N)
+    if swiglu:
+        # |d silu| <= 1.1, |silu(g)| <= |g|: first order in the two products' errors, and the activation's own
+        # float32 steps (a hardware exponential and reciprocal: 8 steps)
+        gt, up = ref.chunk(2, -1)
+        eg, eu = bound.chunk(2, -1)
+        ref = swiglu64(ref, limit)
+        bound = 1.1 * eg * (up.abs() + eu) + gt.abs() * eu + 8 * O.U32 * gt.abs() * up.abs()
+    O.check("y", y, ref, bound)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_quantize_bits(group, dtype):
+    """Scales and values bit for bit from float32 arithmetic, among them zero groups, ties, huge and tiny values."""
+    g = gen(12)
+    w = torch.randn((3, 40, 256), generator=g)
+    w[0, 0] = 0.0
+    w[0, 1, :8] = torch.tensor([7.0, 0.5, 1.5, -2.5, 3.5, -7.0, 6.5, 0.0])
+    w[0, 1, 8:] = 0.0
+    w[0, 2] *= 1e30
+    w[0, 3] *= 1e-42
+    w = w.to(TYPES[dtype])
+    q, s = moe.moe_quantize(dev(w), group)
+    grouped = w.float().view(3, 40, -1, group)
+    rs = (grouped.abs().amax(3) / 7.0).to(BF)
+    d = torch.where(rs > 0, rs.float(), torch.ones_like(rs.float()))[..., None]
+    rq = torch.where(rs[..., None] > 0, torch.round(grouped / d).clamp(-8, 7) + 8, torch.full_like(grouped, 8.0))
+    rq = rq.to(torch.uint8).view(3, 40, -1, 2)
+    assert torch.equal(s.cpu(), rs)
+    assert torch.equal(q.cpu(), rq[..., 0] | (rq[..., 1] << 4))
+
+
+# ---------------------------------------------------------------- together
+def layer(dtype):
+    w = synth.WORKLOADS["tiny_fp32"]
+    if dtype == "bf16":
+        from dataclasses import replace
+        w = replace(w, name="ops_bf16", N=200, D=512, dtype="bf16")
+    return w, moe.config_of(w), H.device_weights(w, generate_on_device=False)[2], H.to_device(synth.x_host(w))
+
+
+def route_and_dispatch(cfg, w, d, x):
+    N, k, i32 = w.N, w.k, dict(dtype=torch.int32, device="cuda")
+    idx, wt = torch.empty((N, k), **i32), torch.empty((N, k), device="cuda")
+    moe.moe_route(cfg, N, x, d["w_router"], d["e_bias"], None, idx, wt, workspace=moe.alloc_workspace(cfg, N))
+    counts, offsets = torch.empty(w.E, **i32), torch.empty(w.E + 1, **i32)
+    pair, inv = torch.zeros(N * k, **i32), torch.empty(N * k, **i32)
+    moe.moe_dispatch(cfg, N, idx, counts, offsets, pair, inv, workspace(moe.moe_dispatch_workspace_size(cfg, N)))
+    return idx, wt, offsets, pair, inv
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layer_from_the_operators(dtype):
+    """norm -> route -> dispatch -> grouped gate_up -> SwiGLU -> grouped down -> combine with the shared expert
+    -> norm, against moe_forward on the same inputs (the layer's parity tolerance) and the closing norm's formula."""
+    w, cfg, d, x = layer(dtype)
+    N, k, R, dt = w.N, w.k, w.N * w.k, x.dtype
+    ones = torch.ones(w.D, dtype=dt, device="cuda")
+    h = torch.empty_like(x)
+    moe.moe_block_norm(N, x, None, None, None, 0, ones, None, h)
+    idx, wt, offsets, pair, inv = route_and_dispatch(cfg, w, d, h)
+    ws = workspace(moe.moe_grouped_workspace_size(w.E, R, dtype))
+    gu = torch.empty((R, 2 * w.d), dtype=dt, device="cuda")
+    moe.moe_grouped_linear(h, d["gate_up"], offsets, gu, ws, row_index=pair, index_div=k)
+    act = (torch.nn.functional.silu(gu[:, :w.d].float()) * gu[:, w.d:].float()).to(dt)
+    rows = torch.empty((R, w.D), dtype=dt, device="cuda")
+    moe.moe_grouped_linear(act, d["down"], offsets, rows, ws)
+    sh = torch.empty_like(x)
+    moe.moe_dense_forward(N, h, d["sh_gate"], d["sh_up"], d["sh_down"], sh,
+                          workspace(moe.moe_dense_workspace_size(N, w.D, w.d * w.n_shared, dtype)))
+    y = torch.empty_like(x)
+    moe.moe_combine(N, k, rows, inv, wt, sh, y)
+    ref = torch.empty_like(x)
+    moe.moe_forward(cfg, N, h, d, ref, moe.alloc_workspace(cfg, N))
+    err = H.rel_err(y.float().cpu().numpy(), ref.float().cpu().numpy())
+    print(f"  operators against the layer: {err:.3g}", flush=True)
+    assert err <= H.TOL[dtype]
+    out = torch.empty_like(x)
+    moe.moe_block_norm(N, x, y, ones, None, 0, None, out, None, residual_scale=0.5)
+    args = [x.cpu().double(), y.cpu().double(), ones.cpu().double(), None, 1, None, 0.5, 1e-5]
+    O.check("closing norm", out, O.norm_forward(*args)[0], O.norm_forward_bound(*args)[0])
+
+
+def test_training_chain_gradients():
+    """Gradients through grouped gate_up, SwiGLU, grouped down and combine against float64 autograd of the same
+    graph, float32 layer: max error over max magnitude within the layer's 1e-4."""
+    w, cfg, d, x = layer("f32")
+    N, k, R = w.N, w.k, w.N * w.k
+    idx, wt, offsets, pair, inv = route_and_dispatch(cfg, w, d, x)
+    ws = workspace(moe.moe_grouped_workspace_size(w.E, R, "f32"))
+    f = dict(dtype=F32, device="cuda")
+    gu, rows, y = torch.empty((R, 2 * w.d), **f), torch.empty((R, w.D), **f), torch.empty((N, w.D), **f)
+    moe.moe_grouped_linear(x, d["gate_up"], offsets, gu, ws, row_index=pair, index_div=k)
+    gu.requires_grad_()
+    act = torch.nn.functional.silu(gu[:, :w.d]) * gu[:, w.d:]
+    moe.moe_grouped_linear(act.detach(), d["down"], offsets, rows, ws)
+    moe.moe_combine(N, k, rows, inv, wt, None, y)
+    dy = torch.randn((N, w.D), generator=gen(13)).cuda()
+    drows, dwt = torch.empty_like(rows), torch.empty_like(wt)
+    moe.moe_combine_backward(N, k, dy, rows, inv, wt, drows, dwt)
+    dact, ddown = torch.empty((R, w.d), **f), torch.empty_like(d["down"])
+    moe.moe_grouped_linear_dgrad(drows, d["down"], offsets, dact, ws)
+    moe.moe_grouped_linear_wgrad(drows, act.detach(), offsets, ddown, ws)
+    act.backward(dact)
+    dgu, dxr, dx = torch.empty_like(d["gate_up"]), torch.empty((R, w.D), **f), torch.empty((N, w.D), **f)
+    moe.moe_grouped_linear_wgrad(gu.grad, x, offsets, dgu, ws, row_index=pair, index_div=k)
+    moe.moe_grouped_linear_dgrad(gu.grad, d["gate_up"], offsets, dxr, ws)
+    moe.moe_combine(N, k, dxr, inv, None, None, dx)
+
+    leaf = {n: t.detach().cpu().double().requires_grad_() for n, t in
+            (("x", x), ("gu", d["gate_up"]), ("down", d["down"]), ("w", wt))}
+    ids = idx.cpu().long()
+    out = torch.zeros((N, w.D), dtype=torch.float64)
+    for s in range(k):
+        e = ids[:, s]
+        z = torch.einsum("nmk,nk->nm", leaf["gu"][e], leaf["x"])
+        a = torch.nn.functional.silu(z[:, :w.d]) * z[:, w.d:]
+        out = out + leaf["w"][:, s:s + 1] * torch.einsum("nmk,nk->nm", leaf["down"][e], a)
+    out.backward(dy.cpu().double())
+    for name, got, ref in (("y", y, out.detach()), ("dx", dx, leaf["x"].grad), ("dW gate_up", dgu, leaf["gu"].grad),
+                           ("dW down", ddown, leaf["down"].grad), ("dw", dwt, leaf["w"].grad)):
+        err = H.rel_err(got.detach().cpu().numpy(), ref.numpy())
+        print(f"  {name}: {err:.3g}", flush=True)
+        assert err <= 1e-4, name
+
+
+def test_quantized_experts_chain():
+    """quantize -> 4-bit gate_up with SwiGLU -> 4-bit down -> combine, against float64 on the dequantised
+    weights: the layer's bf16 tolerance (the intermediate is bf16)."""
+    w, cfg, d, x = layer("bf16")
+    N, k, R = w.N, w.k, w.N * w.k
+    idx, wt, offsets, pair, inv = route_and_dispatch(cfg, w, d, x)
+    q1, s1 = moe.moe_quantize(d["gate_up"], 64)
+    q2, s2 = moe.moe_quantize(d["down"], 32)
+    act = torch.empty((R, w.d), dtype=BF, device="cuda")
+    rows, y = torch.empty((R, w.D), dtype=BF, device="cuda"), torch.empty_like(x)
+    moe.moe_qlinear(x, q1, s1, act, offsets=offsets, row_index=pair, index_div=k, swiglu=True)
+    moe.moe_qlinear(act, q2, s2, rows, offsets=offsets)
+    moe.moe_combine(N, k, rows, inv, wt, None, y)
+    w1, w2 = O.dequantize(q1.cpu(), s1.cpu()), O.dequantize(q2.cpu(), s2.cpu())
+    xs, ids = x.cpu().double(), idx.cpu().long()
+    ref = torch.zeros((N, w.D), dtype=torch.float64)
+    for n in range(N):
+        for s in range(k):
+            e = int(ids[n, s])
+            ref[n] += float(wt[n, s]) * (w2[e] @ swiglu64(w1[e] @ xs[n], 0.0))
+    err = H.rel_err(y.float().cpu().numpy(), ref.numpy())
+    print(f"  rel_err={err:.3g}", flush=True)
+    assert err <= H.TOL["bf16"]
+
+
+def test_streams_and_graph_replays():
+    """A side stream, then one captured graph of a chain of the operators, replayed with changing inputs and
+    eager work between: every replay equals the eager calls."""
+    N, k, E, K, M = 48, 2, 8, 256, 192
+    R = N * k
+    g = gen(14)
+    _, offsets, pair, inv = O.lists(g, N, k, E)
+    x = torch.randn((N, K), generator=g).to(BF).cuda()
+    w = (torch.randn((E, M, K), generator=g) / 16).to(BF).cuda()
+    q, s = moe.moe_quantize(w, 64)
+    o, p, iv, ones = dev(offsets), dev(pair), dev(inv), torch.ones(K, dtype=BF, device="cuda")
+    bf = dict(dtype=BF, device="cuda")
+    buf = dict(h=torch.empty((N, K), **bf), y=torch.empty((R, M), **bf), yq=torch.empty((R, M), **bf),
+               dx=torch.empty((R, K), **bf), dw=torch.empty((E, M, K), **bf), t=torch.empty((N, K), **bf),
+               dh=torch.empty((N, K), **bf), dwn=torch.empty(K, device="cuda"))
+    ws = workspace(moe.moe_grouped_workspace_size(E, R))
+    wsn = workspace(moe.moe_block_norm_workspace_size(N, K))
+
+    def chain(b):
+        moe.moe_block_norm(N, x, None, None, None, 0, ones, None, b["h"])
+        moe.moe_grouped_linear(b["h"], w, o, b["y"], ws, row_index=p, index_div=k)
+        moe.moe_qlinear(b["h"], q, s, b["yq"], offsets=o, row_index=p, index_div=k)
+        moe.moe_grouped_linear_dgrad(b["y"], w, o, b["dx"], ws)
+        moe.moe_grouped_linear_wgrad(b["y"], b["h"], o, b["dw"], ws, row_index=p, index_div=k)
+        moe.moe_combine(N, k, b["dx"], iv, None, None, b["t"])
+        moe.moe_block_norm_backward(N, x, None, None, None, 0, ones, None, b["t"], b["dh"], None, None, None, b["dwn"], wsn)
+
+    def eager():
+        b = {n: torch.full_like(t, 5.0) for n, t in buf.items()}
+        chain(b)
+        torch.cuda.synchronize()
+        return b
+    ref = eager()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        chain(buf)
+    side.synchronize()
+    assert all(torch.equal(buf[n], ref[n]) for n in buf)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(buf)
+    for i in range(4):
+        x.copy_(torch.randn((N, K), generator=g).to(BF))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: t.clone() for n, t in buf.items()}
+        ref = eager()
+        for n in buf:
+            assert torch.equal(got[n], ref[n]), (i, n)
