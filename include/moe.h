@@ -301,7 +301,7 @@ moe_status moe_combine_backward(int64_t N, int32_t k, int32_t D, int32_t dtype, 
  * topk_w == NULL. Offsets and indices are read on the device and kept in range there: offsets outside [0, R]
  * or out of order and indices outside [0, x_rows * index_div) give unspecified values, never an access
  * outside the buffers. Float32 sums over the whole reduction, one rounding. E: 1..512; in and out:
- * multiples of 64, in * out below 2^31; bf16: gathered x below 4 GiB. R = 0 launches nothing (wgrad: writes
+ * multiples of 64 up to 2^22, in * out below 2^31; bf16: gathered x below 4 GiB. R = 0 launches nothing (wgrad: writes
  * zeros). No overlap between an output and an input. */
 size_t moe_grouped_workspace_size(int32_t E, int64_t R, int32_t dtype);
 moe_status moe_grouped_linear(int32_t E, int64_t R, int32_t in, int32_t out, int32_t dtype, const void* x,

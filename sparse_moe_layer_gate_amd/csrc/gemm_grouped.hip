@@ -9,6 +9,9 @@
 // (launch_offset_lists); wgrad needs none, its tiles are those of dW.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -24,26 +27,14 @@ __device__ inline void load8f(const float* p, float* f) {
     f[4 + i] = b[i];
   }
 }
-__device__ inline void load8f(const uint16_t* p, float* f) {
-  const uint4 v = *(const uint4*)p;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ inline void store1(float* p, float v) { *p = v; }
-__device__ inline void store1(uint16_t* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
-
 // 128 x 128 tile of C[i, j] = sum_t A(i, t) B(j, t) in float32: both operands go through LDS as
 // [t][i] / [t][j] (16 t per step), four waves of 64 x 64 as 4 x 4 tiles of v_mfma_f32_16x16x4_f32
 // (A: row lane % 16, k lane / 16; C: column lane % 16, rows 4 (lane / 16) + r).
 //   fwd:   i = row, j = output feature, t = input feature;   both operands contiguous in t
 //   dgrad: i = row, j = input feature,  t = output feature;  B contiguous in j
 //   wgrad: i = output feature, j = input feature, t = row;   both contiguous in i / j
-template <typename T, int MODE>
-__global__ __launch_bounds__(256) void grouped_any(GradArgs a, int col_tiles) {
+template <int MODE>
+__global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tiles) {
   constexpr bool A_T = MODE == GM_WGRAD;              // A contiguous in i
   constexpr bool B_T = MODE != GM_FWD;                // B contiguous in j
   constexpr int BT = 16, PITCH = 128 + 4;
@@ -73,8 +64,8 @@ __global__ __launch_bounds__(256) void grouped_any(GradArgs a, int col_tiles) {
   }
   const int ni = MODE == GM_WGRAD ? M : rows, nj = MODE == GM_FWD ? M : K;
   const int nt = MODE == GM_FWD ? K : MODE == GM_DGRAD ? M : rows;
-  const T* A = (const T*)a.a;
-  const T* B = (const T*)a.b;
+  const float* A = (const float*)a.a;
+  const float* B = (const float*)a.b;
   const int64_t wbase = (int64_t)expert * M * K;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -136,7 +127,7 @@ __global__ __launch_bounds__(256) void grouped_any(GradArgs a, int col_tiles) {
         for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[j], acc[i][j], 0, 0, 0);
     }
   }
-  T* out = (T*)a.out;
+  float* out = (float*)a.out;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -147,13 +138,462 @@ __global__ __launch_bounds__(256) void grouped_any(GradArgs a, int col_tiles) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int jj = j0 + wj + 16 * j + (lane & 15);
-        if (jj < nj) store1(out + base + jj, acc[i][j][q]);
+        if (jj < nj) out[base + jj] = acc[i][j][q];
       }
     }
 }
 
-template <typename T>
-hipError_t launch_any(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s) {
+// ---- bfloat16 gradients ----
+//
+// Both gradients reduce over an index that is not contiguous in one operand (dgrad: W over its rows) or in
+// both (wgrad: dy and x over their rows). Such an operand goes to LDS as it lies in memory, whole rows of
+// the reduction index, and is turned on the way to the matrix cores: ds_read_b64_tr_b16 gives lane i of 16
+// the four elements of column i from four rows of 16 columns, so two of them make the eight consecutive
+// reduction elements that a lane of v_mfma_f32_32x32x16_bf16 holds of its column.
+//  - a row's 32-byte pieces are XOR-swizzled by twice the row's position modulo 4: the four rows x two
+//    neighbouring pieces that half a wave reads at a time then lie in distinct banks;
+//  - operands go global -> LDS directly (1 KiB of LDS per wave and load), no register staging;
+//  - each wave holds 64 x 128 of C as 2 x 4 tiles; the fragments of the next 16-wide slice are read while
+//    the present one's products run.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr int kRawBufferWord3 = 0x00020000;  // raw buffer, 32-bit data format
+
+__device__ inline void wait_lgkm0() { __builtin_amdgcn_s_waitcnt((15) | (3 << 14) | (7 << 4) | (0 << 8)); }
+template <int N>
+__device__ inline void wait_lgkm() {
+  static_assert(N >= 0 && N <= 15, "lgkmcnt is 4 bits");
+  __builtin_amdgcn_s_waitcnt((15) | (3 << 14) | (7 << 4) | (N << 8));
+}
+__device__ inline void bare_barrier() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+// dgrad: 256 x 256 tile, eight waves, 64 reduction elements per step (whole lines of dy), dy in a two-stage
+// ring and W in a three-stage one: all 160 KiB of LDS, one block per CU.
+// wgrad: 256 x 128 tile, four waves, 32 rows per step, three stages: 72 KiB, two blocks per CU, so that one
+// block's products cover the other's first loads and its stores (an expert's few hundred rows make a
+// short loop, and every tile ends in 64 KiB of dW).
+template <int MODE>
+struct GradTile {
+  static constexpr bool A_T = MODE == GM_WGRAD;
+  static constexpr int NW = A_T ? 4 : 8;        // waves
+  static constexpr int BM = 256, BN = A_T ? 128 : 256, BK = A_T ? 32 : 64;
+  static constexpr int SA = A_T ? 3 : 2, SB = 3;  // stages
+  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
+  static constexpr int NLA = A_BYTES / 1024 / NW, NLB = B_BYTES / 1024 / NW;  // loads per wave and step
+  static constexpr int B_BASE = SA * A_BYTES;
+  static constexpr int RING = SA * A_BYTES + SB * B_BYTES;
+  static constexpr int SLICES = BK / 16;
+  static constexpr int OPITCH = 128 + 8;  // staged output row of a wave
+  static_assert(NW * 64 * OPITCH * 2 <= RING - 16, "the staged outputs fit the ring");
+  static constexpr int A_RB = BM * 2, B_RB = BN * 2;  // bytes per reduction row of a turned operand
+};
+
+// Byte offset, within a stage of turned rows of RB bytes, of the fragment of 32 columns from col0: slice s adds
+// 16 rows, the second half of a lane's eight elements 4 rows.
+template <int RB>
+__device__ inline int turned_offset(int col0, int lane) {
+  const int h = lane >> 5, piece = col0 / 16 + ((lane >> 4) & 1), i = lane & 15;
+  return (h * 8 + (i >> 2)) * RB + ((piece ^ (2 * (i >> 2))) * 32) + (i & 3) * 8;
+}
+// The restrict pointer says what the ring's waits ensure: the direct loads in flight write other stages. Without
+// it the compiler puts a vmcnt(0) before each of these reads (it treats the builtin, unlike an ordinary LDS
+// load, as a possible reader of whatever is still being loaded).
+__device__ inline s16x4 read_tr16(const lds_s16x4* __restrict__ p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+}
+template <int RB>
+__device__ inline bf16x8 read_turned(const char* p) {
+  const s16x4 lo = read_tr16((const lds_s16x4*)p);
+  const s16x4 hi = read_tr16((const lds_s16x4*)(p + 4 * RB));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+// Row (of the reduction) and first column of this lane's 16 bytes in load i of a turned operand.
+template <int RB, int NW>
+__device__ inline int turned_row(int i, int wave, int lane) {
+  return (i * NW + wave) * (1024 / RB) + lane / (RB / 16);
+}
+template <int RB>
+__device__ inline int turned_col(int t, int lane) {
+  const int pos = lane % (RB / 16);
+  return (((pos >> 1) ^ (2 * (t & 3))) * 2 + (pos & 1)) * 8;
+}
+
+__device__ inline int line_swz(int r) {
+  r &= 31;
+  return (r ^ (r >> 3)) & 7;
+}
+
+template <bool V>
+struct BoolC {
+  static constexpr bool value = V;
+};
+
+// The reduction loop of one wave. issue_a(step) / issue_b(step) start this wave's loads of a step into its
+// stage; the newest NLB (dgrad) or NLA + NLB (wgrad) loads are those of later steps than the next.
+// (EXTRA: other vector loads that issue_b makes behind its direct ones.)
+template <int MODE, int MI, int EXTRA, class IA, class IB>
+__device__ __attribute__((always_inline)) inline void grad_loop(char* lds, IA&& issue_a, IB&& issue_b,
+                                                                f32x16 (&acc)[2][4], int nk, int lane, int m0,
+                                                                int n0) {
+  using T = GradTile<MODE>;
+  constexpr int AHEAD = (T::SA > 2 ? T::NLA : 0) + (T::SB > 2 ? T::NLB + EXTRA : 0);
+  int a_off[MI > 0 ? MI : 1], b_off[4];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+    a_off[i] = T::A_T ? turned_offset<T::A_RB>(m0 + 32 * i, lane) : (m0 + 32 * i + (lane & 31)) * (T::BK * 2);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b_off[j] = turned_offset<T::B_RB>(n0 + 32 * j, lane);
+  const int sw = line_swz(lane);
+  bf16x8 af[2][MI > 0 ? MI : 1], bf[2][4];
+  constexpr int NR = MI > 0 ? MI * (T::A_T ? 2 : 1) + 8 : 0;  // LDS reads per slice
+  auto read_slice = [&](int step, int sl, int buf) {
+    if (MI == 0) return;
+    const char* sa = lds + (step % T::SA) * T::A_BYTES;
+    const char* sb = lds + T::B_BASE + (step % T::SB) * T::B_BYTES;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) bf[buf][j] = read_turned<T::B_RB>(sb + b_off[j] + sl * 16 * T::B_RB);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      if (T::A_T)
+        af[buf][i] = read_turned<T::A_RB>(sa + a_off[i] + sl * 16 * T::A_RB);
+      else
+        af[buf][i] = *(const bf16x8*)(sa + a_off[i] + ((2 * sl + (lane >> 5)) ^ sw) * 16);
+    }
+  };
+  auto compute = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[buf][i], bf[buf][j], acc[i][j], 0, 0, 0);
+  };
+  auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+
+  // prologue: the steps before the first compute, oldest first
+  issue_a(0);
+  issue_b(0);
+  if (nk > 1) {
+    if (T::SA > 2) issue_a(1);
+    if (T::SB > 2) issue_b(1);
+    wait_vmcnt<AHEAD>();
+  } else {
+    wait_vmcnt<0>();
+  }
+  bare_barrier();
+  read_slice(0, 0, 0);
+  fence();
+  auto step = [&](int kt, auto more_a, auto more_b, auto last) {
+    constexpr bool MA = decltype(more_a)::value, MB = decltype(more_b)::value, LAST = decltype(last)::value;
+    if (MA) issue_a(kt + T::SA - 1);  // into the stage that step kt - 1 used
+#pragma unroll
+    for (int sl = 0; sl < T::SLICES; ++sl) {
+      if (sl + 1 < T::SLICES) {
+        read_slice(kt, sl + 1, (sl + 1) & 1);
+        fence();
+        wait_lgkm<NR>();
+        if (sl == 0 && MB) issue_b(kt + T::SB - 1);
+        compute(sl & 1);
+        fence();
+      } else {
+        wait_lgkm0();  // every read of this step has landed
+        if (MA && MB)
+          wait_vmcnt<AHEAD>();
+        else if (!LAST)
+          wait_vmcnt<0>();
+        bare_barrier();
+        if (!LAST) read_slice(kt + 1, 0, 0);
+        fence();
+        compute(sl & 1);  // while the next step's first reads land
+        fence();
+      }
+    }
+  };
+  static_assert(T::SLICES % 2 == 0, "the last slice is in buffer 1, the next step's first in buffer 0");
+  int kt = 0;
+  for (; kt + T::SB - 1 < nk; ++kt) step(kt, BoolC<true>{}, BoolC<true>{}, BoolC<false>{});
+  if (kt + 1 < nk) {
+    // the step before the last: with two stages of A its loads are still to come
+    if (T::SA == 2)
+      step(kt++, BoolC<true>{}, BoolC<false>{}, BoolC<false>{});
+    else
+      step(kt++, BoolC<false>{}, BoolC<false>{}, BoolC<false>{});
+  }
+  step(kt, BoolC<false>{}, BoolC<false>{}, BoolC<true>{});
+}
+
+// Results of one wave through its part of the (idle) ring: whole 16-byte pieces of `rows` rows of up to 128
+// columns, `ld` elements apart.
+template <int MODE>
+__device__ __attribute__((always_inline)) inline void store_wave(char* lds, const f32x16 (&acc)[2][4], int wave,
+                                                                 int lane, int rows, int cols, uint16_t* out,
+                                                                 int64_t ld) {
+  using T = GradTile<MODE>;
+  uint16_t* st = (uint16_t*)lds + wave * (64 * T::OPITCH);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (32 * i >= rows) continue;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int row = i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        st[row * T::OPITCH + j * 32 + (lane & 31)] = __builtin_bit_cast(uint16_t, (__bf16)acc[i][j][r]);
+    }
+  }
+  // the region is this wave's own: its writes need only be in order with its reads
+  wait_lgkm0();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+  for (int c = lane; c < rows * 16; c += 64) {
+    const int row = c >> 4, ch = c & 15;
+    if (ch * 8 < cols) {
+      const u32x4 v = *(const u32x4*)(st + row * T::OPITCH + ch * 8);
+      __builtin_nontemporal_store(v, (u32x4*)(out + row * ld + ch * 8));
+    }
+  }
+}
+
+// One 256 x 256 tile of dx: rows of `tile`, columns from col0.
+__device__ __forceinline__ void dgrad_block(const GradArgs& a, const Tile tile, int col0, char* lds) {
+  using T = GradTile<GM_DGRAD>;
+  const int t = threadIdx.x;
+  int lane = t & 63;
+  // keeps what depends on the lane inside this tile: kept over the claiming loop, it spilled 42 registers
+  asm volatile("" : "+v"(lane));
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int m0 = (wave & 3) * 64, n0 = (wave >> 2) * 128;
+  const int M = a.M, K = a.K;
+  const uint16_t* abase = (const uint16_t*)a.a + (int64_t)tile.row_start * M;
+  const uint16_t* bbase = (const uint16_t*)a.b + (int64_t)tile.expert * M * K;
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)abase, (short)0, -1, kRawBufferWord3);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)bbase, (short)0, -1, kRawBufferWord3);
+  uint32_t oa[T::NLA], ob[T::NLB];
+#pragma unroll
+  for (int i = 0; i < T::NLA; ++i) {
+    const int r = (i * T::NW + wave) * 8 + (lane >> 3), c = (lane & 7) ^ line_swz(r);
+    oa[i] = ((uint32_t)min(r, tile.rows - 1) * (uint32_t)M + 8 * c) * 2;  // rows past the tile repeat its last
+  }
+#pragma unroll
+  for (int i = 0; i < T::NLB; ++i) {
+    const int r = turned_row<T::B_RB, T::NW>(i, wave, lane);
+    const int c = min(col0 + turned_col<T::B_RB>(r, lane), K - 8);  // columns past K repeat the last piece
+    ob[i] = ((uint32_t)r * (uint32_t)K + c) * 2;
+  }
+  // loads that reach a valid row (8 rows per load)
+  const int na = max(0, min(T::NLA, (tile.rows - wave * 8 + 63) / 64));
+  auto issue_a = [&](int k) {
+    char* dst = lds + (k % T::SA) * T::A_BYTES + wave * 1024;
+#pragma unroll
+    for (int i = 0; i < T::NLA; ++i)
+      if (i < na)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(dst + i * T::NW * 1024), 16, (int)oa[i], k * T::BK * 2,
+                                                 0, 0);
+  };
+  auto issue_b = [&](int k) {
+    char* dst = lds + T::B_BASE + (k % T::SB) * T::B_BYTES + wave * 1024;
+    const uint32_t soff = (uint32_t)k * T::BK * (uint32_t)K * 2;
+#pragma unroll
+    for (int i = 0; i < T::NLB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dst + i * T::NW * 1024), 16, (int)ob[i], (int)soff, 0, 0);
+  };
+  f32x16 acc[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const int live = tile.rows - m0, nk = M / T::BK;
+  if (live > 32)
+    grad_loop<GM_DGRAD, 2, 0>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
+  else if (live > 0)
+    grad_loop<GM_DGRAD, 1, 0>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
+  else
+    grad_loop<GM_DGRAD, 0, 0>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
+  // the loop ended on a barrier after the last operand read
+  uint16_t* out = (uint16_t*)a.out + ((int64_t)tile.row_start + m0) * K + col0 + n0;
+  store_wave<GM_DGRAD>(lds, acc, wave, lane, max(0, min(64, live)), min(128, K - col0 - n0), out, K);
+}
+
+// Logical block L over n_rows x n_cols tiles -> rectangles of GR x GC tiles, rows fastest.
+template <int GR, int GC>
+__device__ inline void grad_raster(int64_t L, int64_t n_rows, int n_cols, int64_t& row, int& col) {
+  const int64_t sg = L / ((int64_t)GR * n_cols), within = L % ((int64_t)GR * n_cols);
+  const int64_t gr = min((int64_t)GR, n_rows - sg * GR);
+  const int64_t cg = within / (gr * GC), w2 = within % (gr * GC);
+  row = sg * GR + w2 % gr;
+  col = (int)(cg * GC + w2 / gr);
+}
+
+// Persistent: one block per CU claims tiles, of its own XCD's run of the list first and then of the others',
+// and exits once all eight runs are empty.
+__global__ __launch_bounds__(512, 1) void grouped_dgrad_bf16(GradArgs a, int ncol) {
+  using T = GradTile<GM_DGRAD>;
+  __shared__ __attribute__((aligned(1024))) char lds[T::RING];
+  int* claim = (int*)(lds + T::RING - 4);  // outside the staged outputs; written when the loop's reads are over
+  const int64_t n_tiles = *a.n_tiles, nvalid = n_tiles * ncol, q = nvalid >> 3, r = nvalid & 7;
+  const int x = blockIdx.x & 7;
+  for (int v = 0; v < 8; ++v) {
+    const int y = (x + v) & 7;
+    const int64_t start = y * q + min((int64_t)y, r), len = q + (y < r ? 1 : 0);
+    for (;;) {
+      if (threadIdx.x == 0) *claim = atomicAdd(&a.work_ctr[y], 1);
+      __syncthreads();
+      const int64_t j = *claim;
+      __syncthreads();
+      if (j >= len) break;
+      int64_t tid;
+      int ct;
+      grad_raster<2, 16>(start + j, n_tiles, ncol, tid, ct);
+      const Tile tile = a.tiles[tid];
+      if (tile.rows > 0) dgrad_block(a, tile, ct * T::BN, lds);
+      __syncthreads();  // every wave's stores have read the LDS
+    }
+  }
+}
+
+// One 256 x 128 tile of dW[e]: output features from i0, input features from j0. Rows past the expert's are
+// read as zeros: dy through the descriptor's range (the step's rows of dy and nothing behind them), gathered x
+// through an offset past the range.
+template <bool GATHER>
+__global__ __launch_bounds__(256, 2) void grouped_wgrad_bf16(GradArgs a, int mt, int kt_tiles) {
+  using T = GradTile<GM_WGRAD>;
+  __shared__ __attribute__((aligned(1024))) char lds[T::RING];
+  const int64_t L = xcd_logical_block((int64_t)a.E * mt * kt_tiles);
+  if (L < 0) return;
+  const int expert = (int)(L / ((int64_t)mt * kt_tiles));
+  int64_t it;
+  int jt;
+  grad_raster<4, 16>(L % ((int64_t)mt * kt_tiles), mt, kt_tiles, it, jt);
+  const int i0 = (int)it * T::BM, j0 = jt * T::BN;
+  const int M = a.M, K = a.K;
+  const int64_t row0 = min(max((int64_t)a.offsets[expert], (int64_t)0), a.R);
+  const int cnt = (int)(min(max((int64_t)a.offsets[expert + 1], row0), a.R) - row0);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m0 = wave * 64;
+  f32x16 acc[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  const bool live = i0 + m0 < M;
+  if (cnt > 0) {
+    const int nk = (cnt + T::BK - 1) / T::BK;
+    uint32_t oa[T::NLA], ob[T::NLB];
+    int rb_row[T::NLB];
+#pragma unroll
+    for (int i = 0; i < T::NLA; ++i) {
+      const int r = turned_row<T::A_RB, T::NW>(i, wave, lane);
+      oa[i] = ((uint32_t)r * (uint32_t)M + min(i0 + turned_col<T::A_RB>(r, lane), M - 8)) * 2;
+    }
+#pragma unroll
+    for (int i = 0; i < T::NLB; ++i) {
+      const int r = rb_row[i] = turned_row<T::B_RB, T::NW>(i, wave, lane);
+      const int c = min(j0 + turned_col<T::B_RB>(r, lane), K - 8);
+      ob[i] = GATHER ? (uint32_t)c * 2 : ((uint32_t)r * (uint32_t)K + c) * 2;
+    }
+    const uint16_t* abase = (const uint16_t*)a.a + row0 * M;
+    const uint16_t* bbase = (const uint16_t*)a.b + (GATHER ? 0 : row0 * K);
+    // source rows of this lane's x loads, two steps ahead of the loads that need them: their own loads are then
+    // older than every operand load that may still be in flight when they are used
+    uint32_t src[2][T::NLB];
+    auto source = [&](int k, int i) {
+      return (uint32_t)a.src_row[row0 + min(k * T::BK + rb_row[i], cnt - 1)];
+    };
+    if (GATHER) {
+#pragma unroll
+      for (int i = 0; i < T::NLB; ++i) {
+        src[0][i] = source(0, i);
+        src[1][i] = source(1, i);
+      }
+    }
+    auto issue_a = [&](int k) {
+      const int left = min(cnt - k * T::BK, T::BK);
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(abase + (int64_t)k * T::BK * M), (short)0, left * M * 2, kRawBufferWord3);
+      char* dst = lds + (k % T::SA) * T::A_BYTES + wave * 1024;
+#pragma unroll
+      for (int i = 0; i < T::NLA; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(dst + i * T::NW * 1024), 16, (int)oa[i], 0, 0, 0);
+    };
+    auto issue_b = [&](int k) {
+      char* dst = lds + T::B_BASE + (k % T::SB) * T::B_BYTES + wave * 1024;
+      const int left = min(cnt - k * T::BK, T::BK);
+      if (GATHER) {
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)bbase, (short)0, (int)(uint32_t)(a.x_rows * K * 2), kRawBufferWord3);
+#pragma unroll
+        for (int i = 0; i < T::NLB; ++i) {
+          const uint32_t off = rb_row[i] < left ? src[0][i] * (uint32_t)K * 2 + ob[i] : 0xfffffff0u;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(dst + i * T::NW * 1024), 16, (int)off, 0, 0, 0);
+          src[0][i] = src[1][i];
+          src[1][i] = source(k + 2, i);
+        }
+      } else {
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(bbase + (int64_t)k * T::BK * K), (short)0, left * K * 2, kRawBufferWord3);
+#pragma unroll
+        for (int i = 0; i < T::NLB; ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(dst + i * T::NW * 1024), 16, (int)ob[i], 0, 0, 0);
+      }
+    };
+    if (live)
+      grad_loop<GM_WGRAD, 2, GATHER ? T::NLB : 0>(lds, issue_a, issue_b, acc, nk, lane, m0, 0);
+    else
+      grad_loop<GM_WGRAD, 0, GATHER ? T::NLB : 0>(lds, issue_a, issue_b, acc, nk, lane, m0, 0);
+  }
+  if (!live) return;
+  uint16_t* out = (uint16_t*)a.out + ((int64_t)expert * M + i0 + m0) * K + j0;
+  store_wave<GM_WGRAD>(lds, acc, wave, lane, 64, min(T::BN, K - j0), out, K);
+}
+
+int grad_cus() {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 8) n = 256;
+    n = n / 8 * 8;
+    cached[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+}  // namespace
+
+hipError_t launch_grouped_bf16(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s) {
+  if (mode == GM_DGRAD) {
+    const int nc = (a.K + 255) / 256;
+    const int64_t blocks = (max_tile_count * nc + 7) / 8 * 8;
+    if (blocks == 0) return hipSuccess;
+    if (!a.work_ctr) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(grouped_dgrad_bf16, dim3((unsigned)std::min<int64_t>(blocks, grad_cus())), dim3(512), 0, s, a,
+                       nc);
+    return hipGetLastError();
+  }
+  if (mode != GM_WGRAD) return hipErrorInvalidValue;
+  const int mt = (a.M + 255) / 256, kt = (a.K + 127) / 128;
+  const int64_t blocks = (int64_t)a.E * mt * kt;
+  if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  if (a.src_row)
+    hipLaunchKernelGGL(grouped_wgrad_bf16<true>, dim3((unsigned)blocks), dim3(256), 0, s, a, mt, kt);
+  else
+    hipLaunchKernelGGL(grouped_wgrad_bf16<false>, dim3((unsigned)blocks), dim3(256), 0, s, a, mt, kt);
+  return hipGetLastError();
+}
+hipError_t launch_grouped_f32(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s) {
   const int cols = ((mode == GM_FWD ? a.M : a.K) + 127) / 128;
   const int64_t tiles = mode == GM_WGRAD ? (int64_t)a.E * ((a.M + 127) / 128) : max_tile_count;
   int64_t blocks = tiles * cols;
@@ -162,21 +602,12 @@ hipError_t launch_any(GroupedMode mode, const GradArgs& a, int64_t max_tile_coun
   if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
   if (mode == GM_FWD)
-    hipLaunchKernelGGL((grouped_any<T, GM_FWD>), grid, block, 0, s, a, cols);
+    hipLaunchKernelGGL(grouped_f32_tile<GM_FWD>, grid, block, 0, s, a, cols);
   else if (mode == GM_DGRAD)
-    hipLaunchKernelGGL((grouped_any<T, GM_DGRAD>), grid, block, 0, s, a, cols);
+    hipLaunchKernelGGL(grouped_f32_tile<GM_DGRAD>, grid, block, 0, s, a, cols);
   else
-    hipLaunchKernelGGL((grouped_any<T, GM_WGRAD>), grid, block, 0, s, a, cols);
+    hipLaunchKernelGGL(grouped_f32_tile<GM_WGRAD>, grid, block, 0, s, a, cols);
   return hipGetLastError();
-}
-
-}  // namespace
-
-hipError_t launch_grouped_bf16(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s) {
-  return launch_any<uint16_t>(mode, a, max_tile_count, s);
-}
-hipError_t launch_grouped_f32(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s) {
-  return launch_any<float>(mode, a, max_tile_count, s);
 }
 
 }  // namespace moe

@@ -261,7 +261,7 @@ hipError_t launch_offset_lists(const int32_t* offsets, int E, int64_t R, TileSpe
                                const int32_t* row_index, int32_t div, int64_t x_rows, int32_t* src_row,
                                hipStream_t s);
 enum GroupedMode {
-  GM_FWD = 0,  // y = x W^T    (float32; the bf16 product runs on the expert GEMMs)
+  GM_FWD = 0,  // y = x W^T    (float32 only: the bf16 product runs on the expert GEMMs)
   GM_DGRAD,    // dx = dy W
   GM_WGRAD     // dW = dy^T x over each expert's rows
 };
@@ -276,10 +276,11 @@ struct GradArgs {
   int64_t x_rows;
   const Tile* tiles;        // fwd / dgrad
   const int32_t* n_tiles;
+  int32_t* work_ctr;        // bf16 dgrad: 8 counters, zero at launch
 };
 hipError_t launch_grouped_bf16(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s);
 hipError_t launch_grouped_f32(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s);
-constexpr int kGradRows = 256;  // rows per tile of the bf16 dgrad lists
+constexpr int kGradRows = 256;  // rows per tile of the bf16 dgrad list
 constexpr int kF32Rows = 128;   // rows per tile of the float32 lists
 
 // ---- 4-bit weights ----

@@ -45,7 +45,7 @@ moe_status check_grouped(int32_t E, int64_t R, int32_t in, int32_t out, int32_t 
   if (E > kMaxE || in % 64 != 0 || out % 64 != 0 || R >= kInt31) return MOE_ERR_UNSUPPORTED;
   // the bf16 kernels address an expert's matrix with 32-bit byte offsets
   if (dtype == MOE_BF16 && (int64_t)in * out * 2 >= kGiB4) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)in * out >= kInt31) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)in * out >= kInt31 || in > (1 << 22) || out > (1 << 22)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -70,18 +70,30 @@ struct GroupedLayout {
   int bm0, bm1, pick;
 };
 
+// Lists of the forward product: as the layer's own (moe_forward) for bf16, 128-row tiles for float32. List 1
+// serves dgrad too (256-row tiles). What depends on R is sized so that it never falls as R grows: the tile
+// height drops to 16 rows only below a threshold of rows, and the larger of the two counts is taken.
 GroupedLayout grouped_layout(int32_t E, int64_t R, int32_t dtype) {
   GroupedLayout w{};
-  w.bm0 = kF32Rows;
-  w.max_tiles0 = max_tiles(R, 1, E, 0, w.bm0);
+  const bool f32 = dtype == MOE_F32;
+  w.pick = f32 ? 0 : device_pick_rows(dtype, R, 1, E);
+  w.bm0 = f32 ? kF32Rows : w.pick ? 16 : gemm_bm(dtype, R, 1, E);
+  w.bm1 = f32 ? kF32Rows : kGradRows;
+  w.max_tiles0 = max_tiles(R, 1, E, 0, f32 ? kF32Rows : w.bm0);
+  w.max_tiles1 = max_tiles(R, 1, E, 0, w.bm1);
+  // 16-row lists hold at most R / 16 + E tiles, and only while R < MOE_PICK_BAND_ROWS * E; 256-row lists
+  // with their padding at most R / 256 + 4 E
+  const int64_t small_rows = std::min<int64_t>(R, (int64_t)tile_plan_rows(1) * E);
+  const int64_t room0 = f32 ? w.max_tiles0 : std::max(w.max_tiles1, max_tiles(small_rows, 1, E, 0, 16));
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
     o = align_up(o + bytes);
     return at;
   };
-  w.tiles0 = take(sizeof(Tile) * w.max_tiles0);
-  w.ntiles = take(sizeof(int32_t) * 20);
+  w.tiles0 = take(sizeof(Tile) * room0);
+  w.tiles1 = take(f32 ? 0 : sizeof(Tile) * w.max_tiles1);
+  w.ntiles = take(sizeof(int32_t) * 20);  // two tile counts, 8 work counters per list, two hot counts
   w.src_row = take(sizeof(int32_t) * R);
   w.total = o;
   return w;
@@ -232,11 +244,30 @@ moe_status moe_grouped_linear(int32_t E, int64_t R, int32_t in, int32_t out, int
   int32_t* ntiles = at<int32_t>(ws, L.ntiles);
   int32_t* src = row_index ? at<int32_t>(ws, L.src_row) : nullptr;
   const TileSpec none{0, nullptr, nullptr, 0, nullptr, nullptr};
-  const TileSpec t0{L.bm0, at<Tile>(ws, L.tiles0), ntiles, 0, nullptr, nullptr};
-  MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, t0, none, 0, row_index, index_div, x_rows, src, s));
-  const GradArgs g{x, w, y, R, out, in, E, offsets, src, x_rows, t0.tiles, ntiles};
-  MOE_TRY(ST_GROUPED_LINEAR, dtype == MOE_F32 ? launch_grouped_f32(GM_FWD, g, L.max_tiles0, s)
-                                              : launch_grouped_bf16(GM_FWD, g, L.max_tiles0, s));
+  const TileSpec t0{L.bm0, at<Tile>(ws, L.tiles0), ntiles, small_expert_rows(dtype, L.bm0), ntiles + 2, ntiles + 18};
+  const TileSpec t1{L.bm1, at<Tile>(ws, L.tiles1), ntiles + 1, small_expert_rows(dtype, L.bm1), ntiles + 10,
+                    ntiles + 19};
+  MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, t0, L.pick ? t1 : none, L.pick, row_index, index_div,
+                                                x_rows, src, s));
+  if (dtype == MOE_F32) {
+    const GradArgs g{x, w, y, R, out, in, E, offsets, src, x_rows, t0.tiles, ntiles, nullptr};
+    MOE_TRY(ST_GROUPED_LINEAR, launch_grouped_f32(GM_FWD, g, L.max_tiles0, s));
+    return MOE_OK;
+  }
+  // the layer's expert GEMM without its row scale; source rows are resolved already (k = 1)
+  GroupedArgs g{};
+  g.sorted_pair = src;
+  g.k = 1;
+  g.gather_rows = x_rows;
+  g.prob[0] = ExpertProblem{x, in, row_index ? 1 : 0, w, nullptr, (int64_t)out * in, in, out, y, out, 0};
+  for (int list = 0; list < (L.pick ? 2 : 1); ++list) {
+    g.tiles = list ? t1.tiles : t0.tiles;
+    g.n_tiles = ntiles + list;
+    g.work_ctr = ntiles + (list ? 10 : 2);
+    g.n_hot = ntiles + 18 + list;
+    g.bm = list ? L.bm1 : L.bm0;
+    MOE_TRY(ST_GROUPED_LINEAR, launch_down(dtype, g, list ? L.max_tiles1 : L.max_tiles0, s));
+  }
   return MOE_OK;
 }
 
@@ -253,11 +284,11 @@ moe_status moe_grouped_linear_dgrad(int32_t E, int64_t R, int32_t in, int32_t ou
   void* ws = workspace;
   int32_t* ntiles = at<int32_t>(ws, L.ntiles);
   const TileSpec none{0, nullptr, nullptr, 0, nullptr, nullptr};
-  const TileSpec t0{L.bm0, at<Tile>(ws, L.tiles0), ntiles, 0, nullptr, nullptr};
+  const TileSpec t0{L.bm1, at<Tile>(ws, L.tiles0), ntiles, small_expert_rows(dtype, L.bm1), ntiles + 2, ntiles + 18};
   MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, t0, none, 0, nullptr, 1, 0, nullptr, s));
-  const GradArgs g{dy, w, dx, R, out, in, E, offsets, nullptr, 0, t0.tiles, ntiles};
-  MOE_TRY(ST_GROUPED_LINEAR, dtype == MOE_F32 ? launch_grouped_f32(GM_DGRAD, g, L.max_tiles0, s)
-                                              : launch_grouped_bf16(GM_DGRAD, g, L.max_tiles0, s));
+  const GradArgs g{dy, w, dx, R, out, in, E, offsets, nullptr, 0, t0.tiles, ntiles, ntiles + 2};
+  MOE_TRY(ST_GROUPED_LINEAR, dtype == MOE_F32 ? launch_grouped_f32(GM_DGRAD, g, L.max_tiles1, s)
+                                              : launch_grouped_bf16(GM_DGRAD, g, L.max_tiles1, s));
   return MOE_OK;
 }
 
@@ -279,7 +310,7 @@ moe_status moe_grouped_linear_wgrad(int32_t E, int64_t R, int32_t in, int32_t ou
     const TileSpec none{0, nullptr, nullptr, 0, nullptr, nullptr};
     MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, none, none, 0, row_index, index_div, x_rows, src, s));
   }
-  const GradArgs g{dy, x, dw, R, out, in, E, offsets, src, x_rows, nullptr, nullptr};
+  const GradArgs g{dy, x, dw, R, out, in, E, offsets, src, x_rows, nullptr, nullptr, nullptr};
   MOE_TRY(ST_GROUPED_LINEAR,
           dtype == MOE_F32 ? launch_grouped_f32(GM_WGRAD, g, 0, s) : launch_grouped_bf16(GM_WGRAD, g, 0, s));
   return MOE_OK;
