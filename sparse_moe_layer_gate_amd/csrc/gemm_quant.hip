@@ -27,28 +27,32 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int SEG = 128;           // k per 16-byte piece of the four lanes of a row
-constexpr int NSEG = 4;            // pieces per batch: a wave's loads in flight per weight tile
-constexpr int BATCH = SEG * NSEG;  // k per wave and batch
+constexpr int SEG = 128;  // k per 16-byte piece of the four lanes of a row
 
 // TT: 16-row activation tiles per block; KS: waves that split k (the other factor of the four waves splits
-// the weight rows). Each wave holds two 16-row weight tiles: with SWIGLU a gate tile and its up tile.
-template <int TT, int KS>
+// the weight rows); RT: 16-row weight tiles per wave (with SWIGLU, gate tiles and their up tiles in turn);
+// NSEG: pieces per batch, a wave's weight loads in flight per weight tile; LDS: activations held at a time.
+template <int TT_, int KS_, int RT_, int NSEG_, int LDS_, int BLOCKS_>
 struct QTile {
+  static constexpr int BLOCKS = BLOCKS_;  // per CU, for the register budget
+  static constexpr int TT = TT_, KS = KS_, RT = RT_, NSEG = NSEG_;
   static constexpr int ROWS = 16 * TT;
-  static constexpr int WAVE_N = 4 / KS;                 // waves over weight rows
-  static constexpr int LDS_ELEMS = 32768 + 8 * ROWS;    // activations of a chunk, rows padded by 8
-  static constexpr int STEP = KS * BATCH;               // k per batch of the block
+  static constexpr int WAVE_N = 4 / KS;            // waves over weight rows
+  static constexpr int BATCH = SEG * NSEG;         // k per wave and batch
+  static constexpr int STEP = KS * BATCH;          // k per batch of the block
+  static constexpr int LDS_ELEMS = LDS_ + 8 * ROWS;  // activations of a chunk, rows padded by 8
+  static_assert(ROWS * STEP <= LDS_, "a full tile's step fits");
   // k per chunk for a tile of `rows` activation rows: what the LDS holds, no more than the row needs
-  __device__ static int chunk(int rows, int K) {
-    return min(32768 / rows / STEP * STEP, (K + STEP - 1) / STEP * STEP);
-  }
+  __device__ static int chunk(int rows, int K) { return min(LDS_ / rows / STEP * STEP, (K + STEP - 1) / STEP * STEP); }
 };
 
-__device__ inline bf16x8 unpack8(uint32_t w) {
+// Eight values of a word as bfloat16 128 + q, in the order 0 4 1 5 2 6 3 7: three shifts and four and-ors. The
+// mask comes in a scalar and the exponent in a vector register: one instruction takes no two literals, and
+// with both as constants the compiler emits an and, then an or.
+__device__ inline bf16x8 unpack8(uint32_t w, uint32_t mask, uint32_t magic) {
   u32x4 v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+  for (int i = 0; i < 4; ++i) v[i] = ((w >> (4 * i)) & mask) | magic;
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -64,10 +68,9 @@ __device__ inline void exchange4(u32x4& d) {
   d[3] = e[1];
 }
 
-template <int TT, int KS, int G, bool SWIGLU>
-__global__ __launch_bounds__(256) void qlinear_kernel(QuantArgs a) {
-  using T = QTile<TT, KS>;
-  constexpr int RT = 2;                       // weight tiles per wave
+template <class T, int G, bool SWIGLU>
+__global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
+  constexpr int TT = T::TT, KS = T::KS, RT = T::RT, NSEG = T::NSEG, BATCH = T::BATCH;
   constexpr int GPS = SEG / G;                // groups per piece
   constexpr int STEPS = G / 32;               // matrix steps per group
   __shared__ __attribute__((aligned(16))) uint16_t xs[T::LDS_ELEMS];
@@ -86,18 +89,23 @@ __global__ __launch_bounds__(256) void qlinear_kernel(QuantArgs a) {
   const int kw = wave % KS, nw = wave / KS;   // this wave's k share and weight rows
   const int r16 = lane & 15, j = lane >> 4;
   // output columns of the block, and this wave's two weight tiles
-  constexpr int WCOLS = SWIGLU ? 16 : 32;
+  constexpr int WCOLS = SWIGLU ? 8 * RT : 16 * RT;
   const int ncols = SWIGLU ? half : a.M;
   const int col0 = (blockIdx.x * T::WAVE_N + nw) * WCOLS;
-  const uint8_t* wq[RT];
-  const uint16_t* ws[RT];
+  // an expert's matrix is below 4 GiB: one scalar base and 32-bit offsets
+  const uint8_t* qb = a.q + (int64_t)expert * a.M * (K / 2);
+  const uint16_t* sb = a.s + (int64_t)expert * a.M * (K / G);
+  uint32_t wq[RT], ws[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    int m = SWIGLU ? t * half + min(col0, ncols - WCOLS) : min(col0, ncols - WCOLS) + 16 * t;
-    const int64_t row = (int64_t)expert * a.M + m + r16;
-    wq[t] = a.q + row * (K / 2);
-    ws[t] = a.s + row * (K / G);
+    const int c = min(col0, ncols - WCOLS);
+    const int m = SWIGLU ? (t & 1) * half + c + 16 * (t >> 1) : c + 16 * t;
+    wq[t] = (uint32_t)(m + r16) * (uint32_t)(K / 2);
+    ws[t] = (uint32_t)(m + r16) * (uint32_t)(K / G);
   }
+  uint32_t mask = 0x000f000fu, magic = 0x43004300u;
+  asm("" : "+s"(mask));  // not constants to the compiler: see unpack8
+  asm("" : "+v"(magic));
   const u32x4 neg = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};  // -136 as bfloat16 pairs
   const bf16x8 minus136 = __builtin_bit_cast(bf16x8, neg);
 
@@ -121,8 +129,9 @@ __global__ __launch_bounds__(256) void qlinear_kernel(QuantArgs a) {
       for (int t = 0; t < RT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     u32x4 q[RT][NSEG];
-    uint16_t sc[RT][NSEG][GPS];
-    // this wave's batch at k0: 16 bytes per piece and weight tile, and the pieces' scales; past K the last
+    constexpr int SW = (NSEG * GPS + 1) / 2;  // words of a batch's scales, two a word
+    uint32_t sc[RT][SW];
+    // this wave's batch at k0: 16 bytes per piece and weight tile, and the batch's scales; past K the last
     // valid piece again (the activations there are zero)
     auto load = [&](int k0) {
 #pragma unroll
@@ -132,11 +141,25 @@ __global__ __launch_bounds__(256) void qlinear_kernel(QuantArgs a) {
         for (int t = 0; t < RT; ++t) {
           // one row tile per expert: the bytes are used once; more of them share the weights in L2
           if (TT == 1)
-            q[t][p] = __builtin_nontemporal_load((const u32x4*)(wq[t] + (k >> 1)));
+            q[t][p] = __builtin_nontemporal_load((const u32x4*)(qb + (wq[t] + (uint32_t)(k >> 1))));
           else
-            q[t][p] = *(const u32x4*)(wq[t] + (k >> 1));
+            q[t][p] = *(const u32x4*)(qb + (wq[t] + (uint32_t)(k >> 1)));
+        }
+      }
+      if (k0 + BATCH <= K) {  // the wave's scales of the batch lie together: wide loads
 #pragma unroll
-          for (int g = 0; g < GPS; ++g) sc[t][p][g] = ws[t][min((k0 + p * SEG) / G + g, K / G - 1)];
+        for (int t = 0; t < RT; ++t) {
+          sc[t][SW - 1] = 0;
+          __builtin_memcpy(sc[t], sb + (ws[t] + (uint32_t)(k0 / G)), 2 * NSEG * GPS);
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+#pragma unroll
+          for (int g = 0; g < SW; ++g) {
+            sc[t][g] = sb[ws[t] + (uint32_t)min(k0 / G + 2 * g, K / G - 1)];
+            sc[t][g] |= (uint32_t)sb[ws[t] + (uint32_t)min(k0 / G + 2 * g + 1, K / G - 1)] << 16;
+          }
         }
       }
     };
@@ -159,15 +182,14 @@ __global__ __launch_bounds__(256) void qlinear_kernel(QuantArgs a) {
       __syncthreads();
       for (int b0 = kw * BATCH; b0 < kc && c0 + b0 < K; b0 += T::STEP) {
         u32x4 cq[RT][NSEG];
-        uint16_t cs[RT][NSEG][GPS];
+        uint32_t cs[RT][SW];
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
+        for (int t = 0; t < RT; ++t) {
 #pragma unroll
-          for (int p = 0; p < NSEG; ++p) {
-            cq[t][p] = q[t][p];
+          for (int p = 0; p < NSEG; ++p) cq[t][p] = q[t][p];
 #pragma unroll
-            for (int g = 0; g < GPS; ++g) cs[t][p][g] = sc[t][p][g];
-          }
+          for (int g = 0; g < SW; ++g) cs[t][g] = sc[t][g];
+        }
         // the next batch is STEP further on, within the chunk or at the next one's start (chunks are
         // whole steps); nothing is read past the row
         if (c0 + b0 + T::STEP < K) load(c0 + b0 + T::STEP);
@@ -181,35 +203,37 @@ __global__ __launch_bounds__(256) void qlinear_kernel(QuantArgs a) {
           const uint16_t* xp = xs + b0 + p * SEG;
 #pragma unroll
           for (int g = 0; g < GPS; ++g) {
-            f32x4 sum[TT][RT];
+            f32x4 off[TT];  // -136 sum(x) of the group, the start of every tile's sum
             bf16x8 xf[STEPS][TT];
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
-              f32x4 c = {0.f, 0.f, 0.f, 0.f};
+              off[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
               for (int u = 0; u < STEPS; ++u) {
                 const int piece = G < SEG ? 4 * (g * STEPS + u) + j : 4 * j + u;
                 xf[u][i] = *(const bf16x8*)(xp + min(16 * i + r16, rows - 1) * pitch + piece * 8);
-                c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], minus136, c, 0, 0, 0);
+                off[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], minus136, off[i], 0, 0, 0);
               }
-#pragma unroll
-              for (int t = 0; t < RT; ++t) sum[i][t] = c;
             }
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
+              f32x4 sum[TT];
 #pragma unroll
               for (int u = 0; u < STEPS; ++u) {
-                const bf16x8 w = unpack8(cq[t][p][g * STEPS + u]);
+                const bf16x8 w = unpack8(cq[t][p][g * STEPS + u], mask, magic);
 #pragma unroll
                 for (int i = 0; i < TT; ++i)
-                  sum[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, sum[i][t], 0, 0, 0);
+                  sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, u == 0 ? off[i] : sum[i], 0, 0, 0);
               }
-              const float s = bf16_f32(cs[t][p][g]);
+              const uint32_t sw = cs[t][(p * GPS + g) / 2];
+              const float s = __uint_as_float((p * GPS + g) & 1 ? sw & 0xffff0000u : sw << 16);
 #pragma unroll
               for (int i = 0; i < TT; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][t][r] += s * sum[i][t][r];
+                for (int r = 0; r < 4; ++r) acc[i][t][r] += s * sum[i][r];
             }
+            // keeps the compiler from reading several groups' activations ahead, which spilled
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
@@ -248,36 +272,37 @@ __global__ __launch_bounds__(256) void qlinear_kernel(QuantArgs a) {
           const int row = 16 * i + 4 * j + r;
           if (row >= rows) continue;
           uint16_t* y = a.y + (row0 + tile0 + row) * ncols + col0 + r16;
-          if (SWIGLU) {
-            y[0] = (uint16_t)bf16_pair(swiglu_bf16(acc[i][0][r], acc[i][1][r], a.limit), 0.f);
-          } else {
-            y[0] = (uint16_t)bf16_pair(acc[i][0][r], 0.f);
-            y[16] = (uint16_t)bf16_pair(acc[i][1][r], 0.f);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            if (SWIGLU) {
+              if (t & 1) y[8 * (t - 1)] = (uint16_t)bf16_pair(swiglu_bf16(acc[i][t - 1][r], acc[i][t][r], a.limit), 0.f);
+            } else {
+              y[16 * t] = (uint16_t)bf16_pair(acc[i][t][r], 0.f);
+            }
           }
         }
     }
   }
 }
 
-template <int TT, int KS, int G>
+template <class T, int G>
 hipError_t launch_q(const QuantArgs& a, hipStream_t s) {
-  using T = QTile<TT, KS>;
-  const int wcols = (a.swiglu ? 16 : 32) * T::WAVE_N, ncols = a.swiglu ? a.M / 2 : a.M;
+  const int wcols = (a.swiglu ? 8 : 16) * T::RT * T::WAVE_N, ncols = a.swiglu ? a.M / 2 : a.M;
   int64_t z = (a.R + (int64_t)a.E * T::ROWS - 1) / ((int64_t)a.E * T::ROWS);  // even load: one tile per block
   if (z > 65535) z = 65535;
   const dim3 grid((ncols + wcols - 1) / wcols, a.E, (unsigned)z);
   if (a.swiglu)
-    hipLaunchKernelGGL((qlinear_kernel<TT, KS, G, true>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((qlinear_kernel<T, G, true>), grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((qlinear_kernel<TT, KS, G, false>), grid, dim3(256), 0, s, a);
+    hipLaunchKernelGGL((qlinear_kernel<T, G, false>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
-template <int TT, int KS>
+template <class T>
 hipError_t launch_group(const QuantArgs& a, hipStream_t s) {
-  if (a.group == 32) return launch_q<TT, KS, 32>(a, s);
-  if (a.group == 64) return launch_q<TT, KS, 64>(a, s);
-  return launch_q<TT, KS, 128>(a, s);
+  if (a.group == 32) return launch_q<T, 32>(a, s);
+  if (a.group == 64) return launch_q<T, 64>(a, s);
+  return launch_q<T, 128>(a, s);
 }
 
 // One thread per eight values, group / 8 neighbouring lanes per group: the group's largest magnitude over
@@ -310,8 +335,10 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ w, 
 }  // namespace
 
 hipError_t launch_qlinear(const QuantArgs& a, hipStream_t s) {
-  if (a.R <= (int64_t)16 * a.E) return launch_group<1, 4>(a, s);
-  return launch_group<4, 1>(a, s);
+  if (a.R <= (int64_t)16 * a.E) return launch_group<QTile<1, 4, 2, 2, 16384, 4>>(a, s);
+  const int64_t wide_blocks = (a.M + 255) / 256 * ((a.R + 63) / 64);
+  if (wide_blocks < 128) return launch_group<QTile<4, 4, 2, 1, 32768, 2>>(a, s);
+  return launch_group<QTile<4, 1, 4, 1, 32768, 2>>(a, s);
 }
 
 hipError_t launch_quantize(int dtype, const void* w, int64_t rows, int K, int group, uint8_t* q, uint16_t* s,
