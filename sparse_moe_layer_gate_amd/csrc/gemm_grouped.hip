@@ -13,6 +13,7 @@
 #include <atomic>
 
 #include "moe_internal.h"
+#include "row_ops.h"
 
 namespace moe {
 namespace {
@@ -175,25 +176,24 @@ __device__ inline void bare_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
-// dgrad: 256 x 256 tile, eight waves, 64 reduction elements per step (whole lines of dy), dy in a two-stage
-// ring and W in a three-stage one: all 160 KiB of LDS, one block per CU.
-// wgrad: 256 x 128 tile, four waves, 32 rows per step, three stages: 72 KiB, two blocks per CU, so that one
-// block's products cover the other's first loads and its stores (an expert's few hundred rows make a
-// short loop, and every tile ends in 64 KiB of dW).
+// Both: 256 x 256 tile, eight waves, one block per CU.
+// dgrad: 64 reduction elements per step (whole lines of dy), dy in a two-stage ring and W in a three-stage
+// one: all 160 KiB of LDS.
+// wgrad: 32 rows per step, four stages of both operands (128 KiB).
 template <int MODE>
 struct GradTile {
   static constexpr bool A_T = MODE == GM_WGRAD;
-  static constexpr int NW = A_T ? 4 : 8;        // waves
-  static constexpr int BM = 256, BN = A_T ? 128 : 256, BK = A_T ? 32 : 64;
-  static constexpr int SA = A_T ? 3 : 2, SB = 3;  // stages
+  static constexpr int NW = 8;  // waves
+  static constexpr int BM = 256, BN = 256, BK = A_T ? 32 : 64;
+  static constexpr int SA = A_T ? 4 : 2, SB = A_T ? 4 : 3;  // stages
   static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;
   static constexpr int NLA = A_BYTES / 1024 / NW, NLB = B_BYTES / 1024 / NW;  // loads per wave and step
   static constexpr int B_BASE = SA * A_BYTES;
   static constexpr int RING = SA * A_BYTES + SB * B_BYTES;
   static constexpr int SLICES = BK / 16;
-  static constexpr int OPITCH = 128 + 8;  // staged output row of a wave
-  static_assert(NW * 64 * OPITCH * 2 <= RING - 16, "the staged outputs fit the ring");
+  static constexpr int OPITCH = 128 + 8;  // staged output row of a wave (dgrad)
   static constexpr int A_RB = BM * 2, B_RB = BN * 2;  // bytes per reduction row of a turned operand
+  static_assert(RING <= 160 * 1024 && SLICES % 2 == 0, "LDS; the last slice of a step is in buffer 1");
 };
 
 // Byte offset, within a stage of turned rows of RB bytes, of the fragment of 32 columns from col0: slice s adds
@@ -208,6 +208,12 @@ __device__ inline int turned_offset(int col0, int lane) {
 // load, as a possible reader of whatever is still being loaded).
 __device__ inline s16x4 read_tr16(const lds_s16x4* __restrict__ p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+}
+// The same for writes into a stage with no loads under way.
+typedef __attribute__((address_space(3))) uint2 lds_uint2;
+__device__ inline void write_lds8(lds_uint2* __restrict__ p, uint32_t x, uint32_t y) {
+  p->x = x;
+  p->y = y;
 }
 template <int RB>
 __device__ inline bf16x8 read_turned(const char* p) {
@@ -236,28 +242,32 @@ struct BoolC {
   static constexpr bool value = V;
 };
 
-// The reduction loop of one wave. issue_a(step) / issue_b(step) start this wave's loads of a step into its
-// stage; the newest NLB (dgrad) or NLA + NLB (wgrad) loads are those of later steps than the next.
-// (EXTRA: other vector loads that issue_b makes behind its direct ones.)
-template <int MODE, int MI, int EXTRA, class IA, class IB>
-__device__ __attribute__((always_inline)) inline void grad_loop(char* lds, IA&& issue_a, IB&& issue_b,
-                                                                f32x16 (&acc)[2][4], int nk, int lane, int m0,
-                                                                int n0) {
+// One wave's fragments of a 16-wide slice, double-buffered, and its products: 32 MI x 128 of C^T (the column
+// operand first, so that a lane holds four neighbouring columns of one row).
+template <int MODE, int MI>
+struct GradWave {
   using T = GradTile<MODE>;
-  constexpr int AHEAD = (T::SA > 2 ? T::NLA : 0) + (T::SB > 2 ? T::NLB + EXTRA : 0);
-  int a_off[MI > 0 ? MI : 1], b_off[4];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-    a_off[i] = T::A_T ? turned_offset<T::A_RB>(m0 + 32 * i, lane) : (m0 + 32 * i + (lane & 31)) * (T::BK * 2);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) b_off[j] = turned_offset<T::B_RB>(n0 + 32 * j, lane);
-  const int sw = line_swz(lane);
+  static constexpr int NR = MI > 0 ? MI * (T::A_T ? 2 : 1) + 8 : 0;  // LDS reads per slice
+  int a_off[MI > 0 ? MI : 1], b_off[4], sw, half;
   bf16x8 af[2][MI > 0 ? MI : 1], bf[2][4];
-  constexpr int NR = MI > 0 ? MI * (T::A_T ? 2 : 1) + 8 : 0;  // LDS reads per slice
-  auto read_slice = [&](int step, int sl, int buf) {
+  __device__ __attribute__((always_inline)) inline void init(int lane, int m0, int n0) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      a_off[i] = T::A_T ? turned_offset<T::A_RB>(m0 + 32 * i, lane) : (m0 + 32 * i + (lane & 31)) * (T::BK * 2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b_off[j] = turned_offset<T::B_RB>(n0 + 32 * j, lane);
+    sw = line_swz(lane);
+    half = lane >> 5;
+  }
+  // slice sl of the step in A stage sta and B stage stb
+  __device__ __attribute__((always_inline)) inline void read(const char* lds, int sta, int stb, int sl, int buf) {
     if (MI == 0) return;
-    const char* sa = lds + (step % T::SA) * T::A_BYTES;
-    const char* sb = lds + T::B_BASE + (step % T::SB) * T::B_BYTES;
+    // the stage's place is a scalar to the compiler, which otherwise keeps an address register per read
+    int oa = sta * T::A_BYTES, ob = T::B_BASE + stb * T::B_BYTES;
+    asm("" : "+s"(oa));
+    asm("" : "+s"(ob));
+    const char* sa = lds + oa;
+    const char* sb = lds + ob;
 #pragma unroll
     for (int j = 0; j < 4; ++j) bf[buf][j] = read_turned<T::B_RB>(sb + b_off[j] + sl * 16 * T::B_RB);
 #pragma unroll
@@ -265,24 +275,38 @@ __device__ __attribute__((always_inline)) inline void grad_loop(char* lds, IA&& 
       if (T::A_T)
         af[buf][i] = read_turned<T::A_RB>(sa + a_off[i] + sl * 16 * T::A_RB);
       else
-        af[buf][i] = *(const bf16x8*)(sa + a_off[i] + ((2 * sl + (lane >> 5)) ^ sw) * 16);
+        af[buf][i] = *(const bf16x8*)(sa + a_off[i] + ((2 * sl + half) ^ sw) * 16);
     }
-  };
-  auto compute = [&](int buf) {
+  }
+  __device__ __attribute__((always_inline)) inline void compute(f32x16 (&acc)[2][4], int buf) {
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[buf][i], bf[buf][j], acc[i][j], 0, 0, 0);
-  };
-  auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[buf][j], af[buf][i], acc[i][j], 0, 0, 0);
+  }
+};
+__device__ inline void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
+
+// dgrad's reduction loop of one wave. issue_a(step) / issue_b(step) start this wave's loads of a step into its
+// stage; the newest NLB loads are those of the step after the next.
+template <int MI, class IA, class IB>
+__device__ __attribute__((always_inline)) inline void dgrad_loop(char* lds, IA&& issue_a, IB&& issue_b,
+                                                                 f32x16 (&acc)[2][4], int nk, int lane, int m0,
+                                                                 int n0) {
+  using T = GradTile<GM_DGRAD>;
+  GradWave<GM_DGRAD, MI> w;
+  constexpr int NR = GradWave<GM_DGRAD, MI>::NR, AHEAD = T::NLB;
+  w.init(lane, m0, n0);
+  auto fence = [] { sched_fence(); };
+  auto read_slice = [&](int step, int sl, int buf) { w.read(lds, step % T::SA, step % T::SB, sl, buf); };
+  auto compute = [&](int buf) { w.compute(acc, buf); };
 
   // prologue: the steps before the first compute, oldest first
   issue_a(0);
   issue_b(0);
   if (nk > 1) {
-    if (T::SA > 2) issue_a(1);
-    if (T::SB > 2) issue_b(1);
+    issue_b(1);
     wait_vmcnt<AHEAD>();
   } else {
     wait_vmcnt<0>();
@@ -316,47 +340,47 @@ __device__ __attribute__((always_inline)) inline void grad_loop(char* lds, IA&& 
       }
     }
   };
-  static_assert(T::SLICES % 2 == 0, "the last slice is in buffer 1, the next step's first in buffer 0");
   int kt = 0;
   for (; kt + T::SB - 1 < nk; ++kt) step(kt, BoolC<true>{}, BoolC<true>{}, BoolC<false>{});
-  if (kt + 1 < nk) {
-    // the step before the last: with two stages of A its loads are still to come
-    if (T::SA == 2)
-      step(kt++, BoolC<true>{}, BoolC<false>{}, BoolC<false>{});
-    else
-      step(kt++, BoolC<false>{}, BoolC<false>{}, BoolC<false>{});
-  }
+  if (kt + 1 < nk) step(kt++, BoolC<true>{}, BoolC<false>{}, BoolC<false>{});
   step(kt, BoolC<false>{}, BoolC<false>{}, BoolC<true>{});
 }
 
 // Results of one wave through its part of the (idle) ring: whole 16-byte pieces of `rows` rows of up to 128
 // columns, `ld` elements apart.
-template <int MODE>
-__device__ __attribute__((always_inline)) inline void store_wave(char* lds, const f32x16 (&acc)[2][4], int wave,
-                                                                 int lane, int rows, int cols, uint16_t* out,
-                                                                 int64_t ld) {
-  using T = GradTile<MODE>;
+__device__ __attribute__((always_inline)) inline void store_dgrad(char* lds, const f32x16 (&acc)[2][4], int wave,
+                                                                  int lane, int rows, int cols, uint16_t* out,
+                                                                  int64_t ld) {
+  using T = GradTile<GM_DGRAD>;
+  static_assert(T::NW * 64 * T::OPITCH * 2 <= T::RING - 16, "the staged outputs fit the ring");
   uint16_t* st = (uint16_t*)lds + wave * (64 * T::OPITCH);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (32 * i >= rows) continue;
+    uint16_t* row = st + (i * 32 + (lane & 31)) * T::OPITCH + 4 * (lane >> 5);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int row = i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        st[row * T::OPITCH + j * 32 + (lane & 31)] = __builtin_bit_cast(uint16_t, (__bf16)acc[i][j][r]);
-    }
+      for (int q = 0; q < 4; ++q) {
+        const uint2 v = make_uint2(bf16_pair(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                                   bf16_pair(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
+        *(uint2*)(row + j * 32 + 8 * q) = v;
+      }
   }
   // the region is this wave's own: its writes need only be in order with its reads
   wait_lgkm0();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-  for (int c = lane; c < rows * 16; c += 64) {
-    const int row = c >> 4, ch = c & 15;
-    if (ch * 8 < cols) {
-      const u32x4 v = *(const u32x4*)(st + row * T::OPITCH + ch * 8);
-      __builtin_nontemporal_store(v, (u32x4*)(out + row * ld + ch * 8));
+  // 4 rows of 16 pieces at a time, eight reads ahead of their stores
+  const int row0 = lane >> 4, ch = lane & 15;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    u32x4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = *(const u32x4*)(st + (h * 32 + u * 4 + row0) * T::OPITCH + ch * 8);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int row = h * 32 + u * 4 + row0;
+      if (row < rows && ch * 8 < cols) __builtin_nontemporal_store(v[u], (u32x4*)(out + row * ld + ch * 8));
     }
   }
 }
@@ -413,14 +437,14 @@ __device__ __forceinline__ void dgrad_block(const GradArgs& a, const Tile tile, 
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
   const int live = tile.rows - m0, nk = M / T::BK;
   if (live > 32)
-    grad_loop<GM_DGRAD, 2, 0>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
+    dgrad_loop<2>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
   else if (live > 0)
-    grad_loop<GM_DGRAD, 1, 0>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
+    dgrad_loop<1>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
   else
-    grad_loop<GM_DGRAD, 0, 0>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
+    dgrad_loop<0>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
   // the loop ended on a barrier after the last operand read
   uint16_t* out = (uint16_t*)a.out + ((int64_t)tile.row_start + m0) * K + col0 + n0;
-  store_wave<GM_DGRAD>(lds, acc, wave, lane, max(0, min(64, live)), min(128, K - col0 - n0), out, K);
+  store_dgrad(lds, acc, wave, lane, max(0, min(64, live)), min(128, K - col0 - n0), out, K);
 }
 
 // Logical block L over n_rows x n_cols tiles -> rectangles of GR x GC tiles, rows fastest.
@@ -460,102 +484,222 @@ __global__ __launch_bounds__(512, 1) void grouped_dgrad_bf16(GradArgs a, int nco
   }
 }
 
-// One 256 x 128 tile of dW[e]: output features from i0, input features from j0. Rows past the expert's are
-// read as zeros: dy through the descriptor's range (the step's rows of dy and nothing behind them), gathered x
-// through an offset past the range.
+// wgrad. An expert's few hundred rows make a short loop (eight steps at 256 rows) and every tile ends in 128 KiB
+// of dW, so what counts is that neither the first loads of a tile nor its stores are waited for: a block is
+// persistent and its ring runs across tile borders. While a tile's last steps compute and its results are
+// stored, the next tile's first three steps are already being loaded; the results pass through the one
+// stage that is free at that point. Tiles are dealt in runs of one per CU of an XCD, runs to the XCDs in turn:
+// the blocks of an XCD work on one rectangle of one expert's dW and share its rows in L2, and experts of
+// different sizes spread over all XCDs.
+//
+// Rows past the expert's are read as zeros: dy through the descriptor's range (the step's rows of dy and nothing
+// behind them), gathered x through an offset past the range.
+struct WgradTile {
+  int expert, i0, j0, cnt, nk;
+  int64_t row0;
+};
 template <bool GATHER>
-__global__ __launch_bounds__(256, 2) void grouped_wgrad_bf16(GradArgs a, int mt, int kt_tiles) {
+__global__ __launch_bounds__(512, 1) void grouped_wgrad_bf16(GradArgs a, int mt, int kt_tiles) {
   using T = GradTile<GM_WGRAD>;
+  constexpr int S = T::SA, PER = T::NLA + T::NLB, NST = 16;  // stages, loads per step, stores per tile
+  static_assert(T::SA == T::SB && (S & (S - 1)) == 0 && (S - 2) * PER + NST < 64, "ring indices and vmcnt");
   __shared__ __attribute__((aligned(1024))) char lds[T::RING];
-  const int64_t L = xcd_logical_block((int64_t)a.E * mt * kt_tiles);
-  if (L < 0) return;
-  const int expert = (int)(L / ((int64_t)mt * kt_tiles));
-  int64_t it;
-  int jt;
-  grad_raster<4, 16>(L % ((int64_t)mt * kt_tiles), mt, kt_tiles, it, jt);
-  const int i0 = (int)it * T::BM, j0 = jt * T::BN;
-  const int M = a.M, K = a.K;
-  const int64_t row0 = min(max((int64_t)a.offsets[expert], (int64_t)0), a.R);
-  const int cnt = (int)(min(max((int64_t)a.offsets[expert + 1], row0), a.R) - row0);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int m0 = wave * 64;
-  f32x16 acc[2][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  const bool live = i0 + m0 < M;
-  if (cnt > 0) {
-    const int nk = (cnt + T::BK - 1) / T::BK;
-    uint32_t oa[T::NLA], ob[T::NLB];
-    int rb_row[T::NLB];
+  const int m0 = (wave & 3) * 64, n0 = (wave >> 2) * 128;
+  const int M = a.M, K = a.K;
+  typedef const __attribute__((address_space(4))) int32_t* const_i32;  // scalar loads: none counts in vmcnt
+  const uint32_t slots = gridDim.x >> 3, stride = gridDim.x;
+  const uint32_t per_expert = (uint32_t)(mt * kt_tiles), total = per_expert * (uint32_t)a.E;
+  const uint32_t first = (blockIdx.x & 7) * slots + (blockIdx.x >> 3);
+
+  auto decode = [&](uint32_t id) {
+    WgradTile t;
+    t.expert = (int)(id / per_expert);
+    // rectangles of 4 x 8 tiles, rows fastest
+    const uint32_t in = id % per_expert, sg = in / (4u * kt_tiles), within = in % (4u * kt_tiles);
+    const uint32_t gr = min(4u, (uint32_t)mt - sg * 4), cg = within / (gr * 8), w2 = within % (gr * 8);
+    t.i0 = (int)(sg * 4 + w2 % gr) * T::BM;
+    t.j0 = (int)(cg * 8 + w2 / gr) * T::BN;
+    const int64_t lo = ((const_i32)a.offsets)[t.expert], hi = ((const_i32)a.offsets)[t.expert + 1];
+    t.row0 = min(max(lo, (int64_t)0), a.R);
+    t.cnt = (int)(min(max(hi, t.row0), a.R) - t.row0);
+    t.nk = (t.cnt + T::BK - 1) / T::BK;
+    return t;
+  };
+
+  // ---- the load stream: its own tile and step, up to three steps ahead of the products ----
+  uint32_t load_id = first;
+  int load_k = 0;
+  int issued = 0;  // steps
+  WgradTile lt{};
+  uint32_t oa[T::NLA], ob[T::NLB];
+  auto load_tile = [&](uint32_t id) {  // the first tile from id on that has rows
+    for (; id < total; id += stride) {
+      lt = decode(id);
+      if (lt.nk > 0) break;
+    }
+    load_id = id;
+    load_k = 0;
+    if (id >= total) return;
 #pragma unroll
     for (int i = 0; i < T::NLA; ++i) {
       const int r = turned_row<T::A_RB, T::NW>(i, wave, lane);
-      oa[i] = ((uint32_t)r * (uint32_t)M + min(i0 + turned_col<T::A_RB>(r, lane), M - 8)) * 2;
+      oa[i] = ((uint32_t)r * (uint32_t)M + min(lt.i0 + turned_col<T::A_RB>(r, lane), M - 8)) * 2;
     }
 #pragma unroll
     for (int i = 0; i < T::NLB; ++i) {
-      const int r = rb_row[i] = turned_row<T::B_RB, T::NW>(i, wave, lane);
-      const int c = min(j0 + turned_col<T::B_RB>(r, lane), K - 8);
+      const int r = turned_row<T::B_RB, T::NW>(i, wave, lane);
+      const int c = min(lt.j0 + turned_col<T::B_RB>(r, lane), K - 8);
       ob[i] = GATHER ? (uint32_t)c * 2 : ((uint32_t)r * (uint32_t)K + c) * 2;
     }
-    const uint16_t* abase = (const uint16_t*)a.a + row0 * M;
-    const uint16_t* bbase = (const uint16_t*)a.b + (GATHER ? 0 : row0 * K);
-    // source rows of this lane's x loads, two steps ahead of the loads that need them: their own loads are then
-    // older than every operand load that may still be in flight when they are used
-    uint32_t src[2][T::NLB];
-    auto source = [&](int k, int i) {
-      return (uint32_t)a.src_row[row0 + min(k * T::BK + rb_row[i], cnt - 1)];
-    };
-    if (GATHER) {
+  };
+  // source rows of the next issued step's x loads: a wave's load i takes two rows, so their indices are scalar
+  // loads, made a step ahead; fold() turns them into this lane's offsets once they are there
+  int32_t idx[T::NLB][2];
+  uint32_t ox[T::NLB];
+  auto fetch_index = [&]() {
+    if (!GATHER || load_id >= total) return;
 #pragma unroll
-      for (int i = 0; i < T::NLB; ++i) {
-        src[0][i] = source(0, i);
-        src[1][i] = source(1, i);
+    for (int i = 0; i < T::NLB; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = load_k * T::BK + (i * T::NW + wave) * 2 + h;
+        idx[i][h] = ((const_i32)a.src_row)[lt.row0 + min(r, lt.cnt - 1)];
       }
+  };
+  auto fold = [&]() {
+    if (!GATHER || load_id >= total) return;
+    const int left = lt.cnt - load_k * T::BK;
+#pragma unroll
+    for (int i = 0; i < T::NLB; ++i) {
+      const uint32_t r = (uint32_t)(lane < 32 ? idx[i][0] : idx[i][1]);
+      ox[i] = turned_row<T::B_RB, T::NW>(i, wave, lane) < left ? r * (uint32_t)K * 2 + ob[i] : 0xfffffff0u;
     }
-    auto issue_a = [&](int k) {
-      const int left = min(cnt - k * T::BK, T::BK);
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(abase + (int64_t)k * T::BK * M), (short)0, left * M * 2, kRawBufferWord3);
-      char* dst = lds + (k % T::SA) * T::A_BYTES + wave * 1024;
+  };
+  // the stream's next step into its stage; nothing at its end
+  auto issue = [&]() {
+    if (load_id >= total) return;
+    const int left = min(lt.cnt - load_k * T::BK, T::BK);
+    const int64_t row = lt.row0 + (int64_t)load_k * T::BK;
+    char* da = lds + (issued & (S - 1)) * T::A_BYTES + wave * 1024;
+    char* db = lds + T::B_BASE + (issued & (S - 1)) * T::B_BYTES + wave * 1024;
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)((const uint16_t*)a.a + row * M), (short)0,
+                                                                        left * M * 2, kRawBufferWord3);
 #pragma unroll
-      for (int i = 0; i < T::NLA; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(dst + i * T::NW * 1024), 16, (int)oa[i], 0, 0, 0);
-    };
-    auto issue_b = [&](int k) {
-      char* dst = lds + T::B_BASE + (k % T::SB) * T::B_BYTES + wave * 1024;
-      const int left = min(cnt - k * T::BK, T::BK);
-      if (GATHER) {
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)bbase, (short)0, (int)(uint32_t)(a.x_rows * K * 2), kRawBufferWord3);
+    for (int i = 0; i < T::NLA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(da + i * T::NW * 1024), 16, (int)oa[i], 0, 0, 0);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)((const uint16_t*)a.b + (GATHER ? 0 : row * K)), (short)0,
+        GATHER ? (int)(uint32_t)(a.x_rows * K * 2) : left * K * 2, kRawBufferWord3);
 #pragma unroll
-        for (int i = 0; i < T::NLB; ++i) {
-          const uint32_t off = rb_row[i] < left ? src[0][i] * (uint32_t)K * 2 + ob[i] : 0xfffffff0u;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(dst + i * T::NW * 1024), 16, (int)off, 0, 0, 0);
-          src[0][i] = src[1][i];
-          src[1][i] = source(k + 2, i);
-        }
-      } else {
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)(bbase + (int64_t)k * T::BK * K), (short)0, left * K * 2, kRawBufferWord3);
+    for (int i = 0; i < T::NLB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(db + i * T::NW * 1024), 16, (int)(GATHER ? ox[i] : ob[i]),
+                                               0, 0, 0);
+    ++issued;
+    if (++load_k == lt.nk) load_tile(load_id + stride);
+  };
+
+  GradWave<GM_WGRAD, 2> w;
+  constexpr int NR = GradWave<GM_WGRAD, 2>::NR;
+  w.init(lane, m0, n0);
+  load_tile(first);
 #pragma unroll
-        for (int i = 0; i < T::NLB; ++i)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(dst + i * T::NW * 1024), 16, (int)ob[i], 0, 0, 0);
-      }
-    };
-    if (live)
-      grad_loop<GM_WGRAD, 2, GATHER ? T::NLB : 0>(lds, issue_a, issue_b, acc, nk, lane, m0, 0);
-    else
-      grad_loop<GM_WGRAD, 0, GATHER ? T::NLB : 0>(lds, issue_a, issue_b, acc, nk, lane, m0, 0);
+  for (int i = 0; i < S - 1; ++i) {
+    fetch_index();
+    fold();
+    issue();
   }
-  if (!live) return;
-  uint16_t* out = (uint16_t*)a.out + ((int64_t)expert * M + i0 + m0) * K + j0;
-  store_wave<GM_WGRAD>(lds, acc, wave, lane, 64, min(T::BN, K - j0), out, K);
+  fetch_index();
+  fold();
+  wait_vmcnt<0>();
+  bare_barrier();
+  int done = 0;         // steps whose products ran
+  int mark = 0;         // steps issued before this wave's last stores
+  bool stored = false;  // the previous tile's results were stored by this wave
+  if (issued > 0) w.read(lds, 0, 0, 0, 0);
+  sched_fence();
+
+  for (uint32_t id = first; id < total; id += stride) {
+    const WgradTile t = decode(id);
+    f32x16 acc[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    for (int k = 0; k < t.nk; ++k) {
+      const int st = done & (S - 1), nx = (done + 1) & (S - 1);
+      // into the stage of the step before this one (of the tile before: behind its epilogue's barrier)
+      issue();
+      fetch_index();
+      w.read(lds, st, st, 1, 1);
+      sched_fence();
+      wait_lgkm<NR>();
+      w.compute(acc, 0);
+      sched_fence();
+      wait_lgkm0();  // this step's reads have landed, and the indices
+      fold();
+      // the next step has landed: of the loads behind its own, `ahead` steps may be in flight, and the stores of
+      // the last tile if they were issued after it
+      const int ahead = issued - done - 2;
+      ++done;
+      if (ahead < S - 2)
+        wait_vmcnt<0>();
+      else if (stored && issued - mark <= ahead)
+        wait_vmcnt<(S - 2) * PER + NST>();
+      else
+        wait_vmcnt<(S - 2) * PER>();
+      bare_barrier();
+      if (done < issued) w.read(lds, nx, nx, 0, 0);
+      sched_fence();
+      w.compute(acc, 1);
+      sched_fence();
+    }
+    // Epilogue in the stage the last step used (free until the next issue): each wave has 4 KiB of it (two in
+    // each operand's part), 32 rows x 64 columns a pass, 16-byte pieces swizzled by the row. Every pass issues four
+    // stores in any case (lanes past the columns through an offset past the range): the counts above rely on it.
+    const int free_st = (done + S - 1) & (S - 1);
+    stored = t.i0 + m0 < M;
+    mark = issued;
+    if (stored) {
+      char* sp = lds + (wave < 4 ? free_st * T::A_BYTES + wave * 4096 : T::B_BASE + free_st * T::B_BYTES + (wave - 4) * 4096);
+      const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)((uint16_t*)a.out + ((int64_t)t.expert * M + t.i0 + m0) * K), (short)0, 64 * K * 2, kRawBufferWord3);
+      const int cols = K - t.j0 - n0;  // of this wave's 128
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int jp = 0; jp < 2; ++jp) {
+          const int r = lane & 31;
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const f32x16& c = acc[i][2 * jp + jj];
+              write_lds8((lds_uint2*)(sp + r * 128 + (((4 * jj + q) ^ (r & 7)) * 16) + (lane >> 5) * 8),
+                         bf16_pair(c[4 * q], c[4 * q + 1]), bf16_pair(c[4 * q + 2], c[4 * q + 3]));
+            }
+          __atomic_signal_fence(__ATOMIC_SEQ_CST);  // a wave's LDS accesses are in order
+          u32x4 v[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int row = u * 8 + (lane >> 3);
+            v[u] = *(const u32x4*)(sp + row * 128 + (((lane & 7) ^ (row & 7)) * 16));
+          }
+          __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int row = i * 32 + u * 8 + (lane >> 3), col = jp * 64 + (lane & 7) * 8;
+            const uint32_t off = col < cols ? ((uint32_t)row * (uint32_t)K + t.j0 + n0 + col) * 2 : 0xfffffff0u;
+            __builtin_amdgcn_raw_buffer_store_b128(v[u], ro, (int)off, 0, 2);
+          }
+        }
+    }
+    wait_lgkm0();
+    bare_barrier();  // the stage is free again
+  }
 }
 
 int grad_cus() {
@@ -584,13 +728,14 @@ hipError_t launch_grouped_bf16(GroupedMode mode, const GradArgs& a, int64_t max_
     return hipGetLastError();
   }
   if (mode != GM_WGRAD) return hipErrorInvalidValue;
-  const int mt = (a.M + 255) / 256, kt = (a.K + 127) / 128;
-  const int64_t blocks = (int64_t)a.E * mt * kt;
-  if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  const int mt = (a.M + 255) / 256, kt = (a.K + 255) / 256;
+  const int64_t tiles = ((int64_t)a.E * mt * kt + 7) / 8 * 8;
+  if (tiles >= (int64_t)1 << 30) return hipErrorInvalidValue;  // 32-bit tile ids, with a stride to spare
+  const dim3 grid((unsigned)std::min<int64_t>(tiles, grad_cus())), block(512);
   if (a.src_row)
-    hipLaunchKernelGGL(grouped_wgrad_bf16<true>, dim3((unsigned)blocks), dim3(256), 0, s, a, mt, kt);
+    hipLaunchKernelGGL(grouped_wgrad_bf16<true>, grid, block, 0, s, a, mt, kt);
   else
-    hipLaunchKernelGGL(grouped_wgrad_bf16<false>, dim3((unsigned)blocks), dim3(256), 0, s, a, mt, kt);
+    hipLaunchKernelGGL(grouped_wgrad_bf16<false>, grid, block, 0, s, a, mt, kt);
   return hipGetLastError();
 }
 hipError_t launch_grouped_f32(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s) {
