@@ -87,7 +87,6 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kw = wave % KS, nw = wave / KS;   // this wave's k share and weight rows
-  const int r16 = lane & 15, j = lane >> 4;
   // output columns of the block, and this wave's two weight tiles
   constexpr int WCOLS = SWIGLU ? 8 * RT : 16 * RT;
   const int ncols = SWIGLU ? half : a.M;
@@ -95,14 +94,6 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
   // an expert's matrix is below 4 GiB: one scalar base and 32-bit offsets
   const uint8_t* qb = a.q + (int64_t)expert * a.M * (K / 2);
   const uint16_t* sb = a.s + (int64_t)expert * a.M * (K / G);
-  uint32_t wq[RT], ws[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int c = min(col0, ncols - WCOLS);
-    const int m = SWIGLU ? (t & 1) * half + c + 16 * (t >> 1) : c + 16 * t;
-    wq[t] = (uint32_t)(m + r16) * (uint32_t)(K / 2);
-    ws[t] = (uint32_t)(m + r16) * (uint32_t)(K / G);
-  }
   uint32_t mask = 0x000f000fu, magic = 0x43004300u;
   asm("" : "+s"(mask));  // not constants to the compiler: see unpack8
   asm("" : "+v"(magic));
@@ -113,6 +104,18 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
     const int rows = (int)min((int64_t)T::ROWS, cnt - tile0);
     const int kc = T::chunk(rows, K);
     const int pitch = kc + 8;
+    // what depends on the lane stays inside the tile: kept over this loop (mostly one turn), it spilled
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int r16 = ln & 15, j = ln >> 4;
+    uint32_t wq[RT], ws[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int c = min(col0, ncols - WCOLS);
+      const int m = SWIGLU ? (t & 1) * half + c + 16 * (t >> 1) : c + 16 * t;
+      wq[t] = (uint32_t)(m + r16) * (uint32_t)(K / 2);
+      ws[t] = (uint32_t)(m + r16) * (uint32_t)(K / G);
+    }
     __syncthreads();  // the previous tile's LDS reads are over
     if (tid < rows) {
       int64_t r = row0 + tile0 + tid;
@@ -166,18 +169,40 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
     load(kw * BATCH);
     for (int c0 = 0; c0 < K; c0 += kc) {
       __syncthreads();  // src_rows is written; the previous chunk's reads are over
-      // stage rows x kc activations (zeros past K), values 0 4 1 5 2 6 3 7 of every eight
-      const int pieces = kc / 8;
-      for (int c = tid; c < rows * pieces; c += 256) {
-        const int r = c / pieces, kk = (c % pieces) * 8;
-        u32x4 v = {0, 0, 0, 0};
-        if (c0 + kk < K) v = *(const u32x4*)(a.x + (int64_t)src_rows[r] * K + c0 + kk);
-        u32x4 w;
-        w[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100);
-        w[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302);
-        w[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100);
-        w[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302);
-        *(u32x4*)(xs + r * pitch + kk) = w;
+      // stage rows x kc activations (zeros past K), values 0 4 1 5 2 6 3 7 of every eight: a wave takes 512 of one
+      // row at a time (its row address is scalar), four of these loads ahead of their writes
+      const int runs = (kc + 511) / 512;
+      int r = 0, run = wave;
+      auto settle = [&]() {
+        while (run >= runs) {
+          run -= runs;
+          ++r;
+        }
+      };
+      for (settle(); r < rows;) {
+        u32x4 v[4];
+        int to[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int kk = run * 512 + ln * 8;
+          to[u] = r < rows && kk < kc ? r * pitch + kk : -1;
+          v[u] = u32x4{0, 0, 0, 0};
+          if (r < rows) {
+            const uint16_t* xr = a.x + (int64_t)__builtin_amdgcn_readfirstlane(src_rows[r]) * K + c0;
+            if (kk < kc && c0 + kk < K) v[u] = *(const u32x4*)(xr + kk);
+          }
+          run += 4;
+          settle();
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          u32x4 w;
+          w[0] = __builtin_amdgcn_perm(v[u][2], v[u][0], 0x05040100);
+          w[1] = __builtin_amdgcn_perm(v[u][2], v[u][0], 0x07060302);
+          w[2] = __builtin_amdgcn_perm(v[u][3], v[u][1], 0x05040100);
+          w[3] = __builtin_amdgcn_perm(v[u][3], v[u][1], 0x07060302);
+          if (to[u] >= 0) *(u32x4*)(xs + to[u]) = w;
+        }
       }
       __syncthreads();
       for (int b0 = kw * BATCH; b0 < kc && c0 + b0 < K; b0 += T::STEP) {
@@ -242,7 +267,7 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
     if (KS > 1) {
       constexpr int PER = TT * RT * 4;
       float* red = (float*)xs;  // [4 waves][PER][64 lanes]
-      static_assert(4 * PER * 64 * 4 <= T::LDS_ELEMS * 2, "the partial sums fit the activations' space");
+      static_assert(KS == 1 || 4 * PER * 64 * 4 <= T::LDS_ELEMS * 2, "the partial sums fit the activations' space");
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < TT; ++i)
