@@ -8,6 +8,7 @@ without the built library every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -156,13 +157,13 @@ def _ptr(t, name, dtype=None, shape=None, required=True):
         return None
     import torch
 
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -171,7 +172,8 @@ def _stream(stream):
     import torch
 
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object: a third of the time
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -375,16 +377,24 @@ def _tensor_dtype(t, name) -> int:
     return MOE_F32 if t.dtype == torch.float32 else MOE_BF16
 
 
+_NO_CHANGE = contextlib.nullcontext()
+
+
 def _same_device(what, *tensors):
     """The tensors' one device, made the current one for the launch (and its current stream the default)."""
     import torch
 
-    devices = {t.device for t in tensors if t is not None}
-    if any(d.type != "cuda" for d in devices):
-        raise TypeError(f"{what}: every tensor must be a device tensor")
-    if len(devices) != 1:
-        raise ValueError(f"{what}: tensors on more than one device: {sorted(map(str, devices))}")
-    return torch.cuda.device(devices.pop())
+    index = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise TypeError(f"{what}: every tensor must be a device tensor")
+        i = t.get_device()
+        if index is not None and i != index:
+            raise ValueError(f"{what}: tensors on more than one device: {index} and {i}")
+        index = i
+    return _NO_CHANGE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
 def _ws(workspace):

@@ -142,11 +142,9 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
         const int k = min(k0 + p * SEG + j * 32, K - 32);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          // one row tile per expert: the bytes are used once; more of them share the weights in L2
-          if (TT == 1)
-            q[t][p] = __builtin_nontemporal_load((const u32x4*)(qb + (wq[t] + (uint32_t)(k >> 1))));
-          else
-            q[t][p] = *(const u32x4*)(qb + (wq[t] + (uint32_t)(k >> 1)));
+          // (not non-temporal: a load takes half of each row's line, and with the hint the line was fetched again
+          // for the other half: 32 tokens over 256 experts 451 -> 479 us, one token 20 -> 24 us)
+          q[t][p] = *(const u32x4*)(qb + (wq[t] + (uint32_t)(k >> 1)));
         }
       }
       if (k0 + BATCH <= K) {  // the wave's scales of the batch lie together: wide loads
@@ -359,11 +357,30 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ w, 
 
 }  // namespace
 
+// Which form runs, by the average rows per expert r and the blocks a form makes (256 CUs). Measured, us, on
+// dense 12,288 -> 5,120 (groups of 64), dense 5,120 -> 24,576 and 256 experts 6,144 -> 4,096 with eight rows a
+// token (SwiGLU, groups of 128 and 32):
+//   narrow, 16 rows, k over four waves      1 / 64 / 128 rows: 18 / 63 / 104 | 22 / 91 / 177 | 32 tokens: 467
+//   middle, 32 rows, k over two waves       29 / 84 / 93                     | 20 / 51 / 95  | 462
+//   wide, 64 or 48 rows, all of k per wave  98 / 185 / 183                   | 46 / 89 / 91  | 675
+// The narrow form reads the activations most often but makes the most and shortest blocks: it wins while the
+// middle form makes fewer than one block per CU. The wide form shares each unpacked weight among 48 or 64 rows:
+// it wins from 24 rows per expert on (256 experts, 512 / 1,024 tokens: middle 1,203 / 1,756, wide 1,297 /
+// 1,622) once it makes blocks for three quarters of the CUs (512 rows, 12,288 -> 5,120: 202 against 194).
+// Of its two heights a dense product takes the one whose last round of blocks leaves less idle (1,021 rows,
+// 12,288 -> 5,120: 298 with 64 rows, 257 with 48; 2,048 rows, 5,120 -> 24,576: 739 and 762).
 hipError_t launch_qlinear(const QuantArgs& a, hipStream_t s) {
-  if (a.R <= (int64_t)16 * a.E) return launch_group<QTile<1, 4, 2, 2, 16384, 4>>(a, s);
-  const int64_t wide_blocks = (a.M + 255) / 256 * ((a.R + 63) / 64);
-  if (wide_blocks < 128) return launch_group<QTile<4, 4, 2, 1, 32768, 2>>(a, s);
-  return launch_group<QTile<4, 1, 4, 1, 32768, 2>>(a, s);
+  constexpr int64_t kCus = 256;
+  auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  const int64_t r = up(a.R, a.E);
+  const int64_t middle_blocks = up(a.M, 64) * a.E * up(r, 32), wide_blocks = up(a.M, 256) * a.E * up(r, 64);
+  if (r >= 24 && wide_blocks * 4 >= kCus * 3) {
+    const int64_t cost64 = up(wide_blocks, kCus) * 4, cost48 = up(up(a.M, 256) * up(r, 48), kCus) * 3;
+    if (a.E == 1 && cost48 < cost64) return launch_group<QTile<3, 1, 4, 1, 24576, 2>>(a, s);
+    return launch_group<QTile<4, 1, 4, 1, 32768, 2>>(a, s);
+  }
+  if (middle_blocks >= kCus) return launch_group<QTile<2, 2, 2, 2, 16384, 3>>(a, s);
+  return launch_group<QTile<1, 4, 2, 2, 16384, 4>>(a, s);
 }
 
 hipError_t launch_quantize(int dtype, const void* w, int64_t rows, int K, int group, uint8_t* q, uint16_t* s,
