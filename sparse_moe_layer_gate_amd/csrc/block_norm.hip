@@ -11,7 +11,9 @@
 //
 // Everything between the loads and the stores is float32. Both passes are bound by HBM: each row is read
 // once into registers (eight consecutive features per thread and pass over the row), so the sums and the
-// second use of a row cost no second read.
+// second use of a row cost no second read. Rows come straight from the kernel before, so the loads keep the
+// default policy and may hit the last-level cache (8,191 x 5,120 forward 72 us with non-temporal loads, 61
+// without); the stores are non-temporal where nothing reads them soon (61 against 75).
 #include <hip/hip_runtime.h>
 
 #include "moe_internal.h"
@@ -62,9 +64,9 @@ __global__ __launch_bounds__(1024) void norm_forward(NormArgs<T> p) {
   for (int v = 0; v < VPT; ++v) {
     const int c = (threadIdx.x + v * blockDim.x) * 8;
     if (c >= p.D) continue;
-    const Raw8<T> rh = raw_load8<true>(p.h + n * p.D + c);
+    const Raw8<T> rh = raw_load8(p.h + n * p.D + c);
     if (POST) {
-      const Raw8<T> ro = raw_load8<true>(p.o + n * p.D + c);
+      const Raw8<T> ro = raw_load8(p.o + n * p.D + c);
       if (p.w_post) rw[v] = raw_load8(p.w_post + c);
       if (gate) rg[v] = raw_load8(gate + c);
       if (PRE) rp[v] = raw_load8(p.w_pre + c);
@@ -131,8 +133,8 @@ __global__ __launch_bounds__(1024) void norm_forward(NormArgs<T> p) {
 // to one row of the partial arrays, which norm_reduce adds in block order (no atomics: the same inputs
 // give the same bits). With gate rows of no more than a run, a run holds whole gate groups and dgate is
 // written when a group ends; otherwise a run lies inside one group.
-template <typename T, int VPT, bool POST, bool PRE>
-__global__ __launch_bounds__(1024) void norm_backward(NormArgs<T> p) {
+template <typename T, int VPT, int MAXT, bool POST, bool PRE>
+__global__ __launch_bounds__(MAXT) void norm_backward(NormArgs<T> p) {
   __shared__ float buf0[2][16][3], buf1[16][1];
   const int waves = blockDim.x >> 6;
   const float inv_d = 1.0f / (float)p.D;
@@ -156,34 +158,68 @@ __global__ __launch_bounds__(1024) void norm_backward(NormArgs<T> p) {
       if (PRE) ap[v][i] = 0.f;
     }
   const bool norm_o = POST && p.w_post;
-  for (int n = first; n < last; ++n) {
-    const T* gate = POST && p.gate ? p.gate + (int64_t)(n / p.gate_rows) * p.D : nullptr;
-    float h[PRE ? VPT : 1][8], t[PRE ? VPT : 1][8], o[POST ? VPT : 1][8], d[VPT][8];
-    float s[3] = {0.f, 0.f, 0.f};
+  // the weights of this thread's features, and the current gate row's
+  Raw8<T> rwp[PRE ? VPT : 1], rwo[POST ? VPT : 1], rg[POST ? VPT : 1];
+  // the next row's pieces: its loads run under this row's sums (28% of the pass waited for them otherwise)
+  Raw8<T> nd[VPT], nh[PRE ? VPT : 1], nt[PRE ? VPT : 1], no[POST ? VPT : 1];
+  auto fetch = [&](int n) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (threadIdx.x + v * blockDim.x) * 8;
       if (c >= p.D) continue;
       const int64_t at = (int64_t)n * p.D + c;
+      if (p.dh_out) nd[v] = raw_load8(p.dh_out + at);
+      if (PRE) {
+        nh[v] = raw_load8(p.h + at);
+        nt[v] = raw_load8(p.du + at);
+      }
+      if (POST) no[v] = raw_load8(p.o + at);
+    }
+  };
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int c = (threadIdx.x + v * blockDim.x) * 8;
+    if (c >= p.D) continue;
+    if (PRE) rwp[v] = raw_load8(p.w_pre + c);
+    if (norm_o) rwo[v] = raw_load8(p.w_post + c);
+  }
+  if (first < last) fetch(first);
+  int gate_row = -1;
+  for (int n = first; n < last; ++n) {
+    float h[PRE ? VPT : 1][8], t[PRE ? VPT : 1][8], o[POST ? VPT : 1][8], d[VPT][8];
+    float s[3] = {0.f, 0.f, 0.f};
+    if (POST && p.gate && n / p.gate_rows != gate_row) {
+      gate_row = n / p.gate_rows;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = (threadIdx.x + v * blockDim.x) * 8;
+        if (c < p.D) rg[v] = raw_load8(p.gate + (int64_t)gate_row * p.D + c);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = (threadIdx.x + v * blockDim.x) * 8;
+      if (c >= p.D) continue;
       if (p.dh_out)
-        widen8(raw_load8<true>(p.dh_out + at), d[v]);
+        widen8(nd[v], d[v]);
       else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[v][i] = 0.f;
       }
       if (PRE) {
-        widen8(raw_load8<true>(p.h + at), h[v]);
-        widen8(raw_load8<true>(p.du + at), t[v]);
+        widen8(nh[v], h[v]);
+        widen8(nt[v], t[v]);
       }
-      if (POST) widen8(raw_load8<true>(p.o + at), o[v]);
+      if (POST) widen8(no[v], o[v]);
     }
+    if (n + 1 < last) fetch(n + 1);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (threadIdx.x + v * blockDim.x) * 8;
       if (c >= p.D) continue;
       if (PRE) {
         float w[8];
-        widen8(raw_load8(p.w_pre + c), w);
+        widen8(rwp[v], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           s[0] += h[v][i] * h[v][i];
@@ -206,7 +242,7 @@ __global__ __launch_bounds__(1024) void norm_backward(NormArgs<T> p) {
       if (c >= p.D) continue;
       if (PRE) {
         float w[8];
-        widen8(raw_load8(p.w_pre + c), w);
+        widen8(rwp[v], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           ap[v][i] += t[v][i] * (h[v][i] * rh);
@@ -221,8 +257,9 @@ __global__ __launch_bounds__(1024) void norm_backward(NormArgs<T> p) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) out[i] = p.a * d[v][i];
       raw_store8(p.dh + (int64_t)n * p.D + c, out);
-      if (gate) widen8(raw_load8(gate + c), g);
-      if (norm_o) widen8(raw_load8(p.w_post + c), w);
+      const bool gate = p.gate != nullptr;
+      if (gate) widen8(rg[v], g);
+      if (norm_o) widen8(rwo[v], w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float m = o[v][i] * ro;
@@ -265,50 +302,55 @@ __global__ __launch_bounds__(1024) void norm_backward(NormArgs<T> p) {
   }
 }
 
-// Sums of the partial rows: 64 features per block, 16 row lanes of 64 threads, then the lanes in order.
+// Sums of the partial rows: 32 features per block, 32 row lanes, eight rows of a lane in flight, then the lanes
+// in order.
 struct ReduceJob {
   const float* src;  // first partial row of group 0
   float* dst;        // [groups, D]
   int64_t rows;      // partial rows per group
   int64_t groups;
 };
+// Blocks of the backward pass have at most 512 threads (two pieces per thread from 4,096 features on): with up
+// to 1,024, the register budget of 128 spilled (4,096 x 4,096: 68 -> 63 us). Rows of more than 8,192 features
+// still take 1,024.
+constexpr int kBackwardThreads = 512;
 struct ReduceArgs {
   ReduceJob job[3];
   int D;
 };
 __global__ __launch_bounds__(1024) void norm_reduce(ReduceArgs a) {
-  __shared__ float acc[16][64];
+  __shared__ float acc[32][33];
   int64_t g = blockIdx.y;
   int which = 0;
   while (which < 2 && g >= a.job[which].groups) g -= a.job[which++].groups;
   const ReduceJob& job = which == 0 ? a.job[0] : which == 1 ? a.job[1] : a.job[2];
   if (g >= job.groups) return;
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63), lane = threadIdx.x >> 6;
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), lane = threadIdx.x >> 5;
   const float* src = job.src + g * job.rows * a.D + col;
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t r = lane; r < job.rows; r += 64) {
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t r = lane; r < job.rows; r += 256) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (r + 16 * i < job.rows) s[i] += src[(r + 16 * i) * a.D];
+    for (int i = 0; i < 8; ++i)
+      if (r + 32 * i < job.rows) s[i] += src[(r + 32 * i) * a.D];
   }
-  acc[lane][threadIdx.x & 63] = (s[0] + s[1]) + (s[2] + s[3]);
+  acc[lane][threadIdx.x & 31] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
   __syncthreads();
   if (lane == 0) {
     float t = 0.f;
 #pragma unroll
-    for (int l = 0; l < 16; ++l) t += acc[l][threadIdx.x];
+    for (int l = 0; l < 32; ++l) t += acc[l][threadIdx.x];
     job.dst[g * a.D + col] = t;
   }
 }
 
+// Threads of a block and pieces per thread: one piece each while the block has at most `limit` threads, else two.
 struct Shape {
   int threads, vpt;
 };
-Shape shape_of(int D) {
-  int t = (D / 8 + 63) / 64 * 64;
-  if (t <= 1024) return {t, 1};
-  t = (D / 16 + 63) / 64 * 64;
-  return {t, 2};
+Shape shape_of(int D, int limit) {
+  const int t = (D / 8 + 63) / 64 * 64;
+  if (t <= limit) return {t, 1};
+  return {(D / 16 + 63) / 64 * 64, 2};
 }
 
 template <typename T, int VPT>
@@ -323,15 +365,15 @@ hipError_t forward_vpt(const NormArgs<T>& p, int threads, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int VPT>
+template <typename T, int VPT, int MAXT>
 hipError_t backward_vpt(const NormArgs<T>& p, int threads, hipStream_t s) {
   const dim3 grid((unsigned)p.nblocks), block(threads);
   if (p.o && p.w_pre)
-    hipLaunchKernelGGL((norm_backward<T, VPT, true, true>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((norm_backward<T, VPT, MAXT, true, true>), grid, block, 0, s, p);
   else if (p.o)
-    hipLaunchKernelGGL((norm_backward<T, VPT, true, false>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((norm_backward<T, VPT, MAXT, true, false>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((norm_backward<T, VPT, false, true>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((norm_backward<T, VPT, MAXT, false, true>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -353,7 +395,7 @@ hipError_t forward_t(const NormCall& c, hipStream_t s) {
   p.w_pre = (const T*)c.w_pre;
   p.h_out = (T*)c.h_out;
   p.u = (T*)c.u;
-  const Shape sh = shape_of(c.D);
+  const Shape sh = shape_of(c.D, 1024);
   return sh.vpt == 1 ? forward_vpt<T, 1>(p, sh.threads, s) : forward_vpt<T, 2>(p, sh.threads, s);
 }
 
@@ -381,8 +423,10 @@ hipError_t backward_t(const NormCall& c, hipStream_t s) {
   p.chunks_per_group = (int)pl.chunks_per_group;
   p.nblocks = pl.nblocks;
   p.want = (c.dw_post ? 1 : 0) | (c.dw_pre ? 2 : 0) | (c.dgate ? 4 : 0);
-  const Shape sh = shape_of(c.D);
-  const hipError_t e = sh.vpt == 1 ? backward_vpt<T, 1>(p, sh.threads, s) : backward_vpt<T, 2>(p, sh.threads, s);
+  const Shape sh = shape_of(c.D, kBackwardThreads);
+  const hipError_t e = sh.vpt == 1 ? backward_vpt<T, 1, kBackwardThreads>(p, sh.threads, s)
+                       : sh.threads <= kBackwardThreads ? backward_vpt<T, 2, kBackwardThreads>(p, sh.threads, s)
+                                                        : backward_vpt<T, 2, 1024>(p, sh.threads, s);
   if (e != hipSuccess) return e;
   ReduceArgs r{};
   r.D = c.D;
@@ -393,17 +437,21 @@ hipError_t backward_t(const NormCall& c, hipStream_t s) {
     groups += (r.job[2] = ReduceJob{p.part + 2 * pl.nblocks * c.D, c.dgate, pl.chunks_per_group,
                                     pl.nblocks / pl.chunks_per_group}).groups;
   if (groups == 0) return hipSuccess;
-  hipLaunchKernelGGL(norm_reduce, dim3(c.D / 64, (unsigned)groups), dim3(1024), 0, s, r);
+  hipLaunchKernelGGL(norm_reduce, dim3(c.D / 32, (unsigned)groups), dim3(1024), 0, s, r);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Rows per block of the backward pass: enough blocks to fill the chip, few enough that the partial rows
-// (three of D floats per block) stay small against the rows themselves.
+// Runs of the backward pass: eight waves per CU (256 CUs). More runs mean more partial rows (three of D floats
+// per run) to write and add: 4,096 x 4,096 with 256 / 512 runs 51 / 59 us.
+int64_t norm_runs(int D) {
+  const int threads = shape_of(D, kBackwardThreads).threads;
+  return threads >= 512 ? 256 : 256 * (512 / threads);
+}
+
 NormPlan norm_plan(int64_t N, int D, int64_t gate_rows) {
-  constexpr int64_t kBlocks = 512;
-  (void)D;
+  const int64_t kBlocks = norm_runs(D);
   NormPlan p{};
   int64_t c = (N + kBlocks - 1) / kBlocks;
   if (c < 1) c = 1;

@@ -250,6 +250,7 @@ struct NormPlan {
   int64_t chunks_per_group;  // > 0: the blocks of one gate group; 0: blocks hold whole groups (or no gate)
   int64_t nblocks;
 };
+int64_t norm_runs(int D);  // most runs of rows without a gate
 NormPlan norm_plan(int64_t N, int D, int64_t gate_rows);  // gate_rows 0: no gate
 hipError_t launch_norm_forward(int dtype, const NormCall& c, hipStream_t s);
 hipError_t launch_norm_backward(int dtype, const NormCall& c, hipStream_t s);

@@ -30,9 +30,13 @@ moe_status check_norm(int64_t N, int32_t D, int32_t dtype, float eps, float a) {
   return MOE_OK;
 }
 
-// Most blocks norm_plan can choose for at most N rows: 512 runs, or with a gate the runs of ceil(N / T)
-// groups, at most N / c + N / T + T / c + 1 of them with N / c <= 512, T <= N and N / T < N / c.
-int64_t norm_blocks_bound(int64_t N, bool gate) { return gate ? std::min<int64_t>(2 * N, 1537) : std::min<int64_t>(N, 512); }
+// Most blocks norm_plan can choose for at most N rows, with B = norm_runs(D) and c = ceil(N / B) rows a run: B
+// without a gate or with whole gate groups in a run; otherwise (T > c) ceil(N / T) groups of ceil(T / c) runs, at
+// most N / c + N / T + T / c + 1, each term at most B; and no more than 2 N, reached with c = 1.
+int64_t norm_blocks_bound(int64_t N, int D, bool gate) {
+  const int64_t B = norm_runs(D);
+  return gate ? std::min<int64_t>(2 * N, 3 * B + 1) : std::min<int64_t>(N, B);
+}
 
 moe_status check_combine(int64_t N, int32_t k, int32_t D, int32_t dtype, int64_t R, float alpha) {
   if (N < 0 || k < 1 || D < 1 || R < 0 || !dtype_ok(dtype) || !std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
@@ -111,7 +115,7 @@ extern "C" {
 // ---- block norms ----
 size_t moe_block_norm_workspace_size(int64_t N, int32_t D, int32_t dtype, int64_t gate_rows) {
   if (check_norm(N, D, dtype, 0.f, 0.f) != MOE_OK || gate_rows < 0) return 0;
-  return sizeof(float) * (gate_rows > 0 ? 3 : 2) * (size_t)norm_blocks_bound(N, gate_rows > 0) * D;
+  return sizeof(float) * (gate_rows > 0 ? 3 : 2) * (size_t)norm_blocks_bound(N, D, gate_rows > 0) * D;
 }
 
 moe_status moe_block_norm(int64_t N, int32_t D, int32_t dtype, float eps, float residual_scale, const void* h,

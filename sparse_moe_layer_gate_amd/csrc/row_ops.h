@@ -24,14 +24,8 @@ struct Raw8<float> {
   f32x4v a, b;
 };
 
-// NT: the bytes are used once (non-temporal).
-template <bool NT = false>
-__device__ inline Raw8<uint16_t> raw_load8(const uint16_t* p) {
-  return Raw8<uint16_t>{NT ? __builtin_nontemporal_load((const u32x4*)p) : *(const u32x4*)p};
-}
-template <bool NT = false>
+__device__ inline Raw8<uint16_t> raw_load8(const uint16_t* p) { return Raw8<uint16_t>{*(const u32x4*)p}; }
 __device__ inline Raw8<float> raw_load8(const float* p) {
-  if (NT) return Raw8<float>{__builtin_nontemporal_load((const f32x4v*)p), __builtin_nontemporal_load((const f32x4v*)p + 1)};
   return Raw8<float>{*(const f32x4v*)p, *((const f32x4v*)p + 1)};
 }
 __device__ inline void widen8(const Raw8<uint16_t>& r, float* f) {
@@ -56,6 +50,7 @@ __device__ inline uint32_t bf16_pair(float lo, float hi) {
   v[1] = (__bf16)hi;
   return __builtin_bit_cast(uint32_t, v);
 }
+// NT: non-temporal, for bytes that nothing reads soon.
 template <bool NT = true>
 __device__ inline void raw_store8(uint16_t* p, const float* f) {
   u32x4 v;
