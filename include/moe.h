@@ -295,8 +295,7 @@ moe_status moe_combine_backward(int64_t N, int32_t k, int32_t D, int32_t dtype, 
  *           sorted_pair with index_div = k gathers tokens), or r when row_index is NULL (x_rows >= R)
  *   offsets [E + 1] int32 on the device, ascending, as moe_dispatch writes them. Rows outside
  *           [offsets[0], offsets[E]) belong to no expert: no output row of theirs is written.
- *   workspace: at least moe_grouped_workspace_size(E, R, dtype) bytes (wgrad without row_index: may be NULL).
- *           The size never falls as R grows.
+ *   workspace: at least moe_grouped_workspace_size(E, R, dtype) bytes. The size never falls as R grows.
  * dx holds one row per grouped row: the gradient of a gathered token is moe_combine of its rows with
  * topk_w == NULL. Offsets and indices are read on the device and kept in range there: offsets outside [0, R]
  * or out of order and indices outside [0, x_rows * index_div) give unspecified values, never an access

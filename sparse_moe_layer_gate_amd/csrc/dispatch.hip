@@ -324,7 +324,8 @@ __device__ int block_running_max(int v, int* wmax) {
 __global__ __launch_bounds__(512) void offset_lists_kernel(const int32_t* __restrict__ offsets, int E, int64_t R,
                                                            TileSpec t0, TileSpec t1, int pick_rows,
                                                            const int32_t* __restrict__ row_index, int32_t div,
-                                                           int64_t x_rows, int32_t* __restrict__ src_row) {
+                                                           int64_t x_rows, int32_t* __restrict__ src_row,
+                                                           int32_t* __restrict__ row_range) {
   if (blockIdx.x > 0) {
     const int64_t r = (int64_t)(blockIdx.x - 1) * 512 + threadIdx.x;
     if (r < R) src_row[r] = (int32_t)min(max((int64_t)(row_index[r] / div), (int64_t)0), x_rows - 1);
@@ -338,6 +339,8 @@ __global__ __launch_bounds__(512) void offset_lists_kernel(const int32_t* __rest
   const int hi = e < E ? (int)min(max((int64_t)offsets[e + 1], (int64_t)0), R) : 0;
   const int start = block_running_max(lo, wsum);
   const int cnt = e < E ? max(hi - start, 0) : 0;
+  if (row_range && e == 0) row_range[0] = lo;
+  if (row_range && e == E - 1) row_range[1] = max(start, hi);  // the experts' ranges lie end to end
   if (pick_rows > 0 && cnt > 0) atomicMax(&max_cnt, cnt);  // read after the lists' barriers
   if (t0.tiles) build_tiles(t0, e < E, e, cnt, start, 0, 0, wsum);
   if (t1.tiles) build_tiles(t1, e < E, e, cnt, start, 0, 0, wsum);
@@ -365,11 +368,11 @@ hipError_t launch_fill2_i32(int32_t* p, int64_t n, int32_t* q, int64_t m, int32_
 
 hipError_t launch_offset_lists(const int32_t* offsets, int E, int64_t R, TileSpec t0, TileSpec t1, int pick_rows,
                                const int32_t* row_index, int32_t div, int64_t x_rows, int32_t* src_row,
-                               hipStream_t s) {
+                               int32_t* row_range, hipStream_t s) {
   if (E > 512) return hipErrorInvalidValue;
   const int64_t blocks = 1 + (row_index ? (R + 511) / 512 : 0);
   hipLaunchKernelGGL(offset_lists_kernel, dim3((unsigned)blocks), dim3(512), 0, s, offsets, E, R, t0, t1, pick_rows,
-                     row_index, div, x_rows, src_row);
+                     row_index, div, x_rows, src_row, row_range);
   return hipGetLastError();
 }
 

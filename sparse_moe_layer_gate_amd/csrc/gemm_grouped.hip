@@ -42,10 +42,11 @@ __global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tile
   __shared__ float sa[BT][PITCH], sb[BT][PITCH];
   const int M = a.M, K = a.K;
   int64_t row0;   // first grouped row of the tile (fwd, dgrad) or of the expert (wgrad)
-  int expert, rows, i0 = 0, j0;
+  int expert, rows, i0 = 0, j0, split;
   if (MODE == GM_WGRAD) {
     const int mt = (M + 127) / 128;
-    const int64_t b = blockIdx.x;
+    const int64_t b = blockIdx.x / a.splits;
+    split = (int)(blockIdx.x % a.splits);
     j0 = (int)(b % col_tiles) * 128;
     i0 = (int)(b / col_tiles % mt) * 128;
     expert = (int)(b / col_tiles / mt);
@@ -54,8 +55,10 @@ __global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tile
     row0 = lo;
     rows = (int)(hi - lo);
   } else {
-    const int64_t L = xcd_logical_block((int64_t)*a.n_tiles * col_tiles);
+    int64_t L = xcd_logical_block((int64_t)*a.n_tiles * col_tiles * a.splits);
     if (L < 0) return;
+    split = (int)(L % a.splits);
+    L /= a.splits;
     const Tile tile = a.tiles[L / col_tiles];
     j0 = (int)(L % col_tiles) * 128;
     row0 = tile.row_start;
@@ -64,7 +67,10 @@ __global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tile
     if (rows <= 0) return;
   }
   const int ni = MODE == GM_WGRAD ? M : rows, nj = MODE == GM_FWD ? M : K;
-  const int nt = MODE == GM_FWD ? K : MODE == GM_DGRAD ? M : rows;
+  const int nt_all = MODE == GM_FWD ? K : MODE == GM_DGRAD ? M : rows;
+  // this part of the reduction (the last ones may be empty: they write zeros)
+  const int part = (nt_all + a.splits * BT - 1) / (a.splits * BT) * BT;
+  const int nt0 = min(split * part, nt_all), nt = min(nt0 + part, nt_all);
   const float* A = (const float*)a.a;
   const float* B = (const float*)a.b;
   const int64_t wbase = (int64_t)expert * M * K;
@@ -108,8 +114,8 @@ __global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tile
       for (int u = 0; u < 8; ++u) s[t + u][i] = r[u];
     }
   };
-  if (nt > 0) load(0);
-  for (int t0 = 0; t0 < nt; t0 += BT) {
+  if (nt > nt0) load(nt0);
+  for (int t0 = nt0; t0 < nt; t0 += BT) {
     __syncthreads();
     put(sa, A_T, ai, at, ra);
     put(sb, B_T, bj, bt, rb);
@@ -128,7 +134,8 @@ __global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tile
         for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[j], acc[i][j], 0, 0, 0);
     }
   }
-  float* out = (float*)a.out;
+  const int64_t part_elems = MODE == GM_WGRAD ? (int64_t)a.E * M * K : a.R * nj;
+  float* out = a.splits > 1 ? a.part + split * part_elems : (float*)a.out;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -385,8 +392,26 @@ __device__ __attribute__((always_inline)) inline void store_dgrad(char* lds, con
   }
 }
 
-// One 256 x 256 tile of dx: rows of `tile`, columns from col0.
-__device__ __forceinline__ void dgrad_block(const GradArgs& a, const Tile tile, int col0, char* lds) {
+// Float32 results of one wave straight to a part of a split reduction: four columns a lane.
+__device__ __attribute__((always_inline)) inline void store_part(const f32x16 (&acc)[2][4], int lane, int rows, int cols,
+                                                                 float* out, int64_t ld) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = i * 32 + (lane & 31);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = j * 32 + 8 * q + 4 * (lane >> 5);
+        if (row < rows && col < cols)
+          *(f32x4*)(out + row * ld + col) =
+              f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      }
+  }
+}
+
+// One 256 x 256 tile of dx: rows of `tile`, columns from col0, part `split` of the reduction.
+__device__ __forceinline__ void dgrad_block(const GradArgs& a, const Tile tile, int col0, int split, char* lds) {
   using T = GradTile<GM_DGRAD>;
   const int t = threadIdx.x;
   int lane = t & 63;
@@ -395,8 +420,10 @@ __device__ __forceinline__ void dgrad_block(const GradArgs& a, const Tile tile, 
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int m0 = (wave & 3) * 64, n0 = (wave >> 2) * 128;
   const int M = a.M, K = a.K;
-  const uint16_t* abase = (const uint16_t*)a.a + (int64_t)tile.row_start * M;
-  const uint16_t* bbase = (const uint16_t*)a.b + (int64_t)tile.expert * M * K;
+  // this part's steps (never none: grouped_splits)
+  const int all = M / T::BK, per = (all + a.splits - 1) / a.splits, k0 = split * per, nk = min(per, all - k0);
+  const uint16_t* abase = (const uint16_t*)a.a + (int64_t)tile.row_start * M + k0 * T::BK;
+  const uint16_t* bbase = (const uint16_t*)a.b + ((int64_t)tile.expert * M + k0 * T::BK) * K;
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)abase, (short)0, -1, kRawBufferWord3);
   const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)bbase, (short)0, -1, kRawBufferWord3);
   uint32_t oa[T::NLA], ob[T::NLB];
@@ -435,13 +462,18 @@ __device__ __forceinline__ void dgrad_block(const GradArgs& a, const Tile tile, 
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  const int live = tile.rows - m0, nk = M / T::BK;
+  const int live = tile.rows - m0;
   if (live > 32)
     dgrad_loop<2>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
   else if (live > 0)
     dgrad_loop<1>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
   else
     dgrad_loop<0>(lds, issue_a, issue_b, acc, nk, lane, m0, n0);
+  if (a.splits > 1) {
+    store_part(acc, lane, max(0, min(64, live)), min(128, K - col0 - n0),
+               a.part + (split * a.R + tile.row_start + m0) * K + col0 + n0, K);
+    return;
+  }
   // the loop ended on a barrier after the last operand read
   uint16_t* out = (uint16_t*)a.out + ((int64_t)tile.row_start + m0) * K + col0 + n0;
   store_dgrad(lds, acc, wave, lane, max(0, min(64, live)), min(128, K - col0 - n0), out, K);
@@ -463,7 +495,7 @@ __global__ __launch_bounds__(512, 1) void grouped_dgrad_bf16(GradArgs a, int nco
   using T = GradTile<GM_DGRAD>;
   __shared__ __attribute__((aligned(1024))) char lds[T::RING];
   int* claim = (int*)(lds + T::RING - 4);  // outside the staged outputs; written when the loop's reads are over
-  const int64_t n_tiles = *a.n_tiles, nvalid = n_tiles * ncol, q = nvalid >> 3, r = nvalid & 7;
+  const int64_t n_tiles = *a.n_tiles, nvalid = n_tiles * ncol * a.splits, q = nvalid >> 3, r = nvalid & 7;
   const int x = blockIdx.x & 7;
   for (int v = 0; v < 8; ++v) {
     const int y = (x + v) & 7;
@@ -476,9 +508,9 @@ __global__ __launch_bounds__(512, 1) void grouped_dgrad_bf16(GradArgs a, int nco
       if (j >= len) break;
       int64_t tid;
       int ct;
-      grad_raster<2, 16>(start + j, n_tiles, ncol, tid, ct);
+      grad_raster<2, 16>((start + j) / a.splits, n_tiles, ncol, tid, ct);
       const Tile tile = a.tiles[tid];
-      if (tile.rows > 0) dgrad_block(a, tile, ct * T::BN, lds);
+      if (tile.rows > 0) dgrad_block(a, tile, ct * T::BN, (int)((start + j) % a.splits), lds);
       __syncthreads();  // every wave's stores have read the LDS
     }
   }
@@ -495,13 +527,13 @@ __global__ __launch_bounds__(512, 1) void grouped_dgrad_bf16(GradArgs a, int nco
 // Rows past the expert's are read as zeros: dy through the descriptor's range (the step's rows of dy and nothing
 // behind them), gathered x through an offset past the range.
 struct WgradTile {
-  int expert, i0, j0, cnt, nk;
+  int expert, split, i0, j0, cnt, nk;
   int64_t row0;
 };
-template <bool GATHER>
+template <bool GATHER, bool SPLIT>
 __global__ __launch_bounds__(512, 1) void grouped_wgrad_bf16(GradArgs a, int mt, int kt_tiles) {
   using T = GradTile<GM_WGRAD>;
-  constexpr int S = T::SA, PER = T::NLA + T::NLB, NST = 16;  // stages, loads per step, stores per tile
+  constexpr int S = T::SA, PER = T::NLA + T::NLB, NST = SPLIT ? 32 : 16;  // stages, loads per step, stores per tile
   static_assert(T::SA == T::SB && (S & (S - 1)) == 0 && (S - 2) * PER + NST < 64, "ring indices and vmcnt");
   __shared__ __attribute__((aligned(1024))) char lds[T::RING];
   const int lane = threadIdx.x & 63;
@@ -510,12 +542,18 @@ __global__ __launch_bounds__(512, 1) void grouped_wgrad_bf16(GradArgs a, int mt,
   const int M = a.M, K = a.K;
   typedef const __attribute__((address_space(4))) int32_t* const_i32;  // scalar loads: none counts in vmcnt
   const uint32_t slots = gridDim.x >> 3, stride = gridDim.x;
-  const uint32_t per_expert = (uint32_t)(mt * kt_tiles), total = per_expert * (uint32_t)a.E;
+  const uint32_t per_expert = (uint32_t)(mt * kt_tiles);
+  const uint32_t total = per_expert * (uint32_t)a.E * (uint32_t)(SPLIT ? a.splits : 1);
   const uint32_t first = (blockIdx.x & 7) * slots + (blockIdx.x >> 3);
 
   auto decode = [&](uint32_t id) {
     WgradTile t;
     t.expert = (int)(id / per_expert);
+    t.split = 0;
+    if (SPLIT) {
+      t.split = t.expert % a.splits;
+      t.expert /= a.splits;
+    }
     // rectangles of 4 x 8 tiles, rows fastest
     const uint32_t in = id % per_expert, sg = in / (4u * kt_tiles), within = in % (4u * kt_tiles);
     const uint32_t gr = min(4u, (uint32_t)mt - sg * 4), cg = within / (gr * 8), w2 = within % (gr * 8);
@@ -524,6 +562,11 @@ __global__ __launch_bounds__(512, 1) void grouped_wgrad_bf16(GradArgs a, int mt,
     const int64_t lo = ((const_i32)a.offsets)[t.expert], hi = ((const_i32)a.offsets)[t.expert + 1];
     t.row0 = min(max(lo, (int64_t)0), a.R);
     t.cnt = (int)(min(max(hi, t.row0), a.R) - t.row0);
+    if (SPLIT) {  // this part of the expert's rows, in whole steps; perhaps none
+      const int per = (t.cnt + a.splits * T::BK - 1) / (a.splits * T::BK) * T::BK, from = min(t.split * per, t.cnt);
+      t.row0 += from;
+      t.cnt = min(per, t.cnt - from);
+    }
     t.nk = (t.cnt + T::BK - 1) / T::BK;
     return t;
   };
@@ -663,7 +706,24 @@ __global__ __launch_bounds__(512, 1) void grouped_wgrad_bf16(GradArgs a, int mt,
     const int free_st = (done + S - 1) & (S - 1);
     stored = t.i0 + m0 < M;
     mark = issued;
-    if (stored) {
+    if (SPLIT && stored) {  // float32 parts, straight from the registers
+      const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(a.part + (((int64_t)t.split * a.E + t.expert) * M + t.i0 + m0) * K), (short)0, 64 * K * 4,
+          kRawBufferWord3);
+      const int cols = K - t.j0 - n0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int row = i * 32 + (lane & 31), col = j * 32 + 8 * q + 4 * (lane >> 5);
+            const uint32_t off = col < cols ? ((uint32_t)row * (uint32_t)K + t.j0 + n0 + col) * 4 : 0xfffffff0u;
+            const f32x4 c = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, c), ro, (int)off, 0, 0);
+          }
+    }
+    if (!SPLIT && stored) {
       char* sp = lds + (wave < 4 ? free_st * T::A_BYTES + wave * 4096 : T::B_BASE + free_st * T::B_BYTES + (wave - 4) * 4096);
       const __amdgpu_buffer_rsrc_t ro = __builtin_amdgcn_make_buffer_rsrc(
           (void*)((uint16_t*)a.out + ((int64_t)t.expert * M + t.i0 + m0) * K), (short)0, 64 * K * 2, kRawBufferWord3);
@@ -720,7 +780,7 @@ int grad_cus() {
 hipError_t launch_grouped_bf16(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s) {
   if (mode == GM_DGRAD) {
     const int nc = (a.K + 255) / 256;
-    const int64_t blocks = (max_tile_count * nc + 7) / 8 * 8;
+    const int64_t blocks = (max_tile_count * nc * a.splits + 7) / 8 * 8;
     if (blocks == 0) return hipSuccess;
     if (!a.work_ctr) return hipErrorInvalidValue;
     hipLaunchKernelGGL(grouped_dgrad_bf16, dim3((unsigned)std::min<int64_t>(blocks, grad_cus())), dim3(512), 0, s, a,
@@ -729,19 +789,106 @@ hipError_t launch_grouped_bf16(GroupedMode mode, const GradArgs& a, int64_t max_
   }
   if (mode != GM_WGRAD) return hipErrorInvalidValue;
   const int mt = (a.M + 255) / 256, kt = (a.K + 255) / 256;
-  const int64_t tiles = ((int64_t)a.E * mt * kt + 7) / 8 * 8;
+  const int64_t tiles = ((int64_t)a.E * mt * kt * a.splits + 7) / 8 * 8;
   if (tiles >= (int64_t)1 << 30) return hipErrorInvalidValue;  // 32-bit tile ids, with a stride to spare
   const dim3 grid((unsigned)std::min<int64_t>(tiles, grad_cus())), block(512);
-  if (a.src_row)
-    hipLaunchKernelGGL(grouped_wgrad_bf16<true>, grid, block, 0, s, a, mt, kt);
-  else
-    hipLaunchKernelGGL(grouped_wgrad_bf16<false>, grid, block, 0, s, a, mt, kt);
+  if (a.splits > 1) {
+    if (a.src_row)
+      hipLaunchKernelGGL((grouped_wgrad_bf16<true, true>), grid, block, 0, s, a, mt, kt);
+    else
+      hipLaunchKernelGGL((grouped_wgrad_bf16<false, true>), grid, block, 0, s, a, mt, kt);
+  } else if (a.src_row) {
+    hipLaunchKernelGGL((grouped_wgrad_bf16<true, false>), grid, block, 0, s, a, mt, kt);
+  } else {
+    hipLaunchKernelGGL((grouped_wgrad_bf16<false, false>), grid, block, 0, s, a, mt, kt);
+  }
   return hipGetLastError();
 }
+
+// Parts of the reduction. A call with few tiles (few rows and narrow outputs; wgrad: few experts and small
+// matrices) leaves most CUs idle while a few walk a long reduction, so it is cut until there is a block for every
+// CU (two for the smaller float32 tiles), in parts of at least four steps, as long as the parts' float32 outputs
+// fit `part_bytes`. With the tile counts known only on the device, fwd and dgrad assume the most there can be.
+int grouped_splits(GroupedMode mode, int dtype, int E, int64_t R, int M, int K, size_t part_bytes) {
+  const bool f32 = dtype == MOE_F32;
+  const int64_t bm = f32 ? kF32Rows : kGradRows, bn = f32 ? 128 : 256;
+  const int64_t target = f32 ? 512 : 256;
+  if (R == 0) return 1;
+  auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  const int64_t used = std::min<int64_t>(R, E);  // experts with rows, at most
+  int64_t items, red, step, elems;
+  if (mode == GM_WGRAD) {
+    items = (int64_t)E * up(M, bm) * up(K, bn);
+    red = up(R, used);
+    step = f32 ? 16 : 32;
+    elems = (int64_t)E * M * K;
+  } else {
+    const int64_t J = mode == GM_FWD ? M : K;
+    items = (used + R / bm) * up(J, bn);
+    red = mode == GM_FWD ? K : M;
+    step = f32 ? 16 : 64;
+    elems = R * J;
+  }
+  int64_t n = std::min(target / items, red / (4 * step));
+  n = std::min<int64_t>(n, (int64_t)(part_bytes / 4) / elems);
+  n = std::min<int64_t>(n, 32);
+  if (n < 2) return 1;
+  if (mode != GM_WGRAD) {  // equal whole steps, none of the parts empty
+    const int64_t steps = up(red, step), per = up(steps, n);
+    n = up(steps, per);
+  }
+  return (int)n;
+}
+
+namespace {
+
+// out = the sum of the parts, in order; eight elements a thread. Rows outside the grouped ones are left alone.
+template <typename T>
+__global__ __launch_bounds__(256) void grouped_join_kernel(const float* __restrict__ part, int splits, int64_t elems,
+                                                           int64_t row_elems, const int32_t* __restrict__ row_range,
+                                                           T* __restrict__ out) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  const int64_t lo = row_range ? row_range[0] * row_elems : 0, hi = row_range ? row_range[1] * row_elems : elems;
+  if (i < lo || i >= hi) return;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < splits; s0 += 4) {
+    Raw8<float> v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (s0 + u < splits) v[u] = raw_load8(part + (s0 + u) * elems + i);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (s0 + u < splits) {
+        float f[8];
+        widen8(v[u], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += f[e];
+      }
+  }
+  raw_store8<false>(out + i, acc);
+}
+
+}  // namespace
+
+hipError_t launch_grouped_join(GroupedMode mode, int dtype, const GradArgs& a, hipStream_t s) {
+  const int64_t row = mode == GM_FWD ? a.M : a.K;
+  const int64_t elems = mode == GM_WGRAD ? (int64_t)a.E * a.M * a.K : a.R * row;
+  const int64_t blocks = (elems / 8 + 255) / 256;
+  if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
+  const int32_t* range = mode == GM_WGRAD ? nullptr : a.row_range;
+  if (dtype == MOE_F32)
+    hipLaunchKernelGGL(grouped_join_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, s, a.part, a.splits, elems, row,
+                       range, (float*)a.out);
+  else
+    hipLaunchKernelGGL(grouped_join_kernel<uint16_t>, dim3((unsigned)blocks), dim3(256), 0, s, a.part, a.splits, elems,
+                       row, range, (uint16_t*)a.out);
+  return hipGetLastError();
+}
+
 hipError_t launch_grouped_f32(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s) {
   const int cols = ((mode == GM_FWD ? a.M : a.K) + 127) / 128;
   const int64_t tiles = mode == GM_WGRAD ? (int64_t)a.E * ((a.M + 127) / 128) : max_tile_count;
-  int64_t blocks = tiles * cols;
+  int64_t blocks = tiles * cols * a.splits;
   if (mode != GM_WGRAD) blocks = (blocks + 7) / 8 * 8;
   if (blocks == 0) return hipSuccess;
   if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;

@@ -257,10 +257,11 @@ hipError_t launch_norm_backward(int dtype, const NormCall& c, hipStream_t s);
 
 // ---- grouped products and their gradients ----
 // Row-tile lists of rows grouped by `offsets` [E + 1] (made monotone and kept within [0, R]), and, with
-// row_index, the source row of every grouped row, kept within [0, x_rows).
+// row_index, the source row of every grouped row, kept within [0, x_rows). row_range (or nullptr): the first grouped
+// row and the one behind the last.
 hipError_t launch_offset_lists(const int32_t* offsets, int E, int64_t R, TileSpec t0, TileSpec t1, int pick_rows,
                                const int32_t* row_index, int32_t div, int64_t x_rows, int32_t* src_row,
-                               hipStream_t s);
+                               int32_t* row_range, hipStream_t s);
 enum GroupedMode {
   GM_FWD = 0,  // y = x W^T    (float32 only: the bf16 product runs on the expert GEMMs)
   GM_DGRAD,    // dx = dy W
@@ -278,9 +279,16 @@ struct GradArgs {
   const Tile* tiles;        // fwd / dgrad
   const int32_t* n_tiles;
   int32_t* work_ctr;        // bf16 dgrad: 8 counters, zero at launch
+  // splits > 1: the reduction in that many parts, each writing its own float32 output (fwd / dgrad [R, J], wgrad
+  // [E, M, K]) into `part`; launch_grouped_join adds them in order
+  int splits;
+  float* part;
+  const int32_t* row_range;  // fwd / dgrad: first grouped row and the one behind the last
 };
 hipError_t launch_grouped_bf16(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s);
 hipError_t launch_grouped_f32(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s);
+int grouped_splits(GroupedMode mode, int dtype, int E, int64_t R, int M, int K, size_t part_bytes);
+hipError_t launch_grouped_join(GroupedMode mode, int dtype, const GradArgs& a, hipStream_t s);
 constexpr int kGradRows = 256;  // rows per tile of the bf16 dgrad list
 constexpr int kF32Rows = 128;   // rows per tile of the float32 lists
 

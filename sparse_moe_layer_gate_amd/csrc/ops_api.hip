@@ -69,7 +69,7 @@ moe_status check_source(int64_t R, int64_t x_rows, const int32_t* row_index, int
 }
 
 struct GroupedLayout {
-  size_t tiles0, tiles1, ntiles, src_row, total;
+  size_t tiles0, tiles1, ntiles, src_row, part, part_bytes, total;
   int64_t max_tiles0, max_tiles1;
   int bm0, bm1, pick;
 };
@@ -97,8 +97,11 @@ GroupedLayout grouped_layout(int32_t E, int64_t R, int32_t dtype) {
   };
   w.tiles0 = take(sizeof(Tile) * room0);
   w.tiles1 = take(f32 ? 0 : sizeof(Tile) * w.max_tiles1);
-  w.ntiles = take(sizeof(int32_t) * 20);  // two tile counts, 8 work counters per list, two hot counts
+  w.ntiles = take(sizeof(int32_t) * 22);  // two tile counts, 8 work counters per list, two hot counts, row range
   w.src_row = take(sizeof(int32_t) * R);
+  // float32 parts of a reduction that is split (grouped_splits): a call with few rows needs little of it
+  w.part_bytes = (size_t)std::min<int64_t>(R, 32) << 19;
+  w.part = take(w.part_bytes);
   w.total = o;
   return w;
 }
@@ -252,10 +255,12 @@ moe_status moe_grouped_linear(int32_t E, int64_t R, int32_t in, int32_t out, int
   const TileSpec t1{L.bm1, at<Tile>(ws, L.tiles1), ntiles + 1, small_expert_rows(dtype, L.bm1), ntiles + 10,
                     ntiles + 19};
   MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, t0, L.pick ? t1 : none, L.pick, row_index, index_div,
-                                                x_rows, src, s));
+                                                x_rows, src, ntiles + 20, s));
   if (dtype == MOE_F32) {
-    const GradArgs g{x, w, y, R, out, in, E, offsets, src, x_rows, t0.tiles, ntiles, nullptr};
+    const GradArgs g{x, w, y, R, out, in, E, offsets, src, x_rows, t0.tiles, ntiles, nullptr,
+                     grouped_splits(GM_FWD, dtype, E, R, out, in, L.part_bytes), at<float>(ws, L.part), ntiles + 20};
     MOE_TRY(ST_GROUPED_LINEAR, launch_grouped_f32(GM_FWD, g, L.max_tiles0, s));
+    if (g.splits > 1) MOE_TRY(ST_GROUPED_LINEAR, launch_grouped_join(GM_FWD, dtype, g, s));
     return MOE_OK;
   }
   // the layer's expert GEMM without its row scale; source rows are resolved already (k = 1)
@@ -289,10 +294,12 @@ moe_status moe_grouped_linear_dgrad(int32_t E, int64_t R, int32_t in, int32_t ou
   int32_t* ntiles = at<int32_t>(ws, L.ntiles);
   const TileSpec none{0, nullptr, nullptr, 0, nullptr, nullptr};
   const TileSpec t0{L.bm1, at<Tile>(ws, L.tiles0), ntiles, small_expert_rows(dtype, L.bm1), ntiles + 2, ntiles + 18};
-  MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, t0, none, 0, nullptr, 1, 0, nullptr, s));
-  const GradArgs g{dy, w, dx, R, out, in, E, offsets, nullptr, 0, t0.tiles, ntiles, ntiles + 2};
+  MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, t0, none, 0, nullptr, 1, 0, nullptr, ntiles + 20, s));
+  const GradArgs g{dy, w, dx, R, out, in, E, offsets, nullptr, 0, t0.tiles, ntiles, ntiles + 2,
+                   grouped_splits(GM_DGRAD, dtype, E, R, out, in, L.part_bytes), at<float>(ws, L.part), ntiles + 20};
   MOE_TRY(ST_GROUPED_LINEAR, dtype == MOE_F32 ? launch_grouped_f32(GM_DGRAD, g, L.max_tiles1, s)
                                               : launch_grouped_bf16(GM_DGRAD, g, L.max_tiles1, s));
+  if (g.splits > 1) MOE_TRY(ST_GROUPED_LINEAR, launch_grouped_join(GM_DGRAD, dtype, g, s));
   return MOE_OK;
 }
 
@@ -306,17 +313,19 @@ moe_status moe_grouped_linear_wgrad(int32_t E, int64_t R, int32_t in, int32_t ou
   if (!dw || !offsets || (R > 0 && (!dy || !x))) return MOE_ERR_INVALID_ARG;
   if (dw == dy || dw == x || !all_aligned16(dy, x, dw)) return MOE_ERR_INVALID_ARG;
   const GroupedLayout L = grouped_layout(E, R, dtype);
-  if (row_index && (!workspace || ws_bytes < L.total || !aligned16(workspace))) return MOE_ERR_WORKSPACE;
+  if (!workspace || ws_bytes < L.total || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   int32_t* src = nullptr;
   if (row_index && R > 0) {
     src = at<int32_t>(workspace, L.src_row);
     const TileSpec none{0, nullptr, nullptr, 0, nullptr, nullptr};
-    MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, none, none, 0, row_index, index_div, x_rows, src, s));
+    MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, none, none, 0, row_index, index_div, x_rows, src, nullptr, s));
   }
-  const GradArgs g{dy, x, dw, R, out, in, E, offsets, src, x_rows, nullptr, nullptr, nullptr};
+  const GradArgs g{dy, x, dw, R, out, in, E, offsets, src, x_rows, nullptr, nullptr, nullptr,
+                   grouped_splits(GM_WGRAD, dtype, E, R, out, in, L.part_bytes), at<float>(workspace, L.part), nullptr};
   MOE_TRY(ST_GROUPED_LINEAR,
           dtype == MOE_F32 ? launch_grouped_f32(GM_WGRAD, g, 0, s) : launch_grouped_bf16(GM_WGRAD, g, 0, s));
+  if (g.splits > 1) MOE_TRY(ST_GROUPED_LINEAR, launch_grouped_join(GM_WGRAD, dtype, g, s));
   return MOE_OK;
 }
 
