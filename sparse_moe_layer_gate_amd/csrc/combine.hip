@@ -100,8 +100,8 @@ __global__ __launch_bounds__(1024) void combine_kernel(const T* __restrict__ Y, 
 template <typename T>
 __global__ __launch_bounds__(1024) void combine_rows_kernel(const T* __restrict__ rows_in, int64_t R,
                                                            const int32_t* __restrict__ inv_row,
-                                                           const float* __restrict__ w, const T* __restrict__ shared,
-                                                           int k, int D, float alpha, T* __restrict__ y) {
+                                                           const float* __restrict__ w, const T* shared,
+                                                           int k, int D, float alpha, T* y) {
   __shared__ int rows[MAX_K];
   __shared__ float wt[MAX_K];
   const int64_t n = blockIdx.x;

@@ -29,7 +29,7 @@ def workspace(n):
 # ---------------------------------------------------------------- block norms
 NORM_CASES = [
     # N, D, gate rows (0: no gate), parts
-    (1, 64, 0, "post+pre"), (1, 6144, 1 << 40, "post+pre"), (3, 320, 1, "post+pre"), (37, 512, 5, "post+pre"),
+    (1, 64, 0, "post+pre"), (1, 6144, 1 << 40, "post+pre"), (300, 4160, 9, "post+pre"), (300, 4096, 0, "post+pre"), (3, 320, 1, "post+pre"), (37, 512, 5, "post+pre"),
     (700, 192, 256, "post+pre"), (1500, 64, 700, "post+pre"), (1030, 64, 3, "post+pre"),
     (5, 8256, 2, "post+pre"), (2, 16384, 2, "post+pre"),
     (19, 256, 4, "post"), (19, 256, 4, "plain+pre"), (33, 576, 0, "plain"), (19, 256, 0, "pre"), (1100, 128, 0, "pre"),
@@ -214,12 +214,13 @@ GROUPED = [  # N, k, E, K, M, share of empty slots
     (1, 1, 1, 64, 64, 0.0), (1, 4, 16, 256, 192, 0.0), (3, 2, 512, 64, 128, 0.0), (65, 2, 4, 320, 576, 0.2),
     (300, 2, 3, 128, 320, 0.1), (700, 1, 2, 192, 64, 0.0), (40, 8, 16, 448, 832, 0.3), (9, 1, 5, 128, 64, 1.0),
     (2000, 1, 2, 64, 256, 0.0), (130, 4, 60, 512, 256, 0.0),
+    (37, 2, 3, 128, 2112, 0.0),   # few rows and a long reduction: split
 ]
 
 
 def grouped_setup(N, k, E, K, M, empty, dt, gather, seed=6):
-    """Integer-valued operands: every sum is exact in float32 (|sum| <= 9 * 2000 and a K or M of at most 832),
-    so an output is the exact value rounded once."""
+    """Integer-valued operands: every sum is exact in float32 (at most 9 * 6000 in magnitude), so an output is the
+    exact value rounded once, in whatever order and parts it was summed."""
     g = gen(seed)
     _, offsets, pair, _ = O.lists(g, N, k, E, empty)
     R = N * k
@@ -258,6 +259,36 @@ def test_grouped_linear_and_gradients(N, k, E, K, M, empty, gather, dtype):
     torch.cuda.synchronize()
     print("  wgrad done", flush=True)
     assert torch.equal(dw.cpu(), O.grouped_wgrad(dy.double(), x.double(), offsets, src, E).to(dt))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_grouped_uneven_experts(dtype):
+    """One expert with most of the rows (more than 2,048 of them, gathered), small ones of every remainder by the
+    tile and step sizes, and empty ones between: the weight gradient's load stream crosses all of these borders."""
+    dt, K, M = TYPES[dtype], 320, 576
+    g = gen(15)
+    counts = [0, 5, 4097, 0, 0, 1, 31, 32, 33, 0, 255, 256, 257, 64, 0, 511, 3, 0]
+    E, R, N = len(counts), sum(counts) + 7, 900
+    offsets = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
+    used = int(offsets[-1])
+    pair = torch.randint(0, 2 * N, (R,), generator=g, dtype=torch.int32)
+    x, w, dy = O.ints(g, (N, K), -3, 3, dt), O.ints(g, (E, M, K), -3, 3, dt), O.ints(g, (R, M), -3, 3, dt)
+    src = (pair // 2).long()
+    ws = workspace(moe.moe_grouped_workspace_size(E, R, dtype))
+    y, dx, dw = (torch.full(s, 7.0, dtype=dt, device="cuda") for s in ((R, M), (R, K), (E, M, K)))
+    o, p = dev(offsets), dev(pair)
+    moe.moe_grouped_linear(dev(x), dev(w), o, y, ws, row_index=p, index_div=2)
+    moe.moe_grouped_linear_dgrad(dev(dy), dev(w), o, dx, ws)
+    moe.moe_grouped_linear_wgrad(dev(dy), dev(x), o, dw, ws, row_index=p, index_div=2)
+    torch.cuda.synchronize()
+    xd, wd, dyd = x.double(), w.double(), dy.double()
+    assert torch.equal(y[:used].cpu(), O.grouped(xd, wd, offsets, src, R)[:used].to(dt))
+    assert torch.equal(dx[:used].cpu(), O.grouped_dgrad(dyd, wd, offsets)[:used].to(dt))
+    assert torch.equal(dw.cpu(), O.grouped_wgrad(dyd, xd, offsets, src, E).to(dt))
+    assert (y[used:] == 7.0).all() and (dx[used:] == 7.0).all()
+    again = torch.empty_like(dw)
+    moe.moe_grouped_linear_wgrad(dev(dy), dev(x), o, again, ws, row_index=p, index_div=2)
+    assert torch.equal(again, dw)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -324,7 +355,10 @@ def swiglu64(y, limit):
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("N,k,E,K,M", [(1, 1, 1, 128, 64), (1, 1, 1, 5120, 128), (17, 1, 1, 384, 192), (70, 1, 1, 640, 320),
                                        (3, 2, 512, 256, 64), (33, 4, 16, 896, 256), (500, 1, 3, 256, 128),
-                                       (16, 1, 1, 6144, 64), (5, 1, 1, 12288, 64)])
+                                       (16, 1, 1, 6144, 64), (5, 1, 1, 12288, 64),
+                                       # 32-row, 64-row and 48-row tiles
+                                       (40, 2, 64, 256, 256), (200, 1, 1, 128, 16384), (400, 8, 64, 128, 1024),
+                                       (1021, 1, 1, 128, 5120)])
 def test_qlinear_exact(N, k, E, K, M, group):
     """Integer activations and power-of-two scales: float32 holds every sum exactly, so the output is the exact
     value rounded once."""
@@ -347,11 +381,12 @@ def test_qlinear_exact(N, k, E, K, M, group):
 
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("swiglu,limit", [(False, 0.0), (True, 0.0), (True, 1.5)])
-@pytest.mark.parametrize("N,E", [(1, 1), (9, 1), (130, 1), (40, 8)])
-def test_qlinear_float_values(N, E, swiglu, limit, group):
+@pytest.mark.parametrize("N,E,M", [(1, 1, 256), (9, 1, 256), (130, 1, 256), (40, 8, 256), (30, 1, 16384),
+                                   (200, 1, 16384), (410, 1, 12288)])
+def test_qlinear_float_values(N, E, M, swiglu, limit, group):
     """Ordinary values. Bound of the product: every float32 step of the offset form (products of 128 + q and
     -136, at most 280 |x| s a value; group sums of 2 group terms, then K / group scaled sums)."""
-    K, M, k = 768, 256, 1
+    K, k = 768 if M == 256 else 384, 1
     g = gen(11)
     _, offsets, pair, _ = O.lists(g, N, k, E)
     x = torch.randn((N, K), generator=g).to(BF)
