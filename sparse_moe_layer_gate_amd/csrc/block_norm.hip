@@ -13,10 +13,12 @@
 // once into registers (eight consecutive features per thread and pass over the row), so the sums and the
 // second use of a row cost no second read. Rows come straight from the kernel before, so the loads keep the
 // default policy and may hit the last-level cache (8,191 x 5,120 forward 72 us with non-temporal loads, 61
-// without); the stores are non-temporal where nothing reads them soon (61 against 75).
+// without); the stores are non-temporal where nothing reads them soon (61 against 75). On inputs that are not in
+// that cache the forward takes 69 us, 4.9 TB/s, the rate of a large copy; the gradients of 4,096 x 4,096 take 55 us,
+// 3.7 TB/s (two barriers and the partial sums of the parameter gradients cost the rest).
 #include <hip/hip_runtime.h>
 
-#include "moe_internal.h"
+#include "ops_internal.h"
 #include "row_ops.h"
 
 namespace moe {

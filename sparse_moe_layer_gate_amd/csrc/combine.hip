@@ -5,7 +5,7 @@
 // Empty slots (inv_row < 0) add nothing. No atomics: the same inputs always give the same bits.
 #include <hip/hip_runtime.h>
 
-#include "moe_internal.h"
+#include "ops_internal.h"
 #include "row_ops.h"
 
 namespace moe {

@@ -302,51 +302,6 @@ __global__ __launch_bounds__(256) void dense_tiles_kernel(int64_t N, TileSpec t0
   }
 }
 
-// Inclusive running maximum of one int per thread over a 512-thread block.
-__device__ int block_running_max(int v, int* wmax) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int y = __shfl_up(v, off);
-    if (lane >= off) v = max(v, y);
-  }
-  if (lane == 63) wmax[wave] = v;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) v = max(v, wmax[w]);
-  __syncthreads();
-  return v;
-}
-
-// Tile lists of the rows that `offsets` [E + 1] groups (block 0), and the source row of every grouped row
-// (the other blocks). The offsets and indices come from the caller: ranges are kept within [0, R] and in
-// order (each start is the largest offset so far), so that the lists never hold more than R rows, and
-// source rows within [0, x_rows).
-__global__ __launch_bounds__(512) void offset_lists_kernel(const int32_t* __restrict__ offsets, int E, int64_t R,
-                                                           TileSpec t0, TileSpec t1, int pick_rows,
-                                                           const int32_t* __restrict__ row_index, int32_t div,
-                                                           int64_t x_rows, int32_t* __restrict__ src_row,
-                                                           int32_t* __restrict__ row_range) {
-  if (blockIdx.x > 0) {
-    const int64_t r = (int64_t)(blockIdx.x - 1) * 512 + threadIdx.x;
-    if (r < R) src_row[r] = (int32_t)min(max((int64_t)(row_index[r] / div), (int64_t)0), x_rows - 1);
-    return;
-  }
-  __shared__ int wsum[8];
-  __shared__ int max_cnt;
-  if (threadIdx.x == 0) max_cnt = 0;
-  const int e = threadIdx.x;  // E <= 512: one expert per thread
-  const int lo = e < E ? (int)min(max((int64_t)offsets[e], (int64_t)0), R) : 0;
-  const int hi = e < E ? (int)min(max((int64_t)offsets[e + 1], (int64_t)0), R) : 0;
-  const int start = block_running_max(lo, wsum);
-  const int cnt = e < E ? max(hi - start, 0) : 0;
-  if (row_range && e == 0) row_range[0] = lo;
-  if (row_range && e == E - 1) row_range[1] = max(start, hi);  // the experts' ranges lie end to end
-  if (pick_rows > 0 && cnt > 0) atomicMax(&max_cnt, cnt);  // read after the lists' barriers
-  if (t0.tiles) build_tiles(t0, e < E, e, cnt, start, 0, 0, wsum);
-  if (t1.tiles) build_tiles(t1, e < E, e, cnt, start, 0, 0, wsum);
-  if (pick_rows > 0 && threadIdx.x == 0) *(max_cnt <= pick_rows ? t1.n_tiles : t0.n_tiles) = 0;
-}
-
 __global__ __launch_bounds__(256) void fill2_i32_kernel(int32_t* __restrict__ p, int64_t n, int32_t* __restrict__ q,
                                                        int64_t m, int32_t v) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n + m; i += (int64_t)gridDim.x * 256) {
@@ -363,16 +318,6 @@ hipError_t launch_fill2_i32(int32_t* p, int64_t n, int32_t* q, int64_t m, int32_
   if (n + m <= 0) return hipSuccess;
   const int64_t blocks = min((n + m + 255) / 256, (int64_t)1024);
   hipLaunchKernelGGL(fill2_i32_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p, n, q, m, v);
-  return hipGetLastError();
-}
-
-hipError_t launch_offset_lists(const int32_t* offsets, int E, int64_t R, TileSpec t0, TileSpec t1, int pick_rows,
-                               const int32_t* row_index, int32_t div, int64_t x_rows, int32_t* src_row,
-                               int32_t* row_range, hipStream_t s) {
-  if (E > 512) return hipErrorInvalidValue;
-  const int64_t blocks = 1 + (row_index ? (R + 511) / 512 : 0);
-  hipLaunchKernelGGL(offset_lists_kernel, dim3((unsigned)blocks), dim3(512), 0, s, offsets, E, R, t0, t1, pick_rows,
-                     row_index, div, x_rows, src_row, row_range);
   return hipGetLastError();
 }
 

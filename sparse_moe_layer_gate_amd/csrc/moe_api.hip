@@ -7,7 +7,7 @@
 #include <mutex>
 #include <vector>
 
-#include "moe_internal.h"
+#include "ops_internal.h"
 
 using namespace moe;
 
@@ -194,7 +194,7 @@ hipEvent_t next_event() {
   return g_pool[g_pool_next++];
 }
 
-const char* kStageNames[ST_COUNT_STAGES] = {"router_split", "router_logits", "router_select",  "dispatch_count",
+const char* kStageNames[ST_ALL_STAGES] = {"router_split", "router_logits", "router_select",  "dispatch_count",
                                             "dispatch_scan", "dispatch_place", "experts_gate_up", "experts_down",
                                             "combine", "block_norm", "grouped_lists", "grouped_linear", "qlinear",
                                             "quantize"};
@@ -625,9 +625,9 @@ moe_status moe_profile_end(double* ms_per_stage, int32_t* launches_per_stage, in
 }
 
 const char* moe_stage_name(int32_t stage) {
-  return (stage >= 0 && stage < ST_COUNT_STAGES) ? kStageNames[stage] : nullptr;
+  return (stage >= 0 && stage < ST_ALL_STAGES) ? kStageNames[stage] : nullptr;
 }
 
-int32_t moe_stage_count(void) { return ST_COUNT_STAGES; }
+int32_t moe_stage_count(void) { return ST_ALL_STAGES; }
 
 }  // extern "C"

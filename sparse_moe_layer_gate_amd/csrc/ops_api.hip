@@ -6,7 +6,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "moe_internal.h"
+#include "ops_internal.h"
 
 using namespace moe;
 
