@@ -317,7 +317,10 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
 template <class T, int G>
 hipError_t launch_q(const QuantArgs& a, hipStream_t s) {
   const int wcols = (a.swiglu ? 8 : 16) * T::RT * T::WAVE_N, ncols = a.swiglu ? a.M / 2 : a.M;
-  int64_t z = (a.R + (int64_t)a.E * T::ROWS - 1) / ((int64_t)a.E * T::ROWS);  // even load: one tile per block
+  // row tiles side by side: what an even load needs, twice that for experts with more rows than the others (a
+  // block takes every z-th tile of its expert)
+  int64_t z = (a.R + (int64_t)a.E * T::ROWS - 1) / ((int64_t)a.E * T::ROWS);
+  if (a.E > 1 && z > 1) z *= 2;
   if (z > 65535) z = 65535;
   const dim3 grid((ncols + wcols - 1) / wcols, a.E, (unsigned)z);
   if (a.swiglu)
