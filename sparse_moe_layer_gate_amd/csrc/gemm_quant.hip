@@ -74,6 +74,11 @@ __device__ inline void exchange4(u32x4& d) {
   d[3] = e[1];
 }
 
+template <int V>
+struct IntC {
+  static constexpr int value = V;
+};
+
 template <class T, int G, bool SWIGLU>
 __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
   constexpr int TT = T::TT, KS = T::KS, RT = T::RT, NSEG = T::NSEG, BATCH = T::BATCH;
@@ -222,49 +227,59 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
         // the next batch is STEP further on, within the chunk or at the next one's start (chunks are
         // whole steps); nothing is read past the row
         if (c0 + b0 + T::STEP < K) load(c0 + b0 + T::STEP);
+        // of a 32-row tile with at most 16 rows only the first half (32 tokens over 256 experts, groups of 32: 472 ->
+        // 446 us). Groups of 128 hold more activations at a time and spilled with both bodies: they always run the
+        // whole tile (one token, 5,120 -> 24,576: 19 us, 25 with both bodies).
+        auto batch = [&](auto tiles) {
+          constexpr int NT = decltype(tiles)::value;
 #pragma unroll
-        for (int p = 0; p < NSEG; ++p) {
-          if (c0 + b0 + p * SEG >= K) break;
-          if (G < SEG) {
+          for (int p = 0; p < NSEG; ++p) {
+            if (c0 + b0 + p * SEG >= K) break;
+            if (G < SEG) {
 #pragma unroll
-            for (int t = 0; t < RT; ++t) exchange4(cq[t][p]);
-          }
-          const uint16_t* xp = xs + b0 + p * SEG;
-#pragma unroll
-          for (int g = 0; g < GPS; ++g) {
-            f32x4 off[TT];  // -136 sum(x) of the group, the start of every tile's sum
-            bf16x8 xf[STEPS][TT];
-#pragma unroll
-            for (int i = 0; i < TT; ++i) {
-              off[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int u = 0; u < STEPS; ++u) {
-                const int piece = G < SEG ? 4 * (g * STEPS + u) + j : 4 * j + u;
-                xf[u][i] = *(const bf16x8*)(xp + min(16 * i + r16, rows - 1) * pitch + piece * 8);
-                off[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], minus136, off[i], 0, 0, 0);
-              }
+              for (int t = 0; t < RT; ++t) exchange4(cq[t][p]);
             }
+            const uint16_t* xp = xs + b0 + p * SEG;
 #pragma unroll
-            for (int t = 0; t < RT; ++t) {
-              f32x4 sum[TT];
+            for (int g = 0; g < GPS; ++g) {
+              f32x4 off[NT];  // -136 sum(x) of the group, the start of every tile's sum
+              bf16x8 xf[STEPS][NT];
 #pragma unroll
-              for (int u = 0; u < STEPS; ++u) {
-                const bf16x8 w = unpack8(cq[t][p][g * STEPS + u], mask, magic);
+              for (int i = 0; i < NT; ++i) {
+                off[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < TT; ++i)
-                  sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, u == 0 ? off[i] : sum[i], 0, 0, 0);
+                for (int u = 0; u < STEPS; ++u) {
+                  const int piece = G < SEG ? 4 * (g * STEPS + u) + j : 4 * j + u;
+                  xf[u][i] = *(const bf16x8*)(xp + min(16 * i + r16, rows - 1) * pitch + piece * 8);
+                  off[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], minus136, off[i], 0, 0, 0);
+                }
               }
-              const uint32_t sw = cs[t][(p * GPS + g) / 2];
-              const float s = __uint_as_float((p * GPS + g) & 1 ? sw & 0xffff0000u : sw << 16);
 #pragma unroll
-              for (int i = 0; i < TT; ++i)
+              for (int t = 0; t < RT; ++t) {
+                f32x4 sum[NT];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][t][r] += s * sum[i][r];
+                for (int u = 0; u < STEPS; ++u) {
+                  const bf16x8 w = unpack8(cq[t][p][g * STEPS + u], mask, magic);
+#pragma unroll
+                  for (int i = 0; i < NT; ++i)
+                    sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, u == 0 ? off[i] : sum[i], 0, 0, 0);
+                }
+                const uint32_t sw = cs[t][(p * GPS + g) / 2];
+                const float s = __uint_as_float((p * GPS + g) & 1 ? sw & 0xffff0000u : sw << 16);
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) acc[i][t][r] += s * sum[i][r];
+              }
+              // keeps the compiler from reading several groups' activations ahead, which spilled
+              __builtin_amdgcn_sched_barrier(0);
             }
-            // keeps the compiler from reading several groups' activations ahead, which spilled
-            __builtin_amdgcn_sched_barrier(0);
           }
-        }
+        };
+        if (TT == 2 && G < SEG && rows <= 16)
+          batch(IntC<1>{});
+        else
+          batch(IntC<TT>{});
       }
     }
     // the waves that split k: partial sums through LDS, added in wave order by the first of them
@@ -370,12 +385,12 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ w, 
 // dense 12,288 -> 5,120 (groups of 64), dense 5,120 -> 24,576 and 256 experts 6,144 -> 4,096 with eight rows a
 // token (SwiGLU, groups of 128 and 32):
 //   narrow, 16 rows, k over four waves      1 / 64 / 128 rows: 18 / 63 / 104 | 22 / 91 / 177 | 32 tokens: 467
-//   middle, 32 rows, k over two waves       29 / 84 / 93                     | 20 / 51 / 95  | 462
+//   middle, 32 rows, k over two waves       29 / 84 / 93                     | 20 / 51 / 95  | 446
 //   wide, 64 or 48 rows, all of k per wave  98 / 185 / 183                   | 46 / 89 / 91  | 675
 // The narrow form reads the activations most often but makes the most and shortest blocks: it wins while the
 // middle form makes fewer than one block per CU. The wide form shares each unpacked weight among 48 or 64 rows:
-// it wins from 24 rows per expert on (256 experts, 512 / 1,024 tokens: middle 1,203 / 1,756, wide 1,297 /
-// 1,622) once it makes blocks for three quarters of the CUs (512 rows, 12,288 -> 5,120: 202 against 194).
+// it wins from 24 rows per expert on (256 experts, 512 / 1,024 tokens: middle 1,130 / 1,756, wide 1,297 /
+// 1,597) once it makes blocks for three quarters of the CUs (512 rows, 12,288 -> 5,120: 202 against 194).
 // Of its two heights a dense product takes the one whose last round of blocks leaves less idle (1,021 rows,
 // 12,288 -> 5,120: 298 with 64 rows, 257 with 48; 2,048 rows, 5,120 -> 24,576: 739 and 762).
 hipError_t launch_qlinear(const QuantArgs& a, hipStream_t s) {
