@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "ops_internal.h"
 #include "row_ops.h"
@@ -40,9 +41,11 @@ __device__ inline void load8f(const float* p, float* f) {
 //   fwd:   i = row, j = output feature, t = input feature;   both operands contiguous in t
 //   dgrad: i = row, j = input feature,  t = output feature;  B contiguous in j
 //   wgrad: i = output feature, j = input feature, t = row;   both contiguous in i / j
-// (60 experts, 704 -> 1,024, 1,024 tokens of four: 121 / 162 / 95 us; one matrix step per LDS round trip and two
+// (60 experts, 704 -> 1,024, 1,024 tokens of four: 116 / 155 / 94 us; one matrix step per LDS round trip and two
 // barriers bound it, not the matrix cores.)
-template <int MODE>
+// FEW, for groups of few rows (launch_grouped_f32): the waves stand side by side, 128 rows x 32 columns each as 8 x 2
+// tiles, and multiply only the row tiles that hold rows (rounded up to 1, 2, 4 or 8).
+template <int MODE, bool FEW>
 __global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tiles) {
   constexpr bool A_T = MODE == GM_WGRAD;              // A contiguous in i
   constexpr bool B_T = MODE != GM_FWD;                // B contiguous in j
@@ -84,7 +87,8 @@ __global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tile
   const int64_t wbase = (int64_t)expert * M * K;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wi = (wave >> 1) * 64, wj = (wave & 1) * 64;
+  constexpr int TI = FEW ? 8 : 4, TJ = FEW ? 2 : 4;  // 16 x 16 tiles of a wave
+  const int wi = FEW ? 0 : (wave >> 1) * 64, wj = FEW ? wave * 32 : (wave & 1) * 64;
   // this thread's eight elements of each operand per step
   const int ai = A_T ? (tid & 15) * 8 : tid >> 1, at = A_T ? tid >> 4 : (tid & 1) * 8;
   const int bj = B_T ? (tid & 15) * 8 : tid >> 1, bt = B_T ? tid >> 4 : (tid & 1) * 8;
@@ -92,11 +96,13 @@ __global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tile
   int64_t a_row = 0;
   if (MODE == GM_FWD && ai < rows) a_row = src(row0 + ai);
 
-  f32x4 acc[4][4];
+  f32x4 acc[TI][TJ];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < TI; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int live = __builtin_amdgcn_readfirstlane((min(ni - i0, 128) + 15) / 16);  // row tiles that hold rows
 
   float ra[8], rb[8];
   auto load = [&](int t0) {
@@ -129,30 +135,45 @@ __global__ __launch_bounds__(256) void grouped_f32_tile(GradArgs a, int col_tile
     put(sb, B_T, bj, bt, rb);
     __syncthreads();
     if (t0 + BT < nt) load(t0 + BT);
+    auto products = [&](auto tiles) {
+      constexpr int TILES = decltype(tiles)::value;
 #pragma unroll
-    for (int k = 0; k < BT; k += 4) {
-      float av[4], bv[4];
+      for (int k = 0; k < BT; k += 4) {
+        float av[TILES], bv[TJ];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) av[i] = sa[k + (lane >> 4)][wi + 16 * i + (lane & 15)];
+        for (int i = 0; i < TILES; ++i) av[i] = sa[k + (lane >> 4)][wi + 16 * i + (lane & 15)];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) bv[j] = sb[k + (lane >> 4)][wj + 16 * j + (lane & 15)];
+        for (int j = 0; j < TJ; ++j) bv[j] = sb[k + (lane >> 4)][wj + 16 * j + (lane & 15)];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < TILES; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[j], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[j], acc[i][j], 0, 0, 0);
+      }
+    };
+    if constexpr (!FEW) {
+      products(std::integral_constant<int, TI>{});
+    } else {
+      if (live > 4)
+        products(std::integral_constant<int, TI>{});
+      else if (live > 2)
+        products(std::integral_constant<int, TI / 2>{});
+      else if (live == 2)
+        products(std::integral_constant<int, 2>{});
+      else
+        products(std::integral_constant<int, 1>{});
     }
   }
   const int64_t part_elems = MODE == GM_WGRAD ? (int64_t)a.E * M * K : a.R * nj;
   float* out = a.splits > 1 ? a.part + split * part_elems : (float*)a.out;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < TI; ++i)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int ii = i0 + wi + 16 * i + 4 * (lane >> 4) + q;
       if (ii >= ni) continue;
       const int64_t base = MODE == GM_WGRAD ? wbase + (int64_t)ii * K : (row0 + ii) * (int64_t)nj;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < TJ; ++j) {
         const int jj = j0 + wj + 16 * j + (lane & 15);
         if (jj < nj) out[base + jj] = acc[i][j][q];
       }
@@ -901,12 +922,21 @@ hipError_t launch_grouped_f32(GroupedMode mode, const GradArgs& a, int64_t max_t
   if (blocks == 0) return hipSuccess;
   if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
-  if (mode == GM_FWD)
-    hipLaunchKernelGGL(grouped_f32_tile<GM_FWD>, grid, block, 0, s, a, cols);
+  // Groups of few rows on average: most of a 128-row tile is empty, and the form that skips its empty row tiles wins
+  // up to about 32 rows per group (60 experts, 704 -> 1,024, us with / without: fwd of 8 / 16 / 32 / 40 rows 54 / 113,
+  // 72 / 111, 108 / 112, 124 / 113; dgrad 78 / 149, 91 / 151, 148 / 155, 175 / 154). With full tiles it is slower
+  // (dgrad, 48 rows: 176 / 158): it holds 196 registers instead of 108, so fewer waves hide the loads.
+  const bool few = a.R <= 32 * (int64_t)a.E;
+  if (mode == GM_FWD && few)
+    hipLaunchKernelGGL((grouped_f32_tile<GM_FWD, true>), grid, block, 0, s, a, cols);
+  else if (mode == GM_FWD)
+    hipLaunchKernelGGL((grouped_f32_tile<GM_FWD, false>), grid, block, 0, s, a, cols);
+  else if (mode == GM_DGRAD && few)
+    hipLaunchKernelGGL((grouped_f32_tile<GM_DGRAD, true>), grid, block, 0, s, a, cols);
   else if (mode == GM_DGRAD)
-    hipLaunchKernelGGL(grouped_f32_tile<GM_DGRAD>, grid, block, 0, s, a, cols);
+    hipLaunchKernelGGL((grouped_f32_tile<GM_DGRAD, false>), grid, block, 0, s, a, cols);
   else
-    hipLaunchKernelGGL(grouped_f32_tile<GM_WGRAD>, grid, block, 0, s, a, cols);
+    hipLaunchKernelGGL((grouped_f32_tile<GM_WGRAD, false>), grid, block, 0, s, a, cols);
   return hipGetLastError();
 }
 

@@ -292,6 +292,33 @@ def test_grouped_uneven_experts(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("K,M", [(192, 320), (320, 64), (1216, 128)])
+def test_grouped_few_rows_on_average(K, M, dtype):
+    """Few rows per expert on average, with groups on both sides of every multiple of 16 that a product's form changes
+    at, so that each of the forms that skip empty row tiles runs."""
+    dt = TYPES[dtype]
+    g = gen(16)
+    counts = [1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 112, 127, 128, 129] + [0, 2] * 25
+    E, R = len(counts), sum(counts) + 3
+    assert R <= 32 * E
+    offsets = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
+    used = int(offsets[-1])
+    x, w, dy = O.ints(g, (R, K), -3, 3, dt), O.ints(g, (E, M, K), -3, 3, dt), O.ints(g, (R, M), -3, 3, dt)
+    ws = workspace(moe.moe_grouped_workspace_size(E, R, dtype))
+    y, dx, dw = (torch.full(s, 7.0, dtype=dt, device="cuda") for s in ((R, M), (R, K), (E, M, K)))
+    o = dev(offsets)
+    moe.moe_grouped_linear(dev(x), dev(w), o, y, ws)
+    moe.moe_grouped_linear_dgrad(dev(dy), dev(w), o, dx, ws)
+    moe.moe_grouped_linear_wgrad(dev(dy), dev(x), o, dw, ws)
+    torch.cuda.synchronize()
+    xd, wd, dyd, src = x.double(), w.double(), dy.double(), torch.arange(R)
+    assert torch.equal(y[:used].cpu(), O.grouped(xd, wd, offsets, src, R)[:used].to(dt))
+    assert torch.equal(dx[:used].cpu(), O.grouped_dgrad(dyd, wd, offsets)[:used].to(dt))
+    assert torch.equal(dw.cpu(), O.grouped_wgrad(dyd, xd, offsets, src, E).to(dt))
+    assert (y[used:] == 7.0).all() and (dx[used:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_grouped_float_values(dtype):
     """Ordinary values: within the bound of a float32 sum and one rounding."""
     dt, N, k, E, K, M = TYPES[dtype], 150, 2, 3, 576, 320
