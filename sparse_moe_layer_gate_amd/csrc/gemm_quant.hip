@@ -20,9 +20,11 @@
 // What bounds it: 32 tokens over 256 experts, 6,144 -> 4,096, groups of 32: 0.44 ms, 5.2 TB/s of weights and
 // scales, faster than a large copy, the vector unit busy about half the cycles; one token, 5,120 -> 24,576, groups
 // of 128: 18-20 us, of which the 65 MB would take 13 (the launch's ramp, three rounds of loads per wave); 1,021
-// rows, 12,288 -> 5,120, groups of 64: 0.25 ms, 510 TFLOP/s, vector unit 44% and matrix cores 26% busy with two
-// waves per SIMD that rarely overlap.
+// rows, 12,288 -> 5,120, groups of 64: 0.23 ms, 560 TFLOP/s: per 48 x 64 x 256 values of a wave 120 matrix
+// instructions (16 cycles each) and about 650 vector ones (4 each) of two waves per SIMD that overlap in part.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "ops_internal.h"
 #include "row_ops.h"
@@ -283,10 +285,10 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
       }
     }
     // the waves that split k: partial sums through LDS, added in wave order by the first of them
-    if (KS > 1) {
+    {
       constexpr int PER = TT * RT * 4;
       float* red = (float*)xs;  // [4 waves][PER][64 lanes]
-      static_assert(KS == 1 || 4 * PER * 64 * 4 <= T::LDS_ELEMS * 2, "the partial sums fit the activations' space");
+      static_assert(4 * PER * 64 * 4 <= T::LDS_ELEMS * 2, "the partial sums fit the activations' space");
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < TT; ++i)
@@ -327,6 +329,241 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
         }
     }
   }
+}
+
+// Many rows: TT 16-row activation tiles and 256 weight rows per block, all of k in every wave, so that a wave uses
+// each value it unpacks for 16 TT rows. The activations pass through two LDS stages of 256 k: half of the next
+// stage's rows is in flight in registers during each of the two 128-wide batches of the present one. A batch's
+// weights are loaded while the batch before it runs. No load is behind a branch (past the end the last valid piece
+// is read again), so every wait names its own loads. Against one stage of twice the length that is loaded, waited
+// for and then used: 1,021 rows, 12,288 -> 5,120, groups of 64, 254 -> 230 us; 2,048 rows, 5,120 -> 24,576 SwiGLU,
+// groups of 128, 690 -> 590; 1,021 rows, 4,096 -> 4,096, groups of 32, 86 -> 64. (Weights loaded one batch earlier
+// into copies of their own: 3% faster with groups of 64, 5-12% slower with 32 and 128; the next group's
+// activations read ahead of the present one's products: nothing, or spills.)
+//
+// One tile of `rows` activation rows, at most 16 TT, from row0 on.
+template <int TT, int G, bool SWIGLU>
+__device__ __forceinline__ void wide_tile(const QuantArgs& a, int expert, int64_t row0, int rows, int wave, int lane,
+                                          uint16_t* lds, int* src_rows) {
+  constexpr int RT = 4, ROWS = 16 * TT, STAGE = 2 * SEG, PITCH = STAGE + 8;
+  constexpr int GPS = SEG / G, STEPS = G / 32;  // groups per piece, matrix steps per group
+  constexpr int XL = TT;                        // this thread's 16-byte loads of half a stage
+  constexpr int SW = (GPS + 1) / 2;
+  constexpr int WCOLS = SWIGLU ? 8 * RT : 16 * RT;
+  const int K = a.K, half = a.M / 2, ncols = SWIGLU ? half : a.M;
+  const int tid = wave * 64 + lane;
+  const int col0 = (blockIdx.x * 4 + wave) * WCOLS;
+  const uint8_t* qb = a.q + (int64_t)expert * a.M * (K / 2);
+  const uint16_t* sb = a.s + (int64_t)expert * a.M * (K / G);
+  uint32_t mask = 0x000f000fu, magic = 0x43004300u;
+  asm("" : "+s"(mask));  // not constants to the compiler: see unpack8
+  asm("" : "+v"(magic));
+  const u32x4 neg = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};  // -136 as bfloat16 pairs
+  const bf16x8 minus136 = __builtin_bit_cast(bf16x8, neg);
+  const int stages = (K + STAGE - 1) / STAGE;
+  int ln = lane;
+  asm volatile("" : "+v"(ln));  // what depends on the lane stays inside the tile
+  const int r16 = ln & 15, j = ln >> 4;
+  uint32_t wq[RT], ws[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int c = min(col0, ncols - WCOLS);
+    const int m = SWIGLU ? (t & 1) * half + c + 16 * (t >> 1) : c + 16 * t;
+    wq[t] = (uint32_t)(m + r16) * (uint32_t)(K / 2);
+    ws[t] = (uint32_t)(m + r16) * (uint32_t)(K / G);
+  }
+  __syncthreads();  // the previous tile's LDS reads are over
+  if (tid < ROWS) {
+    int64_t r = row0 + min(tid, rows - 1);  // rows past the tile repeat its last
+    if (a.row_index) {
+      r = a.row_index[r] / a.div;
+      r = min(max(r, (int64_t)0), a.x_rows - 1);
+    }
+    src_rows[tid] = (int)r;
+  }
+  __syncthreads();
+  f32x4 acc[TT][RT];
+#pragma unroll
+  for (int i = 0; i < TT; ++i)
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // rows 8 i + tid / 32 of half a stage's rows, values 8 (tid % 32) .. of the stage
+  const int xr = wave * 2 + (ln >> 5), xk = (ln & 31) * 8;
+  u32x4 xv[XL];
+  auto load_x = [&](int stage, int h) {
+    const int k = min(stage * STAGE + xk, K - 8);
+#pragma unroll
+    for (int i = 0; i < XL; ++i)
+      xv[i] = *(const u32x4*)(a.x + (int64_t)src_rows[h * (ROWS / 2) + 8 * i + xr] * K + k);
+  };
+  // zeros past K; values 0 4 1 5 2 6 3 7 of every eight
+  auto put_x = [&](int stage, int h) {
+    const bool in = stage * STAGE + xk < K;
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      u32x4 v = xv[i], w;
+      if (!in) v = u32x4{0, 0, 0, 0};
+      w[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100);
+      w[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302);
+      w[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100);
+      w[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302);
+      *(u32x4*)&lds[((stage & 1) * ROWS + h * (ROWS / 2) + 8 * i + xr) * PITCH + xk] = w;
+    }
+  };
+  static_assert(ROWS / 2 == 8 * XL, "half a stage's rows");
+
+  u32x4 q[2][RT];
+  uint32_t sc[2][RT][SW];
+  auto load_w = [&](int h, int k0) {
+    const int k = min(k0 + j * 32, K - 32);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) q[h][t] = *(const u32x4*)(qb + (wq[t] + (uint32_t)(k >> 1)));
+    // the piece's scales lie together; at the row's end the row's last ones, moved down to where they belong
+    const int g = min(k0 / G, K / G - GPS), sh = 16 * (k0 / G - g);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      if constexpr (GPS == 4) {
+        uint64_t v;
+        __builtin_memcpy(&v, sb + (ws[t] + (uint32_t)g), 8);
+        v >>= sh & 63;
+        sc[h][t][0] = (uint32_t)v;
+        sc[h][t][1] = (uint32_t)(v >> 32);
+      } else if constexpr (GPS == 2) {
+        uint32_t v;
+        __builtin_memcpy(&v, sb + (ws[t] + (uint32_t)g), 4);
+        sc[h][t][0] = v >> (sh & 31);
+      } else {
+        sc[h][t][0] = sb[ws[t] + (uint32_t)g];
+      }
+    }
+  };
+  load_x(0, 0);
+  put_x(0, 0);
+  load_x(0, 1);
+  load_w(0, 0);
+  load_w(1, SEG);
+  put_x(0, 1);
+  for (int st = 0; st < stages; ++st) {
+    __syncthreads();  // this stage is written; the reads of the stage that the next one replaces are over
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k0 = st * STAGE + h * SEG;
+      if (k0 >= K) break;
+      load_x(st + 1, h);
+      if (G < SEG) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) exchange4(q[h][t]);
+      }
+      const uint16_t* xp = &lds[((st & 1) * ROWS + r16) * PITCH + h * SEG];
+#pragma unroll
+      for (int g = 0; g < GPS; ++g) {
+        f32x4 off[TT];  // -136 sum(x) of the group, the start of every tile's sum
+        bf16x8 xf[STEPS][TT];
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+          off[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int u = 0; u < STEPS; ++u) {
+            const int piece = G < SEG ? 4 * (g * STEPS + u) + j : 4 * j + u;
+            xf[u][i] = *(const bf16x8*)(xp + 16 * i * PITCH + piece * 8);
+            off[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], minus136, off[i], 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          f32x4 sum[TT];
+#pragma unroll
+          for (int u = 0; u < STEPS; ++u) {
+            const bf16x8 w = unpack8(q[h][t][g * STEPS + u], mask, magic);
+#pragma unroll
+            for (int i = 0; i < TT; ++i)
+              sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, u == 0 ? off[i] : sum[i], 0, 0, 0);
+          }
+          const uint32_t sw = sc[h][t][g / 2];
+          const float s = __uint_as_float(g & 1 ? sw & 0xffff0000u : sw << 16);
+#pragma unroll
+          for (int i = 0; i < TT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][t][r] += s * sum[i][r];
+        }
+      }
+      load_w(h, k0 + STAGE);
+      put_x(st + 1, h);
+    }
+  }
+  if (col0 < ncols) {
+#pragma unroll
+    for (int i = 0; i < TT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * i + 4 * j + r;
+        if (row >= rows) continue;
+        uint16_t* y = a.y + (row0 + row) * ncols + col0 + r16;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          if (SWIGLU) {
+            if (t & 1) y[8 * (t - 1)] = (uint16_t)bf16_pair(swiglu_bf16(acc[i][t - 1][r], acc[i][t][r], a.limit), 0.f);
+          } else {
+            y[16 * t] = (uint16_t)bf16_pair(acc[i][t][r], 0.f);
+          }
+        }
+      }
+  }
+}
+
+// EXPERTS: a tile of at most 32 rows runs a body of its own (256 experts 6,144 -> 4,096, 24 / 64 rows each: 1,480 ->
+// 1,379, 2,527 -> 2,412 us). A dense product has at most one such tile and keeps one body, which takes fewer
+// registers (12,288 -> 5,120, 1,021 rows: 231 us, 239 with both); so does the form that both would make spill.
+template <int TT, int G, bool SWIGLU, bool EXPERTS>
+__global__ __launch_bounds__(256, 2) void qlinear_wide_kernel(QuantArgs a) {
+  constexpr int ROWS = 16 * TT;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * ROWS * (2 * SEG + 8)];
+  __shared__ int src_rows[ROWS];
+  const int expert = blockIdx.y;
+  int64_t row0 = 0, cnt = a.R;
+  if (a.offsets) {
+    row0 = min(max((int64_t)a.offsets[expert], (int64_t)0), a.R);
+    cnt = min(max((int64_t)a.offsets[expert + 1], row0), a.R) - row0;
+  }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int64_t tile0 = (int64_t)blockIdx.z * ROWS; tile0 < cnt; tile0 += (int64_t)gridDim.z * ROWS) {
+    const int rows = (int)min((int64_t)ROWS, cnt - tile0);
+    if (EXPERTS && !(TT == 4 && G == SEG) && rows <= 32)
+      wide_tile<2, G, SWIGLU>(a, expert, row0 + tile0, rows, wave, lane, lds, src_rows);
+    else
+      wide_tile<TT, G, SWIGLU>(a, expert, row0 + tile0, rows, wave, lane, lds, src_rows);
+  }
+}
+
+template <int TT, int G>
+hipError_t launch_wide_group(const QuantArgs& a, hipStream_t s) {
+  constexpr int ROWS = 16 * TT;
+  const int wcols = a.swiglu ? 128 : 256, ncols = a.swiglu ? a.M / 2 : a.M;
+  int64_t z = (a.R + (int64_t)a.E * ROWS - 1) / ((int64_t)a.E * ROWS);  // as in launch_q
+  if (a.E > 1 && z > 1) z *= 2;
+  if (z > 65535) z = 65535;
+  const dim3 grid((ncols + wcols - 1) / wcols, a.E, (unsigned)z);
+  auto launch = [&](auto swiglu, auto experts) {
+    hipLaunchKernelGGL((qlinear_wide_kernel<TT, G, decltype(swiglu)::value, decltype(experts)::value>), grid, dim3(256), 0,
+                       s, a);
+  };
+  if (a.E > 1 && a.swiglu)
+    launch(std::true_type{}, std::true_type{});
+  else if (a.E > 1)
+    launch(std::false_type{}, std::true_type{});
+  else if (a.swiglu)
+    launch(std::true_type{}, std::false_type{});
+  else
+    launch(std::false_type{}, std::false_type{});
+  return hipGetLastError();
+}
+
+template <int TT>
+hipError_t launch_wide(const QuantArgs& a, hipStream_t s) {
+  if (a.group == 32) return launch_wide_group<TT, 32>(a, s);
+  if (a.group == 64) return launch_wide_group<TT, 64>(a, s);
+  return launch_wide_group<TT, 128>(a, s);
 }
 
 template <class T, int G>
@@ -385,25 +622,26 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ w, 
 // dense 12,288 -> 5,120 (groups of 64), dense 5,120 -> 24,576 and 256 experts 6,144 -> 4,096 with eight rows a
 // token (SwiGLU, groups of 128 and 32):
 //   narrow, 16 rows, k over four waves      1 / 64 / 128 rows: 18 / 63 / 104 | 22 / 91 / 177 | 32 tokens: 467
-//   middle, 32 rows, k over two waves       29 / 84 / 93                     | 20 / 51 / 95  | 446
-//   wide, 64 or 48 rows, all of k per wave  98 / 185 / 183                   | 46 / 89 / 91  | 675
+//   middle, 32 rows, k over two waves       29 / 57 / 95                     | 20 / 50 / 94  | 446
+//   wide, 64 or 48 rows, all of k per wave  98 / 153 / 151                   | 46 / 54 / 58  | 675
 // The narrow form reads the activations most often but makes the most and shortest blocks: it wins while the
-// middle form makes fewer than one block per CU. The wide form shares each unpacked weight among 48 or 64 rows:
-// it wins from 24 rows per expert on (256 experts, 512 / 1,024 tokens: middle 1,130 / 1,756, wide 1,297 /
-// 1,597) once it makes blocks for three quarters of the CUs (512 rows, 12,288 -> 5,120: 202 against 194).
+// middle form makes fewer than one block per CU. The wide form shares each unpacked value among 48 or 64 rows. For
+// a dense product it wins from about 96 rows on, once it makes blocks for five eighths of the CUs (12,288 -> 5,120,
+// middle / wide: 256 rows, 120 blocks, 118 / 152; 384 rows, 160 blocks, 178 / 150; 512 rows 195 / 150). For experts it
+// wins from 24 rows each (128 experts 1,408 -> 4,096, 24 / 32 rows: 191 / 155, 222 / 169; of 256 experts 6,144 -> 4,096
+// with groups of 32 from 32: 1,387 / 1,465, 1,692 / 1,653).
 // Of its two heights a dense product takes the one whose last round of blocks leaves less idle (1,021 rows,
-// 12,288 -> 5,120: 298 with 64 rows, 257 with 48; 2,048 rows, 5,120 -> 24,576: 739 and 762).
+// 12,288 -> 5,120: 264 with 64 rows, 231 with 48; 768 rows 180 and 228), experts the lower one up to 64 rows each
+// (128 experts, 24 / 64 / 128 rows: 165 / 260 / 396 with 64 rows, 155 / 237 / 414 with 48).
 hipError_t launch_qlinear(const QuantArgs& a, hipStream_t s) {
   constexpr int64_t kCus = 256;
   auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
   const int64_t r = up(a.R, a.E);
-  const int64_t middle_blocks = up(a.M, 64) * a.E * up(r, 32), wide_blocks = up(a.M, 256) * a.E * up(r, 64);
-  if (r >= 24 && wide_blocks * 4 >= kCus * 3) {
-    const int64_t cost64 = up(wide_blocks, kCus) * 4, cost48 = up(up(a.M, 256) * up(r, 48), kCus) * 3;
-    if (a.E == 1 && cost48 < cost64) return launch_group<QTile<3, 1, 4, 1, 24576, 2>>(a, s);
-    return launch_group<QTile<4, 1, 4, 1, 32768, 2>>(a, s);
-  }
-  if (middle_blocks >= kCus) return launch_group<QTile<2, 2, 2, 2, 16384, 3>>(a, s);
+  const int64_t blocks64 = up(a.M, 256) * a.E * up(r, 64), blocks48 = up(a.M, 256) * a.E * up(r, 48);
+  const bool low = a.E > 1 ? r <= 64 : up(blocks48, kCus) * 3 < up(blocks64, kCus) * 4;
+  if (a.K >= SEG && r >= (a.E > 1 ? 24 : 96) && (low ? blocks48 : blocks64) * 8 >= kCus * 5)
+    return low ? launch_wide<3>(a, s) : launch_wide<4>(a, s);
+  if (up(a.M, 64) * a.E * up(r, 32) >= kCus) return launch_group<QTile<2, 2, 2, 2, 16384, 3>>(a, s);
   return launch_group<QTile<1, 4, 2, 2, 16384, 4>>(a, s);
 }
 

@@ -406,6 +406,39 @@ def test_qlinear_exact(N, k, E, K, M, group):
     assert (y[used:] == 7.0).all()
 
 
+@pytest.mark.parametrize("group,K", [(32, 192), (32, 448), (32, 1088), (64, 256), (64, 448), (64, 1088), (128, 128),
+                                     (128, 640), (128, 768)])
+@pytest.mark.parametrize("rows", ["dense 64", "dense 48", "experts", "many"])
+def test_qlinear_wide_tiles(rows, group, K):
+    """The forms for many rows: reductions that end inside a stage and inside a 128-value piece, tiles of every
+    remainder, experts of none to several tiles, and one weight row of NaN scales, which only its column shows."""
+    g = gen(17)
+    if rows.startswith("dense"):
+        counts, M = ([150], 16384) if rows == "dense 64" else ([390], 5120)
+    else:
+        counts = [0, 1, 15, 16, 17, 31, 32, 33, 47, 48, 49, 0, 63, 64, 65, 3, 96, 97, 128, 129]
+        counts, M = (counts * 2, 1280) if rows == "experts" else ([2 * c for c in counts], 2560)
+    E, R = len(counts), sum(counts) + (3 if len(counts) > 1 else 0)
+    offsets = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
+    used = int(offsets[-1])
+    x = O.ints(g, (R, K), -3, 3)
+    q = torch.randint(0, 256, (E, M, K // 2), generator=g, dtype=torch.uint8)
+    s = (2.0 ** torch.randint(-2, 2, (E, M, K // group), generator=g)).to(BF)
+    index = torch.randperm(R, generator=g).to(torch.int32) if E > 1 else None
+    src = index.long() if E > 1 else torch.arange(R)
+    ref = O.grouped(x.double(), O.dequantize(q, s), offsets, src, R)[:used].to(BF)
+    s[:, 5] = float("nan")
+    y = torch.full((R, M), 7.0, dtype=BF, device="cuda")
+    kw = dict(offsets=dev(offsets), row_index=dev(index)) if E > 1 else {}
+    moe.moe_qlinear(dev(x), dev(q), dev(s), y, **kw)
+    torch.cuda.synchronize()
+    y = y.cpu()
+    assert y[:used, 5].isnan().all()
+    ref[:, 5] = y[:used, 5] = 0.0
+    assert torch.equal(y[:used], ref)
+    assert (y[used:] == 7.0).all()
+
+
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("swiglu,limit", [(False, 0.0), (True, 0.0), (True, 1.5)])
 @pytest.mark.parametrize("N,E,M", [(1, 1, 256), (9, 1, 256), (130, 1, 256), (40, 8, 256), (30, 1, 16384),
