@@ -5,14 +5,13 @@
 // q holds two 4-bit values a byte, even k in the low half; groups of 32, 64 or 128. With few rows per
 // expert the product is a stream of the weights (half a byte each), so the weights go straight from
 // memory to registers in 16-byte pieces of 32 values, several pieces ahead of their use, and are made
-// into matrix operands with one instruction per value:
-//  - 0x4300 | q is the bfloat16 128 + q, exactly, so two values of a word become a pair with one
-//    and-or: (w & 0x000f000f) | 0x43004300 gives values 0 and 4 of the word, w >> 4 values 1 and 5, ...
-//    (the activations are laid out in LDS in that order);
-//  - the products run on the integers 128 + q, v_mfma_f32_16x16x32_bf16 with float32 sums over one
-//    group; the surplus 136 sum(x) is taken out by one more product with the constant -136 (exact in
-//    bfloat16), shared by all weight tiles of the wave; then the group's sum is scaled in float32 and
-//    added. Neither a weight nor a scaled partial sum is ever rounded to bfloat16.
+// into matrix operands there:
+//  - q - 8 becomes a bfloat16, exactly, in twelve instructions per eight values (unpack8); the activations are
+//    laid out in LDS in the order that this gives the values;
+//  - v_mfma_f32_16x16x32_bf16 sums one group in float32, and the group's sum is scaled in float32 and added.
+//    Neither a weight nor a scaled partial sum is ever rounded to bfloat16, and a weight of 0 adds exactly
+//    nothing, however large its activation. (A cheaper unpacking to 128 + q with 136 sum(x) taken off a group's sum
+//    cancels: beside an activation 10,000 times the others its error was a bfloat16 half step.)
 // A lane's 16 bytes are 32 consecutive k of one weight row. Groups of 128 take them as they are (four
 // matrix steps that each cross the four 32-value pieces); smaller groups first exchange the four words
 // among the four lanes of a row (permlane swaps), so that a step's 32 values are consecutive.
@@ -54,13 +53,25 @@ struct QTile {
   __device__ static int chunk(int rows, int K) { return min(LDS_ / rows / STEP * STEP, (K + STEP - 1) / STEP * STEP); }
 };
 
-// Eight values of a word as bfloat16 128 + q, in the order 0 4 1 5 2 6 3 7: three shifts and four and-ors. The
-// mask comes in a scalar and the exponent in a vector register: one instruction takes no two literals, and
-// with both as constants the compiler emits an and, then an or.
-__device__ inline bf16x8 unpack8(uint32_t w, uint32_t mask, uint32_t magic) {
+// Eight values of a word as the bfloat16 q - 8, exactly, in the order 0 2 4 6 1 3 5 7. First the sign (n: 8 where
+// q < 8) and the magnitude of all eight nibbles at once: where q < 8 the three low bits inverted and one added, 8 - q,
+// elsewhere bit 3 taken off. Then bytes of a sign and four magnitude bits: as e4m3 such a byte is its magnitude times
+// 2^-9 (subnormal up to 7, and linear up to 15), so the conversion of a pair to bfloat16, scaled by 2^9, is exact. The
+// compiler is kept from seeing through n and mag: it then forms n three times (16 instructions; one token,
+// 5,120 -> 24,576: 21 us, 19.5 with 12).
+__device__ inline bf16x8 unpack8(uint32_t w) {
+  uint32_t n = ~w & 0x88888888u;
+  asm("" : "+v"(n));
+  const uint32_t r = n >> 3;
+  uint32_t mag = (w ^ (0x88888888u - r)) + r;  // per nibble: no borrow, no carry
+  asm("" : "+v"(mag));
+  const uint32_t n4 = n << 4, mag4 = mag >> 4;
+  const uint32_t even = (mag & 0x0f0f0f0fu) | (n4 & 0xf0f0f0f0u), odd = (mag4 & 0x0f0f0f0fu) | (n & 0xf0f0f0f0u);
   u32x4 v;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = ((w >> (4 * i)) & mask) | magic;
+  v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.f, false));
+  v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(even, 512.f, true));
+  v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.f, false));
+  v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(odd, 512.f, true));
   return __builtin_bit_cast(bf16x8, v);
 }
 
@@ -107,11 +118,6 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
   // an expert's matrix is below 4 GiB: one scalar base and 32-bit offsets
   const uint8_t* qb = a.q + (int64_t)expert * a.M * (K / 2);
   const uint16_t* sb = a.s + (int64_t)expert * a.M * (K / G);
-  uint32_t mask = 0x000f000fu, magic = 0x43004300u;
-  asm("" : "+s"(mask));  // not constants to the compiler: see unpack8
-  asm("" : "+v"(magic));
-  const u32x4 neg = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};  // -136 as bfloat16 pairs
-  const bf16x8 minus136 = __builtin_bit_cast(bf16x8, neg);
 
   for (int64_t tile0 = (int64_t)blockIdx.z * T::ROWS; tile0 < cnt; tile0 += (int64_t)gridDim.z * T::ROWS) {
     const int rows = (int)min((int64_t)T::ROWS, cnt - tile0);
@@ -180,7 +186,7 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
     load(kw * BATCH);
     for (int c0 = 0; c0 < K; c0 += kc) {
       __syncthreads();  // src_rows is written; the previous chunk's reads are over
-      // stage rows x kc activations (zeros past K), values 0 4 1 5 2 6 3 7 of every eight: a wave takes 512 of one
+      // stage rows x kc activations (zeros past K), values 0 2 4 6 1 3 5 7 of every eight: a wave takes 512 of one
       // row at a time (its row address is scalar), four of these loads ahead of their writes
       const int runs = (kc + 511) / 512;
       int r = 0, run = wave;
@@ -208,10 +214,10 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           u32x4 w;
-          w[0] = __builtin_amdgcn_perm(v[u][2], v[u][0], 0x05040100);
-          w[1] = __builtin_amdgcn_perm(v[u][2], v[u][0], 0x07060302);
-          w[2] = __builtin_amdgcn_perm(v[u][3], v[u][1], 0x05040100);
-          w[3] = __builtin_amdgcn_perm(v[u][3], v[u][1], 0x07060302);
+          w[0] = __builtin_amdgcn_perm(v[u][1], v[u][0], 0x05040100);
+          w[1] = __builtin_amdgcn_perm(v[u][3], v[u][2], 0x05040100);
+          w[2] = __builtin_amdgcn_perm(v[u][1], v[u][0], 0x07060302);
+          w[3] = __builtin_amdgcn_perm(v[u][3], v[u][2], 0x07060302);
           if (to[u] >= 0) *(u32x4*)(xs + to[u]) = w;
         }
       }
@@ -244,16 +250,13 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
             const uint16_t* xp = xs + b0 + p * SEG;
 #pragma unroll
             for (int g = 0; g < GPS; ++g) {
-              f32x4 off[NT];  // -136 sum(x) of the group, the start of every tile's sum
               bf16x8 xf[STEPS][NT];
 #pragma unroll
               for (int i = 0; i < NT; ++i) {
-                off[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int u = 0; u < STEPS; ++u) {
                   const int piece = G < SEG ? 4 * (g * STEPS + u) + j : 4 * j + u;
                   xf[u][i] = *(const bf16x8*)(xp + min(16 * i + r16, rows - 1) * pitch + piece * 8);
-                  off[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], minus136, off[i], 0, 0, 0);
                 }
               }
 #pragma unroll
@@ -261,10 +264,11 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
                 f32x4 sum[NT];
 #pragma unroll
                 for (int u = 0; u < STEPS; ++u) {
-                  const bf16x8 w = unpack8(cq[t][p][g * STEPS + u], mask, magic);
+                  const bf16x8 w = unpack8(cq[t][p][g * STEPS + u]);
 #pragma unroll
                   for (int i = 0; i < NT; ++i)
-                    sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, u == 0 ? off[i] : sum[i], 0, 0, 0);
+                    sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, u == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[i],
+                                                                     0, 0, 0);
                 }
                 const uint32_t sw = cs[t][(p * GPS + g) / 2];
                 const float s = __uint_as_float((p * GPS + g) & 1 ? sw & 0xffff0000u : sw << 16);
@@ -355,11 +359,6 @@ __device__ __forceinline__ void wide_tile(const QuantArgs& a, int expert, int64_
   const int col0 = (blockIdx.x * 4 + wave) * WCOLS;
   const uint8_t* qb = a.q + (int64_t)expert * a.M * (K / 2);
   const uint16_t* sb = a.s + (int64_t)expert * a.M * (K / G);
-  uint32_t mask = 0x000f000fu, magic = 0x43004300u;
-  asm("" : "+s"(mask));  // not constants to the compiler: see unpack8
-  asm("" : "+v"(magic));
-  const u32x4 neg = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};  // -136 as bfloat16 pairs
-  const bf16x8 minus136 = __builtin_bit_cast(bf16x8, neg);
   const int stages = (K + STAGE - 1) / STAGE;
   int ln = lane;
   asm volatile("" : "+v"(ln));  // what depends on the lane stays inside the tile
@@ -397,17 +396,17 @@ __device__ __forceinline__ void wide_tile(const QuantArgs& a, int expert, int64_
     for (int i = 0; i < XL; ++i)
       xv[i] = *(const u32x4*)(a.x + (int64_t)src_rows[h * (ROWS / 2) + 8 * i + xr] * K + k);
   };
-  // zeros past K; values 0 4 1 5 2 6 3 7 of every eight
+  // zeros past K; values 0 2 4 6 1 3 5 7 of every eight
   auto put_x = [&](int stage, int h) {
     const bool in = stage * STAGE + xk < K;
 #pragma unroll
     for (int i = 0; i < XL; ++i) {
       u32x4 v = xv[i], w;
       if (!in) v = u32x4{0, 0, 0, 0};
-      w[0] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100);
-      w[1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302);
-      w[2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100);
-      w[3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302);
+      w[0] = __builtin_amdgcn_perm(v[1], v[0], 0x05040100);
+      w[1] = __builtin_amdgcn_perm(v[3], v[2], 0x05040100);
+      w[2] = __builtin_amdgcn_perm(v[1], v[0], 0x07060302);
+      w[3] = __builtin_amdgcn_perm(v[3], v[2], 0x07060302);
       *(u32x4*)&lds[((stage & 1) * ROWS + h * (ROWS / 2) + 8 * i + xr) * PITCH + xk] = w;
     }
   };
@@ -458,27 +457,39 @@ __device__ __forceinline__ void wide_tile(const QuantArgs& a, int expert, int64_
       const uint16_t* xp = &lds[((st & 1) * ROWS + r16) * PITCH + h * SEG];
 #pragma unroll
       for (int g = 0; g < GPS; ++g) {
-        f32x4 off[TT];  // -136 sum(x) of the group, the start of every tile's sum
         bf16x8 xf[STEPS][TT];
 #pragma unroll
         for (int i = 0; i < TT; ++i) {
-          off[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int u = 0; u < STEPS; ++u) {
             const int piece = G < SEG ? 4 * (g * STEPS + u) + j : 4 * j + u;
             xf[u][i] = *(const bf16x8*)(xp + 16 * i * PITCH + piece * 8);
-            off[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], minus136, off[i], 0, 0, 0);
           }
         }
+        // the next word is unpacked under the present one's products; with groups of 128 (four steps per sum) the
+        // order is set, a product and then a share of the unpacking: with one wave per SIMD nothing else fills the
+        // matrix core's time (128 rows, 5,120 -> 24,576: 73 -> 63 us). With fewer steps the compiler's own order is
+        // faster (512 rows, 12,288 -> 5,120, groups of 64: 152 us, 184 with the order set).
+        bf16x8 next = unpack8(q[h][0][g * STEPS]);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           f32x4 sum[TT];
 #pragma unroll
           for (int u = 0; u < STEPS; ++u) {
-            const bf16x8 w = unpack8(q[h][t][g * STEPS + u], mask, magic);
+            const bf16x8 w = next;
+            const int n = t * STEPS + u + 1;
+            if (n < RT * STEPS) next = unpack8(q[h][n / STEPS][g * STEPS + n % STEPS]);
 #pragma unroll
             for (int i = 0; i < TT; ++i)
-              sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, u == 0 ? off[i] : sum[i], 0, 0, 0);
+              sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[u][i], w, u == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : sum[i], 0,
+                                                               0, 0);
+            if (G == SEG) {
+#pragma unroll
+              for (int i = 0; i < TT; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);        // matrix instructions
+                __builtin_amdgcn_sched_group_barrier(0x002, 12 / TT, 0);  // vector ones
+              }
+            }
           }
           const uint32_t sw = sc[h][t][g / 2];
           const float s = __uint_as_float(g & 1 ? sw & 0xffff0000u : sw << 16);
@@ -514,9 +525,11 @@ __device__ __forceinline__ void wide_tile(const QuantArgs& a, int expert, int64_
 
 // EXPERTS: a tile of at most 32 rows runs a body of its own (256 experts 6,144 -> 4,096, 24 / 64 rows each: 1,480 ->
 // 1,379, 2,527 -> 2,412 us). A dense product has at most one such tile and keeps one body, which takes fewer
-// registers (12,288 -> 5,120, 1,021 rows: 231 us, 239 with both); so does the form that both would make spill.
+// registers (12,288 -> 5,120, 1,021 rows: 231 us, 239 with both); so does the form that both would make spill. Two
+// waves per SIMD at most: where a form's registers allow three blocks per CU, they push each other's weights out of L2
+// (256 experts 6,144 -> 4,096, groups of 32, 32 rows each: 1,628 us, 1,940 with three).
 template <int TT, int G, bool SWIGLU, bool EXPERTS>
-__global__ __launch_bounds__(256, 2) void qlinear_wide_kernel(QuantArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void qlinear_wide_kernel(QuantArgs a) {
   constexpr int ROWS = 16 * TT;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * ROWS * (2 * SEG + 8)];
   __shared__ int src_rows[ROWS];

@@ -1,0 +1,74 @@
+"""4-bit products beside large activations: the sums are those of x (q - 8), so a weight of 0 (q = 8) adds nothing
+whatever its activation, and the error of a row is that of float32 sums of the products themselves."""
+import pytest
+import torch
+
+import sparse_moe_layer_gate_amd as moe
+from tests import _ops as O
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+FORMS = ["16 rows", "32 rows", "64 rows", "48 rows", "experts", "experts few"]
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+def case(form, group, seed):
+    """x, q, s, the rows' sources and the call's lists, of sizes that run the named form."""
+    counts, M = {"16 rows": ([5], 192), "32 rows": ([40], 16384), "64 rows": ([150], 16384), "48 rows": ([390], 5120),
+                 "experts": ([0, 1, 15, 31, 33, 47, 49, 64, 65, 129] * 4, 1280), "experts few": ([0, 3, 1, 9] * 16, 256)}[form]
+    E, R, K = len(counts), sum(counts), 384
+    g = torch.Generator().manual_seed(seed)
+    offsets = torch.tensor([0] + counts, dtype=torch.int32).cumsum(0).to(torch.int32)
+    index = torch.randperm(R, generator=g).to(torch.int32) if E > 1 else None
+    x = torch.randn((R, K), generator=g).to(BF)
+    q = torch.randint(0, 256, (E, M, K // 2), generator=g, dtype=torch.uint8)
+    s = (torch.rand((E, M, K // group), generator=g) + 0.5).mul(0.01).to(BF)
+    return offsets, index, x, q, s
+
+
+def product(offsets, index, x, q, s):
+    R = x.shape[0]
+    y = torch.full((R, q.shape[1]), 7.0, dtype=BF, device="cuda")
+    kw = dict(offsets=dev(offsets), row_index=dev(index)) if index is not None else {}
+    moe.moe_qlinear(dev(x), dev(q), dev(s), y, **kw)
+    torch.cuda.synchronize()
+    return y.cpu()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_zero_weights_add_nothing(form, group):
+    """Two features whose weights are all 0: their activations, up to bfloat16's largest, leave every bit as it is."""
+    print(f"[zero weights] {form} group={group}", flush=True)
+    offsets, index, x, q, s = case(form, group, 31)
+    q[..., 50 // 2] = (q[..., 50 // 2] & 0xf0) | 8    # feature 50 (low half)
+    q[..., 301 // 2] = (q[..., 301 // 2] & 0x0f) | 0x80  # feature 301 (high half)
+    out = []
+    for big in (0.0, 2.0 ** 20, -float(torch.finfo(BF).max)):
+        x[:, 50], x[:, 301] = big, big
+        out.append(product(offsets, index, x, q, s))
+    assert torch.isfinite(out[0].float()).all()
+    assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+
+
+@pytest.mark.parametrize("outlier", [1.0, 1e4, 1e6])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_error_of_float32_sums(form, group, outlier):
+    """One feature's activations `outlier` times the others'. Bound: a group's float32 sum (one step of 2^-23 per term,
+    if the matrix core's additions are cut rather than rounded), its scaling, and the sum over the groups, each of the
+    products' magnitudes; then the output's rounding."""
+    print(f"[outliers] {form} group={group} outlier={outlier}", flush=True)
+    offsets, index, x, q, s = case(form, group, 32)
+    x[:, 77] = (x[:, 77].float() * outlier).to(BF)
+    K = x.shape[1]
+    y = product(offsets, index, x, q, s)
+    w = O.dequantize(q, s)
+    src = index.long() if index is not None else torch.arange(x.shape[0])
+    ref = O.grouped(x.double(), w, offsets, src, x.shape[0])
+    mag = O.grouped(x.double().abs(), w.abs(), offsets, src, x.shape[0])
+    O.check("y", y, ref, (2 * group + K / group + 4) * O.U32 * mag)
