@@ -632,29 +632,33 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ w, 
 }  // namespace
 
 // Which form runs, by the average rows per expert r and the blocks a form makes (256 CUs). Measured, us, on
-// dense 12,288 -> 5,120 (groups of 64), dense 5,120 -> 24,576 and 256 experts 6,144 -> 4,096 with eight rows a
-// token (SwiGLU, groups of 128 and 32):
-//   narrow, 16 rows, k over four waves      1 / 64 / 128 rows: 18 / 63 / 104 | 22 / 91 / 177 | 32 tokens: 467
-//   middle, 32 rows, k over two waves       29 / 57 / 95                     | 20 / 50 / 94  | 446
-//   wide, 64 or 48 rows, all of k per wave  98 / 153 / 151                   | 46 / 54 / 58  | 675
-// The narrow form reads the activations most often but makes the most and shortest blocks: it wins while the
-// middle form makes fewer than one block per CU. The wide form shares each unpacked value among 48 or 64 rows. For
+// dense 12,288 -> 5,120 (groups of 64), dense 5,120 -> 24,576 (SwiGLU, groups of 128) and 256 experts 6,144 -> 4,096
+// with eight rows a token (SwiGLU, groups of 32):
+//   narrow, 16 rows, k over four waves      1 / 64 / 128 rows: 17 / 59 / 95 | 16 / 79 / 144 | 1 / 32 / 256 tokens: 36 / 435 / 1,006
+//   middle, 32 rows, k over two waves       28 / 85 / 99                    | 20 / 52 / 96  | 41 / 447 / 904
+//   wide, 64 or 48 rows, all of k per wave  149 / 150 / 149                 | 52 / 55 / 62  | 121 / 736 / 1,163
+// The narrow form reads the activations most often but makes the most and shortest blocks. It wins while the middle
+// form makes fewer than one block per CU (experts without rows make none that count), and for up to 16 rows in all,
+// when no expert has more than one of its tiles, unless k is shorter than two of its steps of 1,024 (16 rows,
+// narrow / middle: 12,288 -> 16,384 47 / 54, 4,096 -> 16,384 20 / 22; 1 row, 4,096 -> 16,384 12 / 15; one token, 128
+// experts 4,096 -> 2,816 19 / 25 and 1,408 -> 4,096 15 / 14). The wide form shares each unpacked value among 48 or 64 rows. For
 // a dense product it wins from about 96 rows on, once it makes blocks for five eighths of the CUs (12,288 -> 5,120,
-// middle / wide: 256 rows, 120 blocks, 118 / 152; 384 rows, 160 blocks, 178 / 150; 512 rows 195 / 150). For experts it
-// wins from 24 rows each (128 experts 1,408 -> 4,096, 24 / 32 rows: 191 / 155, 222 / 169; of 256 experts 6,144 -> 4,096
-// with groups of 32 from 32: 1,387 / 1,465, 1,692 / 1,653).
+// middle / wide: 256 rows, 120 blocks, 122 / 148; 384 rows, 160 blocks, 180 / 149; 512 rows 200 / 150). For experts it
+// wins from 24 rows each (128 experts 1,408 -> 4,096, 24 rows: 195 / 154; of 256 experts 6,144 -> 4,096 with groups of
+// 32 24 rows 1,427 / 1,433, 32 rows 1,736 / 1,643).
 // Of its two heights a dense product takes the one whose last round of blocks leaves less idle (1,021 rows,
-// 12,288 -> 5,120: 264 with 64 rows, 231 with 48; 768 rows 180 and 228), experts the lower one up to 64 rows each
-// (128 experts, 24 / 64 / 128 rows: 165 / 260 / 396 with 64 rows, 155 / 237 / 414 with 48).
+// 12,288 -> 5,120: 262 with 64 rows, 235 with 48; 768 rows 168 and 235), experts the lower one up to 64 rows each
+// (128 experts, 24 / 64 / 128 rows: 147 / 241 / 371 with 64 rows, 154 / 238 / 431 with 48).
 hipError_t launch_qlinear(const QuantArgs& a, hipStream_t s) {
   constexpr int64_t kCus = 256;
   auto up = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
-  const int64_t r = up(a.R, a.E);
+  const int64_t r = up(a.R, a.E), live = a.R < a.E ? a.R : a.E;  // live: experts with rows, at most
   const int64_t blocks64 = up(a.M, 256) * a.E * up(r, 64), blocks48 = up(a.M, 256) * a.E * up(r, 48);
   const bool low = a.E > 1 ? r <= 64 : up(blocks48, kCus) * 3 < up(blocks64, kCus) * 4;
   if (a.K >= SEG && r >= (a.E > 1 ? 24 : 96) && (low ? blocks48 : blocks64) * 8 >= kCus * 5)
     return low ? launch_wide<3>(a, s) : launch_wide<4>(a, s);
-  if (up(a.M, 64) * a.E * up(r, 32) >= kCus) return launch_group<QTile<2, 2, 2, 2, 16384, 3>>(a, s);
+  const bool few = a.R <= 16 && a.K >= 2048;
+  if (!few && up(a.M, 64) * live * up(r, 32) >= kCus) return launch_group<QTile<2, 2, 2, 2, 16384, 3>>(a, s);
   return launch_group<QTile<1, 4, 2, 2, 16384, 4>>(a, s);
 }
 
