@@ -317,7 +317,8 @@ moe_status moe_grouped_linear_wgrad(int32_t E, int64_t R, int32_t in, int32_t ou
 /* moe_grouped_linear with 4-bit weights and one scale per group of a weight row:
  *   W[e, m, i] = (q[e, m, i] - 8) * scales[e, m, i / group],   q in 0..15
  *   wq      [E, out, in / 2] uint8: two values a byte, even i in the low four bits
- *   scales  [E, out, in / group] bf16, finite; group 32, 64 or 128, dividing in
+ *   scales  [E, out, in / group] bf16 (one that is not finite shows in the outputs of its weight row, in no other);
+ *           group 32, 64 or 128, dividing in
  *   x, y    bf16; x, x_rows, row_index, index_div, offsets, rows as for moe_grouped_linear. With E = 1 offsets
  *           may be NULL: all R rows (a plain 4-bit linear map).
  *   swiglu  1: the rows of W are [0, out / 2) gate and [out / 2, out) up, and y [R, out / 2] is
@@ -332,7 +333,8 @@ moe_status moe_qlinear(int32_t E, int64_t R, int32_t in, int32_t out, int32_t gr
 
 /* Weights for moe_qlinear from w [rows, in] of dtype (rows = E * out): scale = bf16(max|w| / 7) over each
  * group, q = 8 + the nearest integer (ties to even) of the float32 quotient w / scale, kept in 0..15; a
- * group of zeros has scale 0 and q = 8. */
+ * group whose scale is 0 has q = 8. w need not be finite: a group that holds a NaN has the scale NaN, any other that
+ * holds an infinity the scale infinity, and q = 8, so that every product with the group is NaN. */
 moe_status moe_quantize(int32_t dtype, int64_t rows, int32_t in, int32_t group, const void* w, void* wq, void* scales,
                         void* stream);
 

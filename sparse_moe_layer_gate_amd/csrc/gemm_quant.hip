@@ -604,7 +604,9 @@ hipError_t launch_group(const QuantArgs& a, hipStream_t s) {
 
 // One thread per eight values, group / 8 neighbouring lanes per group: the group's largest magnitude over
 // 7, rounded to bfloat16, is the scale; a value is the nearest integer (ties to even) of its quotient by
-// that scale, kept within [-8, 7]. A group of zeros has the scale 0 and the values 0.
+// that scale, kept within [-8, 7]. A group of zeros has the scale 0 and the values 0. The largest magnitude is taken of
+// the bits, where a NaN is above an infinity and that above every number, so that a group with either has it as its
+// scale and shows in every product; its values are 0.
 template <typename T>
 __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ w, int64_t pieces, int lanes_per_group,
                                                        uint32_t* __restrict__ q, uint16_t* __restrict__ s) {
@@ -612,16 +614,17 @@ __global__ __launch_bounds__(256) void quantize_kernel(const T* __restrict__ w, 
   const bool live = i < pieces;
   float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (live) widen8(raw_load8(w + i * 8), f);
-  float m = 0.f;
+  int m = 0;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) m = fmaxf(m, fabsf(f[u]));
-  for (int off = 1; off < lanes_per_group; off <<= 1) m = fmaxf(m, __shfl_xor(m, off));
-  const uint16_t sb = (uint16_t)bf16_pair(m / 7.0f, 0.f);
+  for (int u = 0; u < 8; ++u) m = max(m, __float_as_int(f[u]) & 0x7fffffff);
+  for (int off = 1; off < lanes_per_group; off <<= 1) m = max(m, __shfl_xor(m, off));
+  const uint16_t sb = (uint16_t)bf16_pair(__int_as_float(m) / 7.0f, 0.f);
   const float sf = bf16_f32(sb);
+  const bool usable = sf > 0.f && sf < __builtin_inff();
   uint32_t word = 0;
 #pragma unroll
   for (int u = 0; u < 8; ++u) {
-    const float v = sf > 0.f ? fminf(fmaxf(rintf(f[u] / sf), -8.f), 7.f) : 0.f;
+    const float v = usable ? fminf(fmaxf(rintf(f[u] / sf), -8.f), 7.f) : 0.f;
     word |= (uint32_t)((int)v + 8) << (4 * u);
   }
   if (!live) return;

@@ -72,3 +72,47 @@ def test_error_of_float32_sums(form, group, outlier):
     ref = O.grouped(x.double(), w, offsets, src, x.shape[0])
     mag = O.grouped(x.double().abs(), w.abs(), offsets, src, x.shape[0])
     O.check("y", y, ref, (2 * group + K / group + 4) * O.U32 * mag)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_quantize_shows_nan_and_infinity(group, dtype):
+    """A NaN (of either sign, at any place of the group) or an infinity becomes the group's scale; the other groups are
+    quantised as without it, and a product shows it in the rows of that weight alone."""
+    K, rows = 512, 64
+    g = torch.Generator().manual_seed(33)
+    w = torch.randn((1, rows, K), generator=g).to(dtype)
+    clean_q, clean_s = moe.moe_quantize(dev(w), group)
+    bad = w.clone()
+    inf, nan = float("inf"), float("nan")
+    at = {3: (0, nan), 10: (group - 1, -nan), 20: (group // 2, inf), 33: (7, -inf), 40: (5, nan), 41: (1, inf)}
+    for row, (k, v) in at.items():
+        bad[0, row, group + k] = v        # the row's second group
+    bad[0, 40, group + 6] = inf           # beside a NaN
+    bad[0, 41, group:2 * group] = inf     # nothing else
+    q, s = moe.moe_quantize(dev(bad), group)
+    sc, qc = s.cpu().float()[0], q.cpu()[0]
+    for row, (_, v) in at.items():
+        assert (sc[row, 1].isnan() if v != v else sc[row, 1] == inf), (row, sc[row, 1])
+        assert (qc[row, group // 2:group] == 0x88).all(), row
+    same_s, same_q = s.clone(), q.clone()
+    for row in at:
+        same_s[0, row, 1] = clean_s[0, row, 1]
+        same_q[0, row, group // 2:group] = clean_q[0, row, group // 2:group]
+    assert torch.equal(same_s, clean_s) and torch.equal(same_q, clean_q)
+    x = torch.randn((3, K), generator=g).to(BF)
+    y, ref = (torch.empty((3, rows), dtype=BF, device="cuda") for _ in range(2))
+    moe.moe_qlinear(dev(x), q, s, y)
+    moe.moe_qlinear(dev(x), clean_q, clean_s, ref)
+    hit = torch.zeros(rows, dtype=torch.bool)
+    hit[list(at)] = True
+    assert y.cpu()[:, hit].isnan().all()
+    assert torch.equal(y.cpu()[:, ~hit], ref.cpu()[:, ~hit])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quantize_group_whose_scale_vanishes(dtype):
+    """Magnitudes so small that a seventh of them rounds to 0 in bfloat16: scale 0, q = 8."""
+    w = torch.full((2, 64), float(torch.finfo(torch.bfloat16).smallest_normal) / 128, dtype=dtype)  # the least bfloat16
+    q, s = moe.moe_quantize(dev(w), 32)
+    assert (s.cpu() == 0).all() and (q.cpu() == 0x88).all()
