@@ -242,7 +242,8 @@ moe_status moe_dense_forward(int64_t N, int32_t D, int32_t dff, int32_t dtype, f
  *   gate    [ceil(N / gate_rows), D] of dtype: row n uses gate row n / gate_rows (gate_rows >= N: one row
  *           for all; 1: a row per token; a sequence's length: one per sequence)
  * Float32 arithmetic; h_out and u are each rounded once, u from the unrounded h_out. h_out may be h
- * (in place); no other overlap. D: a multiple of 64, at most 16384. N = 0 launches nothing. */
+ * (in place); no other overlap. D: a multiple of 64, at most 16384. N below 2^31, and N * T below 2^32 with T the
+ * threads of a row: D / 8 (D / 16 above 8192), rounded up to a multiple of 64. N = 0 launches nothing. */
 moe_status moe_block_norm(int64_t N, int32_t D, int32_t dtype, float eps, float residual_scale, const void* h,
                           const void* o, const void* w_post, const void* gate, int64_t gate_rows, const void* w_pre,
                           void* h_out, void* u, void* stream);
@@ -256,8 +257,8 @@ moe_status moe_block_norm(int64_t N, int32_t D, int32_t dtype, float eps, float 
  *           sums over rows in a fixed order
  *   workspace: at least moe_block_norm_workspace_size(N, D, dtype, gate ? gate_rows : 0) bytes (may be NULL
  *           when no sum is wanted). The size never falls as N grows.
- * dh may be dh_out (in place); no other overlap. residual_scale has no gradient. N = 0 writes zeros to
- * dw_post and dw_pre. */
+ * dh may be dh_out (in place); no other overlap. residual_scale has no gradient. N below 2^31. N = 0 writes zeros
+ * to dw_post and dw_pre. */
 size_t moe_block_norm_workspace_size(int64_t N, int32_t D, int32_t dtype, int64_t gate_rows);
 moe_status moe_block_norm_backward(int64_t N, int32_t D, int32_t dtype, float eps, float residual_scale,
                                    const void* h_out, const void* o, const void* w_post, const void* gate,
@@ -270,7 +271,8 @@ moe_status moe_block_norm_backward(int64_t N, int32_t D, int32_t dtype, float ep
  *   rows [R, D], shared [N, D] or NULL, y [N, D] of dtype; inv_row [N, k] int32 as moe_dispatch writes it;
  *   topk_w [N, k] float32 or NULL (all 1: the gradient of a gathered token is the sum of its rows').
  * Slots whose entry is outside [0, R) add nothing. Float32 sums in slot order, one rounding. y may be
- * shared (in place) but not rows. k: 1..32; D: a multiple of 64. N = 0 launches nothing. */
+ * shared (in place) but not rows. k: 1..32; D: a multiple of 64; N k and R below 2^31, and N * T below 2^32 with T
+ * the threads of a token: D / 8 rounded up to a multiple of 64, at most 1024. N = 0 launches nothing. */
 moe_status moe_combine(int64_t N, int32_t k, int32_t D, int32_t dtype, const void* rows, int64_t R,
                        const int32_t* inv_row, const float* topk_w, const void* shared, float alpha, void* y,
                        void* stream);
@@ -280,7 +282,7 @@ moe_status moe_combine(int64_t N, int32_t k, int32_t D, int32_t dtype, const voi
  *   dtopk_w[n, s]        = alpha * <dy[n], rows[inv_row[n, s]]>   (float32; 0 for an empty slot)
  * The entries of inv_row inside [0, R) are distinct, as moe_dispatch writes them; rows that no slot names
  * are left as they were. dtopk_w may be NULL (not wanted; rows may then be NULL too) and is NULL without
- * topk_w. The gradient of shared is dy. drows overlaps neither dy nor rows. */
+ * topk_w. The gradient of shared is dy. drows overlaps neither dy nor rows. Sizes as for moe_combine. */
 moe_status moe_combine_backward(int64_t N, int32_t k, int32_t D, int32_t dtype, const void* dy, const void* rows,
                                 int64_t R, const int32_t* inv_row, const float* topk_w, float alpha, void* drows,
                                 float* dtopk_w, void* stream);
@@ -300,8 +302,9 @@ moe_status moe_combine_backward(int64_t N, int32_t k, int32_t D, int32_t dtype, 
  * topk_w == NULL. Offsets and indices are read on the device and kept in range there: offsets outside [0, R]
  * or out of order and indices outside [0, x_rows * index_div) give unspecified values, never an access
  * outside the buffers. Float32 sums over the whole reduction, one rounding. E: 1..512; in and out:
- * multiples of 64 up to 2^22, in * out below 2^31; bf16: gathered x below 4 GiB. R = 0 launches nothing (wgrad: writes
- * zeros). No overlap between an output and an input. */
+ * multiples of 64 up to 2^22, in * out below 2^31; bf16: gathered x below 4 GiB; R below 2^31.
+ * Calls whose tiles would take a launch of 2^32 threads are MOE_ERR_UNSUPPORTED (float32: 2^24 tiles of 128 x 128).
+ * R = 0 launches nothing (wgrad: writes zeros). No overlap between an output and an input. */
 size_t moe_grouped_workspace_size(int32_t E, int64_t R, int32_t dtype);
 moe_status moe_grouped_linear(int32_t E, int64_t R, int32_t in, int32_t out, int32_t dtype, const void* x,
                               int64_t x_rows, const int32_t* row_index, int32_t index_div, const void* w,
@@ -334,7 +337,8 @@ moe_status moe_qlinear(int32_t E, int64_t R, int32_t in, int32_t out, int32_t gr
 /* Weights for moe_qlinear from w [rows, in] of dtype (rows = E * out): scale = bf16(max|w| / 7) over each
  * group, q = 8 + the nearest integer (ties to even) of the float32 quotient w / scale, kept in 0..15; a
  * group whose scale is 0 has q = 8. w need not be finite: a group that holds a NaN has the scale NaN, any other that
- * holds an infinity the scale infinity, and q = 8, so that every product with the group is NaN. */
+ * holds an infinity the scale infinity, and q = 8, so that every product with the group is NaN. in: a multiple of 64
+ * and of group; rows * in at most 2^35 - 2^11. */
 moe_status moe_quantize(int32_t dtype, int64_t rows, int32_t in, int32_t group, const void* w, void* wq, void* scales,
                         void* stream);
 

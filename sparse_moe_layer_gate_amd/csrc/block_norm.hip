@@ -445,6 +445,8 @@ hipError_t backward_t(const NormCall& c, hipStream_t s) {
 
 }  // namespace
 
+int norm_forward_threads(int D) { return shape_of(D, 1024).threads; }
+
 // Runs of the backward pass: eight waves per CU (256 CUs). More runs mean more partial rows (three of D floats
 // per run) to write and add: 4,096 x 4,096 with 256 / 512 runs 51 / 59 us.
 int64_t norm_runs(int D) {

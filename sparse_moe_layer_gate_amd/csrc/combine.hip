@@ -200,12 +200,12 @@ __global__ __launch_bounds__(1024) void combine_rows_backward_kernel(const T* __
   }
 }
 
+}  // namespace
+
 int combine_threads(int D) {
   const int threads = (D / 8 + 63) / 64 * 64;
   return threads > 1024 ? 1024 : threads;
 }
-
-}  // namespace
 
 hipError_t launch_combine_rows(int dtype, const void* rows, int64_t R, const int32_t* inv_row, const float* w,
                                const void* shared, int64_t N, int k, int D, float alpha, void* y, hipStream_t s) {

@@ -914,13 +914,16 @@ hipError_t launch_grouped_join(GroupedMode mode, int dtype, const GradArgs& a, h
   return hipGetLastError();
 }
 
+int64_t grouped_f32_blocks(GroupedMode mode, int E, int M, int K, int splits, int64_t max_tile_count) {
+  const int64_t cols = ((mode == GM_FWD ? M : K) + 127) / 128;
+  const int64_t blocks = (mode == GM_WGRAD ? (int64_t)E * ((M + 127) / 128) : max_tile_count) * cols * splits;
+  return mode == GM_WGRAD ? blocks : (blocks + 7) / 8 * 8;
+}
+
 hipError_t launch_grouped_f32(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s) {
   const int cols = ((mode == GM_FWD ? a.M : a.K) + 127) / 128;
-  const int64_t tiles = mode == GM_WGRAD ? (int64_t)a.E * ((a.M + 127) / 128) : max_tile_count;
-  int64_t blocks = tiles * cols * a.splits;
-  if (mode != GM_WGRAD) blocks = (blocks + 7) / 8 * 8;
+  const int64_t blocks = grouped_f32_blocks(mode, a.E, a.M, a.K, a.splits, max_tile_count);
   if (blocks == 0) return hipSuccess;
-  if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
   // Groups of few rows on average: most of a 128-row tile is empty, and the form that skips its empty row tiles wins
   // up to about 32 rows per group (60 experts, 704 -> 1,024, us with / without: fwd of 8 / 16 / 32 / 40 rows 54 / 113,

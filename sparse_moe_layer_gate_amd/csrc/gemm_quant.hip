@@ -670,7 +670,6 @@ hipError_t launch_quantize(int dtype, const void* w, int64_t rows, int K, int gr
   const int64_t pieces = rows * (K / 8);
   const int64_t blocks = (pieces + 255) / 256;
   if (blocks == 0) return hipSuccess;
-  if (blocks >= (int64_t)1 << 31) return hipErrorInvalidValue;
   if (dtype == MOE_F32)
     hipLaunchKernelGGL(quantize_kernel<float>, dim3((unsigned)blocks), dim3(256), 0, st, (const float*)w, pieces,
                        group / 8, (uint32_t*)q, s);

@@ -37,7 +37,7 @@ moe_status check_cfg(const moe_config* c) {
 moe_status check_n(const moe_config* c, int64_t N) {
   if (N < 0) return MOE_ERR_INVALID_ARG;
   // row positions (N k routed + N shared) and token ids are int32
-  if (N * (int64_t)(c->num_experts_per_tok + 1) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
+  if (N >= (int64_t)1 << 31 || N * (int64_t)(c->num_experts_per_tok + 1) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -21,6 +21,8 @@ bool all_aligned16(P... p) {
   return (aligned16(p) && ...);
 }
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
+// A launch holds fewer than 2^32 threads: what would take more is refused here, before anything is launched.
+bool launch_fits(int64_t blocks, int64_t threads) { return blocks <= (kGiB4 - 1) / threads; }
 bool dtype_ok(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
 
 moe_status check_norm(int64_t N, int32_t D, int32_t dtype, float eps, float a) {
@@ -40,7 +42,8 @@ int64_t norm_blocks_bound(int64_t N, int D, bool gate) {
 
 moe_status check_combine(int64_t N, int32_t k, int32_t D, int32_t dtype, int64_t R, float alpha) {
   if (N < 0 || k < 1 || D < 1 || R < 0 || !dtype_ok(dtype) || !std::isfinite(alpha)) return MOE_ERR_INVALID_ARG;
-  if (k > kMaxK || D % 64 != 0 || N * k >= kInt31 || R >= kInt31) return MOE_ERR_UNSUPPORTED;
+  if (k > kMaxK || D % 64 != 0 || N >= kInt31 || N * k >= kInt31 || R >= kInt31) return MOE_ERR_UNSUPPORTED;
+  if (!launch_fits(N, combine_threads(D))) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -127,6 +130,7 @@ moe_status moe_block_norm(int64_t N, int32_t D, int32_t dtype, float eps, float 
   const moe_status st = check_norm(N, D, dtype, eps, residual_scale);
   if (st != MOE_OK) return st;
   if (gate && gate_rows < 1) return MOE_ERR_INVALID_ARG;
+  if (!launch_fits(N, norm_forward_threads(D))) return MOE_ERR_UNSUPPORTED;
   if (N == 0) return MOE_OK;
   if (!h || (!o && (w_post || gate || h_out)) || (o && !h_out)) return MOE_ERR_INVALID_ARG;
   if ((w_pre == nullptr) != (u == nullptr) || (!o && !w_pre)) return MOE_ERR_INVALID_ARG;
@@ -245,6 +249,11 @@ moe_status moe_grouped_linear(int32_t E, int64_t R, int32_t in, int32_t out, int
   if (R == 0) return MOE_OK;
   if (!x || !w || !offsets || !y || x == y || !all_aligned16(x, w, y)) return MOE_ERR_INVALID_ARG;
   const GroupedLayout L = grouped_layout(E, R, dtype);
+  const int splits = dtype == MOE_F32 ? grouped_splits(GM_FWD, dtype, E, R, out, in, L.part_bytes) : 1;
+  // (the 16-row form of the expert GEMMs takes 128 columns per block; the others launch one block per CU)
+  if (dtype == MOE_F32 ? !launch_fits(grouped_f32_blocks(GM_FWD, E, out, in, splits, L.max_tiles0), 256)
+                       : L.bm0 == 16 && !launch_fits(L.max_tiles0 * ((out + 127) / 128) + 7, 256))
+    return MOE_ERR_UNSUPPORTED;
   if (!workspace || ws_bytes < L.total || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   void* ws = workspace;
@@ -258,7 +267,7 @@ moe_status moe_grouped_linear(int32_t E, int64_t R, int32_t in, int32_t out, int
                                                 x_rows, src, ntiles + 20, s));
   if (dtype == MOE_F32) {
     const GradArgs g{x, w, y, R, out, in, E, offsets, src, x_rows, t0.tiles, ntiles, nullptr,
-                     grouped_splits(GM_FWD, dtype, E, R, out, in, L.part_bytes), at<float>(ws, L.part), ntiles + 20};
+                     splits, at<float>(ws, L.part), ntiles + 20};
     MOE_TRY(ST_GROUPED_LINEAR, launch_grouped_f32(GM_FWD, g, L.max_tiles0, s));
     if (g.splits > 1) MOE_TRY(ST_GROUPED_LINEAR, launch_grouped_join(GM_FWD, dtype, g, s));
     return MOE_OK;
@@ -288,6 +297,9 @@ moe_status moe_grouped_linear_dgrad(int32_t E, int64_t R, int32_t in, int32_t ou
   if (R == 0) return MOE_OK;
   if (!dy || !w || !offsets || !dx || dy == dx || !all_aligned16(dy, w, dx)) return MOE_ERR_INVALID_ARG;
   const GroupedLayout L = grouped_layout(E, R, dtype);
+  const int splits = grouped_splits(GM_DGRAD, dtype, E, R, out, in, L.part_bytes);
+  if (dtype == MOE_F32 && !launch_fits(grouped_f32_blocks(GM_DGRAD, E, out, in, splits, L.max_tiles1), 256))
+    return MOE_ERR_UNSUPPORTED;
   if (!workspace || ws_bytes < L.total || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   void* ws = workspace;
@@ -296,7 +308,7 @@ moe_status moe_grouped_linear_dgrad(int32_t E, int64_t R, int32_t in, int32_t ou
   const TileSpec t0{L.bm1, at<Tile>(ws, L.tiles0), ntiles, small_expert_rows(dtype, L.bm1), ntiles + 2, ntiles + 18};
   MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, t0, none, 0, nullptr, 1, 0, nullptr, ntiles + 20, s));
   const GradArgs g{dy, w, dx, R, out, in, E, offsets, nullptr, 0, t0.tiles, ntiles, ntiles + 2,
-                   grouped_splits(GM_DGRAD, dtype, E, R, out, in, L.part_bytes), at<float>(ws, L.part), ntiles + 20};
+                   splits, at<float>(ws, L.part), ntiles + 20};
   MOE_TRY(ST_GROUPED_LINEAR, dtype == MOE_F32 ? launch_grouped_f32(GM_DGRAD, g, L.max_tiles1, s)
                                               : launch_grouped_bf16(GM_DGRAD, g, L.max_tiles1, s));
   if (g.splits > 1) MOE_TRY(ST_GROUPED_LINEAR, launch_grouped_join(GM_DGRAD, dtype, g, s));
@@ -313,6 +325,9 @@ moe_status moe_grouped_linear_wgrad(int32_t E, int64_t R, int32_t in, int32_t ou
   if (!dw || !offsets || (R > 0 && (!dy || !x))) return MOE_ERR_INVALID_ARG;
   if (dw == dy || dw == x || !all_aligned16(dy, x, dw)) return MOE_ERR_INVALID_ARG;
   const GroupedLayout L = grouped_layout(E, R, dtype);
+  const int splits = grouped_splits(GM_WGRAD, dtype, E, R, out, in, L.part_bytes);
+  if (dtype == MOE_F32 && !launch_fits(grouped_f32_blocks(GM_WGRAD, E, out, in, splits, 0), 256))
+    return MOE_ERR_UNSUPPORTED;
   if (!workspace || ws_bytes < L.total || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   int32_t* src = nullptr;
@@ -322,7 +337,7 @@ moe_status moe_grouped_linear_wgrad(int32_t E, int64_t R, int32_t in, int32_t ou
     MOE_TRY(ST_GROUPED_LISTS, launch_offset_lists(offsets, E, R, none, none, 0, row_index, index_div, x_rows, src, nullptr, s));
   }
   const GradArgs g{dy, x, dw, R, out, in, E, offsets, src, x_rows, nullptr, nullptr, nullptr,
-                   grouped_splits(GM_WGRAD, dtype, E, R, out, in, L.part_bytes), at<float>(workspace, L.part), nullptr};
+                   splits, at<float>(workspace, L.part), nullptr};
   MOE_TRY(ST_GROUPED_LINEAR,
           dtype == MOE_F32 ? launch_grouped_f32(GM_WGRAD, g, 0, s) : launch_grouped_bf16(GM_WGRAD, g, 0, s));
   if (g.splits > 1) MOE_TRY(ST_GROUPED_LINEAR, launch_grouped_join(GM_WGRAD, dtype, g, s));
@@ -356,7 +371,8 @@ moe_status moe_quantize(int32_t dtype, int64_t rows, int32_t in, int32_t group, 
   if (!dtype_ok(dtype) || rows < 0 || in < 1) return MOE_ERR_INVALID_ARG;
   if (group != 32 && group != 64 && group != 128) return group < 1 ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED;
   if (in % group != 0) return MOE_ERR_INVALID_ARG;
-  if (in % 64 != 0 || rows >= (int64_t)1 << 40 || rows * (in / 8) >= (int64_t)256 * kInt31) return MOE_ERR_UNSUPPORTED;
+  // a thread per eight values, in whole blocks of 256
+  if (in % 64 != 0 || rows > (kGiB4 - 256) / (in / 8)) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!w || !wq || !scales || !all_aligned16(w, wq, scales)) return MOE_ERR_INVALID_ARG;
   if (wq == w || scales == w || wq == scales) return MOE_ERR_INVALID_ARG;

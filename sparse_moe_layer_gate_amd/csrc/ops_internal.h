@@ -26,6 +26,7 @@ enum OpStage {
   } while (0)
 
 // ---- combine ----
+int combine_threads(int D);  // of the one block per token
 // y = alpha * sum over slots of w rows[inv_row] + shared (w or shared may be null)
 hipError_t launch_combine_rows(int dtype, const void* rows, int64_t R, const int32_t* inv_row, const float* w,
                                const void* shared, int64_t N, int k, int D, float alpha, void* y, hipStream_t s);
@@ -51,6 +52,7 @@ struct NormPlan {
   int64_t chunks_per_group;  // > 0: the blocks of one gate group; 0: blocks hold whole groups (or no gate)
   int64_t nblocks;
 };
+int norm_forward_threads(int D);  // of the one block per row
 int64_t norm_runs(int D);  // most runs of rows without a gate
 NormPlan norm_plan(int64_t N, int D, int64_t gate_rows);  // gate_rows 0: no gate
 hipError_t launch_norm_forward(int dtype, const NormCall& c, hipStream_t s);
@@ -88,6 +90,7 @@ struct GradArgs {
 };
 hipError_t launch_grouped_bf16(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s);
 hipError_t launch_grouped_f32(GroupedMode mode, const GradArgs& a, int64_t max_tile_count, hipStream_t s);
+int64_t grouped_f32_blocks(GroupedMode mode, int E, int M, int K, int splits, int64_t max_tile_count);  // of 256 threads
 int grouped_splits(GroupedMode mode, int dtype, int E, int64_t R, int M, int K, size_t part_bytes);
 hipError_t launch_grouped_join(GroupedMode mode, int dtype, const GradArgs& a, hipStream_t s);
 constexpr int kGradRows = 256;  // rows per tile of the bf16 dgrad list
