@@ -87,6 +87,16 @@ __device__ inline void exchange4(u32x4& d) {
   d[3] = e[1];
 }
 
+// SwiGLU of the products, clamped as swiglu_bf16 does. By comparisons, which leave a NaN as it is: fminf would make it
+// the bound, and a damaged weight's output an ordinary number.
+__device__ inline uint16_t gated(float g, float u, float lim) {
+  if (lim > 0.f) {
+    g = g > lim ? lim : g;
+    u = u > lim ? lim : u < -lim ? -lim : u;
+  }
+  return (uint16_t)bf16_pair(swiglu_bf16(g, u, 0.f), 0.f);
+}
+
 template <int V>
 struct IntC {
   static constexpr int value = V;
@@ -325,7 +335,7 @@ __global__ __launch_bounds__(256, T::BLOCKS) void qlinear_kernel(QuantArgs a) {
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
             if (SWIGLU) {
-              if (t & 1) y[8 * (t - 1)] = (uint16_t)bf16_pair(swiglu_bf16(acc[i][t - 1][r], acc[i][t][r], a.limit), 0.f);
+              if (t & 1) y[8 * (t - 1)] = gated(acc[i][t - 1][r], acc[i][t][r], a.limit);
             } else {
               y[16 * t] = (uint16_t)bf16_pair(acc[i][t][r], 0.f);
             }
@@ -514,7 +524,7 @@ __device__ __forceinline__ void wide_tile(const QuantArgs& a, int expert, int64_
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           if (SWIGLU) {
-            if (t & 1) y[8 * (t - 1)] = (uint16_t)bf16_pair(swiglu_bf16(acc[i][t - 1][r], acc[i][t][r], a.limit), 0.f);
+            if (t & 1) y[8 * (t - 1)] = gated(acc[i][t - 1][r], acc[i][t][r], a.limit);
           } else {
             y[16 * t] = (uint16_t)bf16_pair(acc[i][t][r], 0.f);
           }

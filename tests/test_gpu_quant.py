@@ -116,3 +116,31 @@ def test_quantize_group_whose_scale_vanishes(dtype):
     w = torch.full((2, 64), float(torch.finfo(torch.bfloat16).smallest_normal) / 128, dtype=dtype)  # the least bfloat16
     q, s = moe.moe_quantize(dev(w), 32)
     assert (s.cpu() == 0).all() and (q.cpu() == 0x88).all()
+
+
+@pytest.mark.parametrize("limit", [0.0, 1.5])
+@pytest.mark.parametrize("form", ["16 rows", "64 rows", "experts"])
+def test_swiglu_shows_nan(form, limit):
+    """NaN scales of one gate row and one up row, and a NaN activation row: their outputs and no others are NaN, clamped
+    or not."""
+    offsets, index, x, q, s = case(form, 64, 34)
+    M = q.shape[1] // 128 * 128
+    q, s = q[:, :M].contiguous(), s[:, :M].contiguous()
+    half = M // 2
+    kw = dict(offsets=dev(offsets), row_index=dev(index)) if index is not None else {}
+
+    def run():
+        y = torch.full((x.shape[0], half), 7.0, dtype=BF, device="cuda")
+        moe.moe_qlinear(dev(x), dev(q), dev(s), y, swiglu=True, limit=limit, **kw)
+        return y.cpu()
+    clean = run()
+    s[:, 5, 1] = float("nan")
+    s[:, half + 9, 0] = float("nan")
+    x[2, 17] = float("nan")
+    y = run()
+    row = int((index == 2).nonzero()[0, 0]) if index is not None else 2
+    hit = torch.zeros_like(y, dtype=torch.bool)
+    hit[:, 5] = hit[:, 9] = True
+    hit[row] = True
+    assert torch.isfinite(clean.float()).all() and y[hit].isnan().all()
+    assert torch.equal(y[~hit], clean[~hit])
