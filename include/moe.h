@@ -226,8 +226,8 @@ moe_status moe_dense_forward(int64_t N, int32_t D, int32_t dff, int32_t dtype, f
  * the experts' products as separate calls (other activations, adapters, training), the combine of their
  * rows, and experts with 4-bit weights. They work on the same lists as the layer (moe_route,
  * moe_dispatch). The conventions at the top hold: 16-byte aligned contiguous device pointers, the
- * caller's stream and workspace, errors found on the host before any launch, no atomics (the same inputs
- * give the same bits). Calls that write gradients overwrite them.
+ * caller's stream and workspace, errors found on the host before any launch, no atomics on results (the same
+ * inputs give the same bits). Calls that write gradients overwrite them.
  */
 
 /* Norms before and after a block, fused with the block's gate and the residual scale:

@@ -14,8 +14,8 @@
 // second use of a row cost no second read. Rows come straight from the kernel before, so the loads keep the
 // default policy and may hit the last-level cache (8,191 x 5,120 forward 72 us with non-temporal loads, 61
 // without); the stores are non-temporal where nothing reads them soon (61 against 75). On inputs that are not in
-// that cache the forward takes 69 us, 4.9 TB/s, the rate of a large copy; the gradients of 4,096 x 4,096 take 55 us,
-// 3.7 TB/s (two barriers and the partial sums of the parameter gradients cost the rest).
+// that cache the forward takes 69 us, 4.9 TB/s, the rate of a large copy; the gradients of 4,096 x 4,096 take 56 us,
+// 3.6 TB/s (two barriers and the partial sums of the parameter gradients cost the rest).
 #include <hip/hip_runtime.h>
 
 #include "ops_internal.h"
@@ -312,9 +312,11 @@ struct ReduceJob {
   int64_t rows;      // partial rows per group
   int64_t groups;
 };
-// Blocks of the backward pass have at most 512 threads (two pieces per thread from 4,096 features on): with up
-// to 1,024, the register budget of 128 spilled (4,096 x 4,096: 68 -> 63 us). Rows of more than 8,192 features
-// still take 1,024.
+// Blocks of the backward pass have at most 512 threads (two pieces per thread above 4,096 features): with up
+// to 1,024, the register budget of 128 spilled (4,096 x 4,096: 68 -> 63 us). Some forms still spill: with both norms
+// in float32 above 4,096 features (31 registers; 4,096 x 5,120: 168 us, a copy of its bytes 104), and every form of
+// rows of more than 8,192 features, which take 1,024 threads (both norms: 228 registers in bfloat16, 297 in float32;
+// 1,024 x 16,384: 231 and 363 us, against 41 and 83).
 constexpr int kBackwardThreads = 512;
 struct ReduceArgs {
   ReduceJob job[3];
@@ -447,13 +449,17 @@ hipError_t backward_t(const NormCall& c, hipStream_t s) {
 
 int norm_forward_threads(int D) { return shape_of(D, 1024).threads; }
 
-// Runs of the backward pass: eight waves per CU (256 CUs). More runs mean more partial rows (three of D floats
-// per run) to write and add: 4,096 x 4,096 with 256 / 512 runs 51 / 59 us.
+// Runs of the backward pass: blocks of 512 threads, or as many smaller ones as make no more, per CU (256 CUs): eight
+// waves at 4,096 and 8,192 features, five at 2,560 and 5,120, six at 1,536 and 6,144. More runs mean more partial rows
+// (three of D floats per run) to write and add: 4,096 x 4,096 with 256 / 512 runs 51 / 59 us, the one width where both
+// were measured (4,096 rows of 5,120 and 6,144, the call: 73 and 82 us, copies of their bytes 52 and 62).
 int64_t norm_runs(int D) {
   const int threads = shape_of(D, kBackwardThreads).threads;
   return threads >= 512 ? 256 : 256 * (512 / threads);
 }
 
+// With gate rows of no more than a run, runs are whole gate groups and may then be nearly twice an even share: 8,191
+// rows of 4,096 with 31 rows a gate make 133 runs and take 149 us, 90 without a gate.
 NormPlan norm_plan(int64_t N, int D, int64_t gate_rows) {
   const int64_t kBlocks = norm_runs(D);
   NormPlan p{};

@@ -16,11 +16,11 @@
 // matrix steps that each cross the four 32-value pieces); smaller groups first exchange the four words
 // among the four lanes of a row (permlane swaps), so that a step's 32 values are consecutive.
 //
-// What bounds it: 32 tokens over 256 experts, 6,144 -> 4,096, groups of 32: 0.44 ms, 5.2 TB/s of weights and
-// scales, faster than a large copy, the vector unit busy about half the cycles; one token, 5,120 -> 24,576, groups
-// of 128: 18-20 us, of which the 65 MB would take 13 (the launch's ramp, three rounds of loads per wave); 1,021
-// rows, 12,288 -> 5,120, groups of 64: 0.23 ms, 560 TFLOP/s: per 48 x 64 x 256 values of a wave 120 matrix
-// instructions (16 cycles each) and about 650 vector ones (4 each) of two waves per SIMD that overlap in part.
+// What bounds it: 32 tokens over 256 experts, 6,144 -> 4,096, groups of 32: 0.44-0.46 ms, 4.7 TB/s of the weights and
+// scales that it fetches, about a large copy's rate, with the vector unit busy 70% of the cycles; one token,
+// 5,120 -> 24,576, groups of 128: 14.5-16 us, of which the 65 MB would take 13 (the launch's ramp, few rounds of loads
+// per wave); 1,021 rows, 12,288 -> 5,120, groups of 64: 0.23 ms, 556 TFLOP/s: per 48 x 64 x 256 values of a wave 96
+// matrix instructions (16 cycles each) and 760 vector ones (4 each) of two waves per SIMD that overlap in part.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
