@@ -327,8 +327,9 @@ moe_status moe_grouped_linear_wgrad(int32_t E, int64_t R, int32_t in, int32_t ou
  *   swiglu  1: the rows of W are [0, out / 2) gate and [out / 2, out) up, and y [R, out / 2] is
  *           SiLU(W_gate x) * W_up x, clamped by swiglu_limit > 0 as in moe_config (out a multiple of 128).
  *           0: y [R, out], swiglu_limit 0.
- * Float32 sums of the products x * (q - 8) over a group, which are then scaled and added; no weight and no partial
- * sum is rounded to fewer bits, and a weight of q = 8 adds exactly nothing. No workspace. x does not overlap y. R = 0
+ * Float32 sums of the products x * (q - 8) over a group (which have to stay in float32's range: 8 |x| summed over a
+ * group below 2^128), then scaled and added; no weight and no partial sum is rounded to fewer bits, and a weight of
+ * q = 8 adds exactly nothing. No workspace. x does not overlap y. R = 0
  * launches nothing. */
 moe_status moe_qlinear(int32_t E, int64_t R, int32_t in, int32_t out, int32_t group, const void* x, int64_t x_rows,
                        const int32_t* row_index, int32_t index_div, const void* wq, const void* scales,
