@@ -10,8 +10,8 @@
 // GEMMs (gemm_bf16.hip, gemm_decode.hip); here are the float32 products and the bf16 gradients.
 //
 // What bounds them, measured on whole calls: the Air gate_up shape (128 experts, 4,096 -> 2,816, 4,096 tokens of
-// eight experts) wgrad 1.09-1.15 ms, 660-690 TFLOP/s while it writes 2.95 GB of dW (skipping the stores alone 0.85 ms, the
-// products alone 0.75: neither hides wholly behind the other); the GLM-4.5 down shape (160 experts, 1,536 <- 5,120,
+// eight experts) wgrad 1.09-1.15 ms, 660-690 TFLOP/s while it writes 2.95 GB of dW (skipping the stores alone 0.85 ms,
+// the products alone 0.75: neither hides wholly behind the other); the GLM-4.5 down shape (160 experts, 1,536 <- 5,120,
 // 3,001 tokens) dgrad 0.58-0.61 ms, 4.6-4.9 TB/s of its 2.84 GB, the rate of a large copy: bound by the weights' stream.
 #include <hip/hip_runtime.h>
 

@@ -11,7 +11,8 @@
 //  - v_mfma_f32_16x16x32_bf16 sums one group in float32, and the group's sum is scaled in float32 and added.
 //    Neither a weight nor a scaled partial sum is ever rounded to bfloat16, and a weight of 0 adds exactly
 //    nothing, however large its activation. (A cheaper unpacking to 128 + q with 136 sum(x) taken off a group's sum
-//    cancels: beside an activation 10,000 times the others its error was a bfloat16 half step.)
+//    cancels: 5,120 features, groups of 128, one weight row's 0 beside an activation 10,000 times the others: 30% of
+//    the outputs were not the exact value rounded; now all are.)
 // A lane's 16 bytes are 32 consecutive k of one weight row. Groups of 128 take them as they are (four
 // matrix steps that each cross the four 32-value pieces); smaller groups first exchange the four words
 // among the four lanes of a row (permlane swaps), so that a step's 32 values are consecutive.
@@ -536,8 +537,8 @@ __device__ __forceinline__ void wide_tile(const QuantArgs& a, int expert, int64_
 // EXPERTS: a tile of at most 32 rows runs a body of its own (256 experts 6,144 -> 4,096, 24 / 64 rows each: 1,480 ->
 // 1,379, 2,527 -> 2,412 us). A dense product has at most one such tile and keeps one body, which takes fewer
 // registers (12,288 -> 5,120, 1,021 rows: 231 us, 239 with both); so does the form that both would make spill. Two
-// waves per SIMD at most: where a form's registers allow three blocks per CU, they push each other's weights out of L2
-// (256 experts 6,144 -> 4,096, groups of 32, 32 rows each: 1,628 us, 1,940 with three).
+// waves per SIMD at most: the 48-row form with groups of 32 has the registers for three blocks per CU and is slower with
+// them (256 experts 6,144 -> 4,096, 32 rows each: 1,628 us, 1,940 with three).
 template <int TT, int G, bool SWIGLU, bool EXPERTS>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void qlinear_wide_kernel(QuantArgs a) {
   constexpr int ROWS = 16 * TT;
