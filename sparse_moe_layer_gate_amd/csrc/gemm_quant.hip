@@ -11,7 +11,7 @@
 //  - v_mfma_f32_16x16x32_bf16 sums one group in float32, and the group's sum is scaled in float32 and added.
 //    Neither a weight nor a scaled partial sum is ever rounded to bfloat16, and a weight of 0 adds exactly
 //    nothing, however large its activation. (A cheaper unpacking to 128 + q with 136 sum(x) taken off a group's sum
-//    cancels: 5,120 features, groups of 128, one weight row's 0 beside an activation 10,000 times the others: 30% of
+//    cancels: 5,120 features, groups of 128, weights of 0 beside an activation 10,000 times the others: 30% of
 //    the outputs were not the exact value rounded; now all are.)
 // A lane's 16 bytes are 32 consecutive k of one weight row. Groups of 128 take them as they are (four
 // matrix steps that each cross the four 32-value pieces); smaller groups first exchange the four words
