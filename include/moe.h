@@ -343,6 +343,136 @@ moe_status moe_qlinear(int32_t E, int64_t R, int32_t in, int32_t out, int32_t gr
 moe_status moe_quantize(int32_t dtype, int64_t rows, int32_t in, int32_t group, const void* w, void* wq, void* scales,
                         void* stream);
 
+/* ---- A training step around the layer ----------------------------------------------------------------
+ *
+ * What a training step needs beside the gradients above: layer norm, dense linear maps with a fused epilogue,
+ * the balance loss with the gradient that reaches the router, and clipping of all gradients by their norm.
+ * Conventions as for the operators around the experts.
+ */
+
+/* Layer norm, optionally with the residual sum in front of it:
+ *   h = x + residual,   y = (h - mean(h)) * rstd(h) * w + b,   rstd(v) = 1 / sqrt(mean((v - mean(v))^2) + eps)
+ * over the D features of a row.
+ *   x, residual, h_out, y [N, D] of dtype; w, b [D] of dtype, or NULL: 1 and 0
+ *   residual NULL: h = x, and h_out is NULL. Otherwise h_out receives h.
+ *   stats [N, 2] float32: mean and rstd of each row, for moe_layer_norm_backward, or NULL.
+ * Float32 arithmetic; h_out and y are each rounded once, y from the unrounded h. h_out may be x or residual (in
+ * place); no other overlap. D: a multiple of 8, at most 16384; N below 2^31, and N * T below 2^32 with T the threads of
+ * a row: the least power of two of at least D / 8, from 8 to 64, for D up to 2048; above, D / 8 (D / 16 above 8192)
+ * rounded up to a multiple of 64. N = 0 launches nothing. */
+moe_status moe_layer_norm(int64_t N, int32_t D, int32_t dtype, float eps, const void* x, const void* residual,
+                          const void* w, const void* b, void* h_out, void* y, float* stats, void* stream);
+
+/* Gradients of moe_layer_norm from its h (h_out, or x without a residual), its stats and the gradients of h_out
+ * (dh_out, or NULL: zero) and y:
+ *   n = (h - mean) * rstd, t = dy * w:   dh = dh_out + rstd * (t - mean(t) - n * mean(t * n))
+ *   dw = sum over rows of dy * n,   db = sum over rows of dy
+ *   dh [N, D] of dtype: the gradient of x and of residual alike; w NULL: 1
+ *   dw, db [D] float32, written, or NULL where not wanted: sums in a fixed order
+ *   workspace: at least moe_layer_norm_workspace_size(N, D, dtype) bytes (may be NULL when no sum is wanted). The
+ *           size never falls as N grows.
+ * dh may be dh_out (in place); no other overlap. Sizes as for moe_layer_norm. N = 0 writes zeros to dw and db. */
+size_t moe_layer_norm_workspace_size(int64_t N, int32_t D, int32_t dtype);
+moe_status moe_layer_norm_backward(int64_t N, int32_t D, int32_t dtype, const void* h, const float* stats,
+                                   const void* w, const void* dh_out, const void* dy, void* dh, float* dw, float* db,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/* Activations of moe_linear. MOE_ACT_GELU is z Phi(z) with the normal distribution's own function, MOE_ACT_GELU_TANH
+ * 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_GELU_TANH = 4
+} moe_activation;
+
+/* A linear map of R rows with bias, activation and residual in its epilogue:
+ *   z = x W^T + bias,   y = act(z) + residual
+ *   x [R, in], W [out, in], bias [out] or NULL, residual [R, out] or NULL, y [R, out] of dtype
+ *   z [R, out] of dtype or NULL: the pre-activation, kept for moe_linear_backward
+ *   workspace: at least moe_linear_workspace_size(R, in, out, dtype) bytes (may be NULL when that is 0). The size
+ *           never falls as R grows.
+ * Float32 sums over the whole reduction and float32 epilogue; z and y are each rounded once, y from the unrounded z.
+ * y may be residual (in place); no other overlap. in: a multiple of 64, out: a multiple of 8, both up to 2^22,
+ * in * out below 2^31; R below 2^31 and R * out below 2^40. R = 0 launches nothing. */
+size_t moe_linear_workspace_size(int64_t R, int32_t in, int32_t out, int32_t dtype);
+moe_status moe_linear(int64_t R, int32_t in, int32_t out, int32_t dtype, int32_t activation, const void* x,
+                      const void* w, const void* bias, const void* residual, void* z, void* y, void* workspace,
+                      size_t ws_bytes, void* stream);
+
+/* Gradients of moe_linear's epilogue, from the z that it kept:
+ *   dz = dy * act'(z) (of dtype),   dbias = sum over rows of the unrounded dy * act'(z) (float32, a fixed order)
+ * The others follow with moe_grouped_linear_dgrad (dx = dz W) and moe_grouped_linear_wgrad (dW = dz^T x), E = 1 and
+ * offsets {0, R} (out a multiple of 64); the residual's is dy. relu'(0) = 0.
+ *   dz or dbias may be NULL (not wanted), not both; z may be NULL for MOE_ACT_NONE (dz is then a copy of dy).
+ *   workspace: at least moe_linear_backward_workspace_size(R, out, dtype) bytes (may be NULL without dbias). The size
+ *           never falls as R grows.
+ * dz may be dy or z (in place); no other overlap. Sizes as for moe_linear. R = 0 writes zeros to dbias. */
+size_t moe_linear_backward_workspace_size(int64_t R, int32_t out, int32_t dtype);
+moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t activation, const void* dy,
+                               const void* z, void* dz, float* dbias, void* workspace, size_t ws_bytes, void* stream);
+
+/* The balance loss of a routed batch, per sequence, and the counts behind it. Rows [q T, (q + 1) T) are sequence q,
+ * T = seq_rows, S = ceil(N / T) sequences (the last may be shorter; seq_rows >= N: one). With V the sequence's live
+ * tokens (token_mask != 0; NULL: all), s their scores and p = s / (sum over the experts of s):
+ *   c_i = the live tokens' slots that name expert i,  f_i = E c_i / (k V),  P_i = (sum over live tokens of p_i) / V
+ *   loss = weight / S * (sum over sequences and experts of f_i P_i)
+ * A sequence without live tokens adds nothing; a token whose scores sum to 0 has p = 0. Ids outside [0, E) are empty
+ * slots. The counts are constants of the gradient: d loss / d p = coef_i = weight / S * f_i / V for a live token.
+ *   scores [N, E] float32, topk_idx [N, k] int32, as moe_route writes them (MOE_ROUTE_SCORES_OUT)
+ *   token_mask [N] uint8 or NULL; the scores of a dead token are read but have no effect, whatever they hold
+ *   counts [S, E] int32, coef [S, E] float32 (for moe_route_backward): written, or NULL where not wanted
+ *   loss [1] float32, written
+ *   workspace: at least moe_balance_workspace_size(cfg, N, seq_rows) bytes
+ * Sums in a fixed order. N k below 2^31, N E below 2^40. N = 0 writes 0 to loss. */
+size_t moe_balance_workspace_size(const moe_config* cfg, int64_t N, int64_t seq_rows);
+moe_status moe_balance_loss(const moe_config* cfg, int64_t N, int64_t seq_rows, float weight, const float* scores,
+                            const int32_t* topk_idx, const uint8_t* token_mask, int32_t* counts, float* coef,
+                            float* loss, void* workspace, size_t ws_bytes, void* stream);
+
+/* The gradient of the router's logits (s = sigmoid(logit)) from the mixture weights' gradient and the balance loss's:
+ *   with D = (sum over the token's slots of s) + eps and w_m = alpha s_m / D (alpha s_m without norm_topk_prob; alpha = 1
+ *   where alpha_on_output is set):
+ *   ds_i = sum over the slots m that name i of alpha / D * (dtopk_w_m - sum_l dtopk_w_l s_l / D)
+ *        + dloss * (coef_i - sum_j coef_j p_j) / (sum_j s_j)     (live tokens; coef of the token's sequence)
+ *   dlogits = ds * s * (1 - s)
+ *   scores, topk_idx: as the forward call wrote them (ids outside [0, E): empty slots); dtopk_w [N, k] float32, or NULL:
+ *           no such gradient (topk_idx may then be NULL); coef [S, E] float32 from moe_balance_loss, or NULL: no
+ *           balance loss (seq_rows is then not used). Not both NULL.
+ *   dloss: the loss's gradient, one float32 on the device, or NULL: 1;  token_mask as for moe_balance_loss (it concerns
+ *           the balance loss alone);  dlogits [N, E] float32, written
+ * The router's weight and input gradients are products of dlogits with x and w_router. dlogits may be scores (in place).
+ * Sizes as for moe_balance_loss. N = 0 launches nothing. */
+moe_status moe_route_backward(const moe_config* cfg, int64_t N, const float* scores, const int32_t* topk_idx,
+                              const float* dtopk_w, int64_t seq_rows, const float* coef, const float* dloss,
+                              const uint8_t* token_mask, float* dlogits, void* stream);
+
+/* One tensor of a list: `numel` contiguous values of dtype at `data`, which needs the alignment of its type alone (views
+ * into a flat buffer). The lists themselves are host memory, read before the call returns. */
+typedef struct {
+  void* data;
+  int64_t numel; /* >= 0; data may be NULL when 0 */
+  int32_t dtype; /* moe_dtype */
+} moe_tensor;
+
+/* The 2-norm over all values of n tensors: norm[0] = sqrt(sum of squares), float32 on the device. Squares and sums are
+ * float64, in a fixed order, so neither overflows nor vanishes where the norm itself is a float32; a NaN gives NaN, an
+ * infinity without one infinity. n = 0 or no values: 0.
+ *   workspace: at least moe_grad_norm_workspace_size(tensors, n) bytes, 16-byte aligned
+ * n up to 65536, 2^40 values in all. */
+size_t moe_grad_norm_workspace_size(const moe_tensor* tensors, int32_t n);
+moe_status moe_grad_norm(const moe_tensor* tensors, int32_t n, float* norm, void* workspace, size_t ws_bytes,
+                         void* stream);
+
+/* Clipping by that norm: out = tensor * scale with scale = max_norm / (norm[0] + eps) where that is below 1, else 1,
+ * in float32, rounded once. norm is read on the device. out: n tensors of the same numel, each of its own dtype, or NULL:
+ * in place (with a scale of 1 the tensors are then left as they are). A norm of infinity gives the scale 0 and a NaN the
+ * scale NaN: look at norm before the optimizer's step. No tensor written overlaps another of either list, but out[i] may
+ * be tensors[i] exactly. max_norm >= 0 and eps >= 0, finite. */
+moe_status moe_grad_clip(const moe_tensor* tensors, const moe_tensor* out, int32_t n, const float* norm, float max_norm,
+                         float eps, void* stream);
+
 /* Static string naming a status. */
 const char* moe_status_str(moe_status status);
 

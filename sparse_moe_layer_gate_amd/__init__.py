@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16 = 0, 1
+MOE_ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 MOE_ROUTE_SCORES_IN, MOE_ROUTE_SCORES_OUT, MOE_ROUTE_PREPARED = 1, 2, 4
 
 EXPORTED = ["moe_check_config", "moe_workspace_size", "moe_dispatch_workspace_size", "moe_router_prepared_size",
@@ -24,7 +25,11 @@ EXPORTED = ["moe_check_config", "moe_workspace_size", "moe_dispatch_workspace_si
             "moe_forward_noalloc", "moe_noalloc_scratch_bytes", "moe_dense_workspace_size", "moe_dense_forward",
             "moe_block_norm", "moe_block_norm_backward", "moe_block_norm_workspace_size", "moe_combine",
             "moe_combine_backward", "moe_grouped_workspace_size", "moe_grouped_linear", "moe_grouped_linear_dgrad",
-            "moe_grouped_linear_wgrad", "moe_qlinear", "moe_quantize", "moe_status_str", "moe_profile_begin",
+            "moe_grouped_linear_wgrad", "moe_qlinear", "moe_quantize", "moe_layer_norm",
+            "moe_layer_norm_workspace_size", "moe_layer_norm_backward", "moe_linear_workspace_size", "moe_linear",
+            "moe_linear_backward_workspace_size", "moe_linear_backward", "moe_balance_workspace_size",
+            "moe_balance_loss", "moe_route_backward", "moe_grad_norm_workspace_size", "moe_grad_norm",
+            "moe_grad_clip", "moe_status_str", "moe_profile_begin",
             "moe_profile_begin_mask", "moe_profile_end", "moe_stage_name", "moe_stage_count"]
 
 
@@ -55,6 +60,10 @@ class MoeConfig(ctypes.Structure):
 class MoeWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w_router", "e_bias", "gate_up", "down", "sh_gate", "sh_up", "sh_down",
                                                "w_router_prepared")]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -110,6 +119,26 @@ def lib():
         L.moe_grouped_linear_wgrad.argtypes = [i32, i64, i32, i32, i32, vp, vp, i64, vp, i32, vp, vp, vp, sz, vp]
         L.moe_qlinear.argtypes = [i32, i64, i32, i32, i32, vp, i64, vp, i32, vp, vp, vp, i32, f32, vp, vp]
         L.moe_quantize.argtypes = [i32, i64, i32, i32, vp, vp, vp, vp]
+        tp = ctypes.POINTER(MoeTensor)
+        L.moe_layer_norm_workspace_size.argtypes = [i64, i32, i32]
+        L.moe_layer_norm.argtypes = [i64, i32, i32, f32, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_layer_norm_backward.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_workspace_size.argtypes = [i64, i32, i32, i32]
+        L.moe_linear.argtypes = [i64, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_linear_backward_workspace_size.argtypes = [i64, i32, i32]
+        L.moe_linear_backward.argtypes = [i64, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_balance_workspace_size.argtypes = [cp, i64, i64]
+        L.moe_balance_loss.argtypes = [cp, i64, i64, f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_route_backward.argtypes = [cp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+        L.moe_grad_norm_workspace_size.argtypes = [tp, i32]
+        L.moe_grad_norm.argtypes = [tp, i32, vp, vp, sz, vp]
+        L.moe_grad_clip.argtypes = [tp, tp, i32, vp, f32, f32, vp]
+        for fn in (L.moe_layer_norm_workspace_size, L.moe_linear_workspace_size, L.moe_linear_backward_workspace_size,
+                   L.moe_balance_workspace_size, L.moe_grad_norm_workspace_size):
+            fn.restype = sz
+        for fn in (L.moe_layer_norm, L.moe_layer_norm_backward, L.moe_linear, L.moe_linear_backward,
+                   L.moe_balance_loss, L.moe_route_backward, L.moe_grad_norm, L.moe_grad_clip):
+            fn.restype = ctypes.c_int
         for fn in (L.moe_block_norm, L.moe_block_norm_backward, L.moe_combine, L.moe_combine_backward,
                    L.moe_grouped_linear, L.moe_grouped_linear_dgrad, L.moe_grouped_linear_wgrad, L.moe_qlinear,
                    L.moe_quantize):
@@ -579,6 +608,200 @@ def moe_quantize(w, group: int, wq=None, scales=None, stream=None):
                                 _ptr(scales, "scales", torch.bfloat16, lead + (K // group,)), _stream(stream))
     _check(st, "moe_quantize")
     return wq, scales
+
+
+# ---- a training step around the layer ----
+def moe_layer_norm_workspace_size(N: int, D: int, dtype="bf16") -> int:
+    """Bytes of workspace of moe_layer_norm_backward."""
+    return int(lib().moe_layer_norm_workspace_size(int(N), int(D), _dtype_code(dtype)))
+
+
+def moe_layer_norm(N: int, x, residual, w, b, h_out, y, stats=None, eps: float = 1e-5, stream=None):
+    """h = x + residual and y = (h - mean(h)) / std(h) * w + b over each row; std with eps under the root. residual
+    (and with it h_out, which receives h), w and b may be None; stats [N, 2] float32 receives mean and 1 / std for
+    moe_layer_norm_backward."""
+    import torch
+
+    dt = _tensor_dtype(x, "x")
+    t, D = x.dtype, x.shape[-1]
+    with _same_device("moe_layer_norm", x, residual, w, b, h_out, y, stats):
+        st = lib().moe_layer_norm(
+            int(N), int(D), dt, float(eps), _ptr(x, "x", t, (N, D)),
+            _ptr(residual, "residual", t, (N, D), required=False), _ptr(w, "w", t, (D,), required=False),
+            _ptr(b, "b", t, (D,), required=False), _ptr(h_out, "h_out", t, (N, D), required=False),
+            _ptr(y, "y", t, (N, D)), _ptr(stats, "stats", torch.float32, (N, 2), required=False), _stream(stream))
+    _check(st, "moe_layer_norm")
+
+
+def moe_layer_norm_backward(N: int, h, stats, w, dh_out, dy, dh, dw, db, workspace, stream=None):
+    """Gradients of moe_layer_norm from its h (h_out, or x without a residual) and stats: dh [N, D] (of x and residual
+    alike, dh_out added when given) and, where given, the float32 sums dw and db; workspace:
+    moe_layer_norm_workspace_size(N, D, dtype) bytes, or None without sums."""
+    import torch
+
+    dt = _tensor_dtype(h, "h")
+    t, f, D = h.dtype, torch.float32, h.shape[-1]
+    ws, ws_bytes = _ws(workspace)
+    with _same_device("moe_layer_norm_backward", h, stats, w, dh_out, dy, dh, dw, db, workspace):
+        st = lib().moe_layer_norm_backward(
+            int(N), int(D), dt, _ptr(h, "h", t, (N, D)), _ptr(stats, "stats", f, (N, 2)),
+            _ptr(w, "w", t, (D,), required=False), _ptr(dh_out, "dh_out", t, (N, D), required=False),
+            _ptr(dy, "dy", t, (N, D)), _ptr(dh, "dh", t, (N, D)), _ptr(dw, "dw", f, (D,), required=False),
+            _ptr(db, "db", f, (D,), required=False), ws, ws_bytes, _stream(stream))
+    _check(st, "moe_layer_norm_backward")
+
+
+def _activation(act) -> int:
+    code = MOE_ACTIVATIONS.get(act) if isinstance(act, str) else act
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(MOE_ACTIVATIONS)}, got {act!r}")
+    return int(code)
+
+
+def moe_linear_workspace_size(R: int, K: int, M: int, dtype="bf16") -> int:
+    """Bytes of workspace of moe_linear for R rows, K input and M output features."""
+    return int(lib().moe_linear_workspace_size(int(R), int(K), int(M), _dtype_code(dtype)))
+
+
+def moe_linear(x, w, y, workspace=None, bias=None, residual=None, act="none", z=None, stream=None):
+    """y = act(x w^T + bias) + residual; x [R, in], w [out, in], y [R, out]. z [R, out] receives x w^T + bias for
+    moe_linear_backward. act: a key of MOE_ACTIVATIONS. workspace: moe_linear_workspace_size(R, in, out, dtype) bytes."""
+    dt = _tensor_dtype(x, "x")
+    t, (R, M), K = x.dtype, y.shape, x.shape[-1]
+    ws, ws_bytes = _ws(workspace)
+    with _same_device("moe_linear", x, w, y, workspace, bias, residual, z):
+        st = lib().moe_linear(
+            int(R), int(K), int(M), dt, _activation(act), _ptr(x, "x", t, (R, K)), _ptr(w, "w", t, (M, K)),
+            _ptr(bias, "bias", t, (M,), required=False), _ptr(residual, "residual", t, (R, M), required=False),
+            _ptr(z, "z", t, (R, M), required=False), _ptr(y, "y", t, (R, M)), ws, ws_bytes, _stream(stream))
+    _check(st, "moe_linear")
+
+
+def moe_linear_backward_workspace_size(R: int, M: int, dtype="bf16") -> int:
+    """Bytes of workspace of moe_linear_backward with dbias."""
+    return int(lib().moe_linear_backward_workspace_size(int(R), int(M), _dtype_code(dtype)))
+
+
+def moe_linear_backward(dy, z, dz, dbias, workspace=None, act="none", stream=None):
+    """dz = dy * act'(z) and the float32 dbias = sum of its rows, each where given; z may be None for act "none". dx and
+    dw follow from dz with moe_grouped_linear_dgrad and moe_grouped_linear_wgrad (one expert, offsets [0, R])."""
+    import torch
+
+    dt = _tensor_dtype(dy, "dy")
+    t, (R, M) = dy.dtype, dy.shape
+    ws, ws_bytes = _ws(workspace)
+    with _same_device("moe_linear_backward", dy, z, dz, dbias, workspace):
+        st = lib().moe_linear_backward(
+            int(R), int(M), dt, _activation(act), _ptr(dy, "dy", t, (R, M)), _ptr(z, "z", t, (R, M), required=False),
+            _ptr(dz, "dz", t, (R, M), required=False), _ptr(dbias, "dbias", torch.float32, (M,), required=False), ws,
+            ws_bytes, _stream(stream))
+    _check(st, "moe_linear_backward")
+
+
+def moe_balance_workspace_size(cfg: MoeConfig, N: int, seq_rows: int) -> int:
+    return int(lib().moe_balance_workspace_size(ctypes.byref(cfg), int(N), int(seq_rows)))
+
+
+def moe_balance_loss(cfg: MoeConfig, N: int, scores, topk_idx, seq_rows: int, weight: float, counts, coef, loss,
+                     workspace, token_mask=None, stream=None):
+    """loss[0] = weight * mean over sequences (runs of seq_rows rows) of sum_i f_i P_i, f_i = E / (k V) times the slots
+    that name expert i, P_i the mean of the normalised scores, over the V live tokens (token_mask [N] uint8 or bool).
+    counts [S, E] int32 and coef [S, E] float32 (d loss / d normalised score, for moe_route_backward) may be None."""
+    import torch
+
+    E, k, f = cfg.n_routed_experts, cfg.num_experts_per_tok, torch.float32
+    S = (N + seq_rows - 1) // seq_rows if seq_rows > 0 else 0
+    mask = _token_mask(token_mask, N)
+    ws, ws_bytes = _ws(workspace)
+    with _same_device("moe_balance_loss", scores, topk_idx, token_mask, counts, coef, loss, workspace):
+        st = lib().moe_balance_loss(
+            ctypes.byref(cfg), int(N), int(seq_rows), float(weight), _ptr(scores, "scores", f, (N, E)),
+            _ptr(topk_idx, "topk_idx", torch.int32, (N, k)), mask,
+            _ptr(counts, "counts", torch.int32, (S, E), required=False), _ptr(coef, "coef", f, (S, E), required=False),
+            _ptr(loss, "loss", f, (1,)), ws, ws_bytes, _stream(stream))
+    _check(st, "moe_balance_loss")
+
+
+def _token_mask(t, N):
+    import torch
+
+    return _ptr(t, "token_mask", torch.bool if t is not None and t.dtype == torch.bool else torch.uint8, (N,),
+                required=False)
+
+
+def moe_route_backward(cfg: MoeConfig, N: int, scores, topk_idx, dtopk_w, dlogits, seq_rows: int = 0, coef=None,
+                       dloss=None, token_mask=None, stream=None):
+    """dlogits [N, E] float32 of the router from the gradient of the mixture weights (dtopk_w [N, k], or None) and of the
+    balance loss (coef [S, E] of moe_balance_loss with its seq_rows and token_mask, or None; dloss [1] float32, None: 1)."""
+    import torch
+
+    E, k, f = cfg.n_routed_experts, cfg.num_experts_per_tok, torch.float32
+    S = (N + seq_rows - 1) // seq_rows if seq_rows > 0 else 0
+    mask = _token_mask(token_mask, N)
+    with _same_device("moe_route_backward", scores, topk_idx, dtopk_w, coef, dloss, token_mask, dlogits):
+        st = lib().moe_route_backward(
+            ctypes.byref(cfg), int(N), _ptr(scores, "scores", f, (N, E)),
+            _ptr(topk_idx, "topk_idx", torch.int32, (N, k), required=False),
+            _ptr(dtopk_w, "dtopk_w", f, (N, k), required=False), int(seq_rows),
+            _ptr(coef, "coef", f, (S, E), required=False), _ptr(dloss, "dloss", f, (1,), required=False), mask,
+            _ptr(dlogits, "dlogits", f, (N, E)), _stream(stream))
+    _check(st, "moe_route_backward")
+
+
+class MoeTensorList:
+    """Tensors for moe_grad_norm and moe_grad_clip, described once: calls with the list then cost no walk over it.
+    Holds the tensors, so their memory stays theirs; build it anew when gradients move to other memory."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        for i, t in enumerate(self.tensors):
+            _tensor_dtype(t, f"tensors[{i}]")
+        self.array = (MoeTensor * max(1, len(self.tensors)))(
+            *(MoeTensor(_ptr(t, f"tensors[{i}]"), t.numel(), _tensor_dtype(t, f"tensors[{i}]"))
+              for i, t in enumerate(self.tensors)))
+        _same_device("moe_tensor_list", *self.tensors)
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def moe_tensor_list(tensors) -> MoeTensorList:
+    """A MoeTensorList of contiguous bfloat16 or float32 device tensors of one device (any length; views into a buffer
+    need the alignment of their type alone)."""
+    return tensors if isinstance(tensors, MoeTensorList) else MoeTensorList(tensors)
+
+
+def moe_grad_norm_workspace_size(tensors) -> int:
+    t = moe_tensor_list(tensors)
+    return int(lib().moe_grad_norm_workspace_size(t.array, len(t)))
+
+
+def moe_grad_norm(tensors, norm, workspace, stream=None):
+    """norm[0] = the 2-norm over all values of the tensors (a sequence or a MoeTensorList); workspace:
+    moe_grad_norm_workspace_size(tensors) bytes."""
+    import torch
+
+    t = moe_tensor_list(tensors)
+    ws, ws_bytes = _ws(workspace)
+    with _same_device("moe_grad_norm", *t.tensors[:1], norm, workspace):
+        st = lib().moe_grad_norm(t.array, len(t), _ptr(norm, "norm", torch.float32, (1,)), ws, ws_bytes,
+                                 _stream(stream))
+    _check(st, "moe_grad_norm")
+
+
+def moe_grad_clip(tensors, norm, max_norm: float, out=None, eps: float = 1e-6, stream=None):
+    """out[i] = tensors[i] * min(1, max_norm / (norm[0] + eps)), read on the device; out None: in place. out may have
+    types of its own (bfloat16 gradients clipped into float32 ones)."""
+    import torch
+
+    t = moe_tensor_list(tensors)
+    o = None if out is None else moe_tensor_list(out)
+    if o is not None and len(o) != len(t):
+        raise ValueError(f"out must have {len(t)} tensors, got {len(o)}")
+    with _same_device("moe_grad_clip", *t.tensors[:1], *(o.tensors[:1] if o is not None else ()), norm):
+        st = lib().moe_grad_clip(t.array, None if o is None else o.array, len(t),
+                                 _ptr(norm, "norm", torch.float32, (1,)), float(max_norm), float(eps), _stream(stream))
+    _check(st, "moe_grad_clip")
 
 
 def stage_names() -> list:

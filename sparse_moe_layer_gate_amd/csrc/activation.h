@@ -1,0 +1,144 @@
+// The activations of the linear maps and their derivatives, in float32. FAST: for results rounded to bfloat16, with the
+// hardware exponential and reciprocal and a shorter polynomial for the normal distribution's tail (relative error below 4e-5, a
+// hundredth of the rounding that follows).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "moe_internal.h"
+
+namespace moe {
+
+constexpr float kInvSqrt2Pi = 0.3989422804f;
+constexpr float kGeluTanhA = 0.7978845608f;   // sqrt(2 / pi)
+constexpr float kGeluTanhB = 0.044715f;
+
+template <bool FAST>
+__device__ inline float act_sigmoid(float z) {
+  return FAST ? __builtin_amdgcn_rcpf(1.0f + __expf(-z)) : 1.0f / (1.0f + expf(-z));
+}
+
+// Phi(-a) / exp(-a^2 / 2) for a >= 0: the mass beyond a of the normal distribution over its density's exponential, as a
+// polynomial in 1 / (1 + c a) fitted to erfcx(a / sqrt 2) / 2 by relative error up to a = 14, where the exponential
+// leaves float32: 3.2e-5 with five terms (ROUGH: for values that are rounded to bfloat16 at once), 1.6e-7 with eight.
+template <bool ROUGH>
+__device__ inline float normal_tail_ratio(float a) {
+  if (ROUGH) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.375f, a, 1.0f));
+    float p = fmaf(-0.0906495855f, t, 0.200296755f);
+    p = fmaf(p, t, 0.0835523706f);
+    p = fmaf(p, t, 0.157737649f);
+    p = fmaf(p, t, 0.14906064f);
+    return p * t;
+  }
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, a, 1.0f));
+  float p = fmaf(0.0354239674f, t, -0.156159341f);
+  p = fmaf(p, t, 0.204558206f);
+  p = fmaf(p, t, -0.0520352263f);
+  p = fmaf(p, t, 0.127692364f);
+  p = fmaf(p, t, 0.100175782f);
+  p = fmaf(p, t, 0.120712161f);
+  p = fmaf(p, t, 0.119632006f);
+  return p * t;
+}
+
+template <bool FAST>
+__device__ inline float act_gelu(float z) {
+  // z Phi(z) = max(z, 0) - |z| Phi(-|z|): both tails keep their relative precision
+  const float a = fabsf(z);
+  const float q = (FAST ? __expf(-0.5f * a * a) : expf(-0.5f * a * a)) * normal_tail_ratio<FAST>(a);
+  // |z| q vanishes long before |z| does (an infinite z would make it NaN)
+  return a > 30.0f ? fmaxf(z, 0.f) : fmaf(-a, q, fmaxf(z, 0.f));
+}
+
+template <bool FAST>
+__device__ inline float act_gelu_tanh(float z) {
+  // (1 + tanh(u)) / 2 = sigmoid(2 u)
+  const float u = kGeluTanhA * z * fmaf(kGeluTanhB * z, z, 1.0f);
+  const float y = z * act_sigmoid<FAST>(2.0f * u);
+  return z < -30.0f ? -0.f : y;  // sigmoid is 0 there; the product with an infinity would be NaN
+}
+
+template <bool FAST>
+__device__ inline float act_silu(float z) {
+  const float y = z * act_sigmoid<FAST>(z);
+  return z < -200.0f ? -0.f : y;
+}
+
+// N values at once: one branch on the activation (the same for every thread) for all of them.
+template <bool FAST, int N>
+__device__ inline void act_apply(int act, float* v) {
+  switch (act) {
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];  // a NaN stays one
+      break;
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_silu<FAST>(v[i]);
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = v[i] != v[i] ? v[i] : act_gelu<FAST>(v[i]);
+      break;
+    case MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = act_gelu_tanh<FAST>(v[i]);
+      break;
+    default:
+      break;
+  }
+}
+
+// d act / d z
+template <bool FAST>
+__device__ inline float slope_gelu(float z) {
+  // Phi(z) + z phi(z)
+  const float a = fabsf(z);
+  if (a > 30.0f) return z > 0.f ? 1.f : 0.f;
+  const float e = FAST ? __expf(-0.5f * a * a) : expf(-0.5f * a * a);
+  const float q = e * normal_tail_ratio<false>(a);  // the bias's gradient is a float32 sum of these
+  const float d = a * e * kInvSqrt2Pi;
+  return z > 0.f ? 1.0f - q + d : q - d;
+}
+template <bool FAST>
+__device__ inline float slope_gelu_tanh(float z) {
+  if (fabsf(z) > 30.0f) return z > 0.f ? 1.f : 0.f;
+  const float u2 = 2.0f * kGeluTanhA * z * fmaf(kGeluTanhB * z, z, 1.0f);
+  const float du2 = 2.0f * kGeluTanhA * fmaf(3.0f * kGeluTanhB * z, z, 1.0f);
+  const float s = act_sigmoid<FAST>(u2);
+  return fmaf(z * du2, s * (1.0f - s), s);
+}
+template <bool FAST>
+__device__ inline float slope_silu(float z) {
+  if (fabsf(z) > 200.0f) return z > 0.f ? 1.f : 0.f;
+  const float s = act_sigmoid<FAST>(z);
+  return fmaf(z * s, 1.0f - s, s);
+}
+
+// d[i] *= act'(z[i])
+template <bool FAST, int N>
+__device__ inline void act_slope_times(int act, const float* z, float* d) {
+  switch (act) {
+    case MOE_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) d[i] = z[i] > 0.f ? d[i] : z[i] != z[i] ? z[i] : 0.f * d[i];
+      break;
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) d[i] *= z[i] != z[i] ? z[i] : slope_silu<FAST>(z[i]);
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < N; ++i) d[i] *= z[i] != z[i] ? z[i] : slope_gelu<FAST>(z[i]);
+      break;
+    case MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < N; ++i) d[i] *= z[i] != z[i] ? z[i] : slope_gelu_tanh<FAST>(z[i]);
+      break;
+    default:
+      break;
+  }
+}
+
+}  // namespace moe

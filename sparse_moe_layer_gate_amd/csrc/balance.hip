@@ -1,0 +1,373 @@
+// The balance loss of a routed batch, per sequence, with the counts behind it, and the gradient of the router's
+// logits. For a sequence of V live tokens, with p = s / sum(s) over a token's scores:
+//
+//   c_i = slots that name i    f_i = E c_i / (k V)    P_i = sum_tokens p_i / V    loss = weight / S sum_seq sum_i f_i P_i
+//
+// The loss is linear in p once the counts are constants: d loss / d p_i = weight / S f_i / V = coef_i, and through
+// the normalisation d loss / d s_i = (coef_i - sum_j coef_j p_j) / sum(s). The weights w_m = alpha s_m / D give
+// ds_m = alpha / D (dw_m - sum_l dw_l s_l / D); both meet in dlogit = ds s (1 - s).
+//
+// Both directions read the scores once (N E float32) and are bound by that, or for usual batches, which fit the
+// caches, by latency: a row belongs to a group of 8 to 64 lanes, so that its sums are shuffles.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "ops_internal.h"
+#include "row_ops.h"
+
+namespace moe {
+namespace {
+
+// Sum over the G lanes of a group, the same in each.
+template <int G>
+__device__ inline float group_sum(float v) {
+#pragma unroll
+  for (int off = G / 2; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+struct BalanceArgs {
+  int64_t N, T;  // T <= N
+  int E, k;
+  int64_t S;
+  int64_t chunk, chunks;  // rows per block, blocks per sequence
+  float weight;           // over S
+  const float* scores;
+  const int32_t* idx;
+  const uint8_t* mask;
+  int32_t* counts;  // [S, E] or nullptr
+  float* coef;      // [S, E] or nullptr
+  float* loss;
+  float* part_p;    // [S chunks, E] sums of p
+  int32_t* part_c;  // [S chunks, E] slots
+  int32_t* part_v;  // [S chunks] live tokens
+  float* part_l;    // [S] losses of the sequences
+};
+
+// The end of a sequence: f and P of one expert from its sums; returns f P weight / S.
+__device__ inline float finish_expert(const BalanceArgs& a, int64_t q, int e, float p, int32_t c, int32_t v) {
+  const float live = (float)max(v, 1);
+  const float f = (float)c * (float)a.E / ((float)a.k * live);
+  if (a.counts) a.counts[q * a.E + e] = c;
+  if (a.coef) a.coef[q * a.E + e] = a.weight * f / live;
+  return a.weight * f * (p / live);
+}
+
+// Sum of one float per thread over the block, in a fixed order, valid in thread 0.
+__device__ inline float block_total(float v, float* buf) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float t = 0.f;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) t += buf[w];
+  return t;
+}
+
+// One chunk of a sequence's rows: a group of G lanes per row, lane j holding experts j + G i. Live tokens add to the
+// sums in registers, the slots to a histogram in LDS (whole numbers: the order does not matter). A sequence of one
+// chunk is finished here.
+template <int G, int EPL>
+__global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
+  __shared__ float sum[16][G * EPL];
+  __shared__ int32_t hist[G * EPL];
+  __shared__ int32_t live_rows;
+  __shared__ float buf[16];
+  const int64_t q = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks;
+  const int64_t first = q * a.T + ch * a.chunk;
+  const int64_t last = min(min(first + a.chunk, (q + 1) * a.T), a.N);
+  const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
+  for (int e = threadIdx.x; e < G * EPL; e += blockDim.x) hist[e] = 0;
+  if (threadIdx.x == 0) live_rows = 0;
+  __syncthreads();
+  const int lane = threadIdx.x % G;
+  const int groups = blockDim.x / G;
+  float acc[EPL];
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
+  for (int64_t n = first + threadIdx.x / G; n < last; n += groups) {
+    if (a.mask && a.mask[n] == 0) continue;  // the same for the lanes of a group
+    float v[EPL], s = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + G * i;
+      v[i] = e < a.E ? a.scores[n * a.E + e] : 0.f;
+      s += v[i];
+    }
+    s = group_sum<G>(s);
+    const float inv = s != 0.f ? 1.0f / s : 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) acc[i] += v[i] * inv;
+    for (int m = lane; m < a.k; m += G) {
+      const int32_t e = a.idx[n * a.k + m];
+      if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
+    }
+    mine += lane == 0;
+  }
+  if (mine) atomicAdd(&live_rows, mine);
+  // the groups of a wave, then the waves in order
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+#pragma unroll
+    for (int off = G; off < 64; off <<= 1) acc[i] += __shfl_xor(acc[i], off);
+    if ((threadIdx.x & 63) < G) sum[wave][lane + G * i] = acc[i];
+  }
+  __syncthreads();
+  float loss = 0.f;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    float p = 0.f;
+    for (int w = 0; w < waves; ++w) p += sum[w][e];
+    if (a.chunks == 1) {
+      loss += finish_expert(a, q, e, p, hist[e], live_rows);
+    } else {
+      a.part_p[(int64_t)blockIdx.x * a.E + e] = p;
+      a.part_c[(int64_t)blockIdx.x * a.E + e] = hist[e];
+    }
+  }
+  if (a.chunks == 1) {
+    loss = block_total(loss, buf);
+    if (threadIdx.x == 0) (a.S == 1 ? a.loss : a.part_l + q)[0] = loss;
+  } else if (threadIdx.x == 0) {
+    a.part_v[blockIdx.x] = live_rows;
+  }
+}
+
+// The chunks of one sequence, in order: E experts x 1024 / E lanes.
+__global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
+  __shared__ float sp[1024];
+  __shared__ int32_t sc[1024];
+  __shared__ int32_t sv[16];
+  __shared__ float buf[16];
+  const int64_t q = blockIdx.x, base = q * a.chunks;
+  int v = 0;
+  for (int64_t ch = threadIdx.x; ch < a.chunks; ch += blockDim.x) v += a.part_v[base + ch];
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  if ((threadIdx.x & 63) == 0) sv[threadIdx.x >> 6] = v;
+  const int lanes = 1024 / a.E;  // at least 2
+  const int e = threadIdx.x % a.E, l = threadIdx.x / a.E;
+  float p = 0.f;
+  int32_t c = 0;
+  if (l < lanes) {
+#pragma unroll 8
+    for (int64_t ch = l; ch < a.chunks; ch += lanes) {
+      p += a.part_p[(base + ch) * a.E + e];
+      c += a.part_c[(base + ch) * a.E + e];
+    }
+    sp[l * a.E + e] = p;
+    sc[l * a.E + e] = c;
+  }
+  __syncthreads();
+  float loss = 0.f;
+  if (threadIdx.x < a.E) {
+    for (int i = 1; i < lanes; ++i) {
+      p += sp[i * a.E + e];
+      c += sc[i * a.E + e];
+    }
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) v += sv[w];
+    loss = finish_expert(a, q, e, p, c, v);
+  }
+  loss = block_total(loss, buf);
+  if (threadIdx.x == 0) (a.S == 1 ? a.loss : a.part_l + q)[0] = loss;
+}
+
+__global__ __launch_bounds__(1024) void balance_total(const float* part, int64_t n, float* loss) {
+  __shared__ float buf[16];
+  float s = 0.f;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+  s = block_total(s, buf);
+  if (threadIdx.x == 0) *loss = s;
+}
+
+struct RouteBackArgs {
+  int64_t N, T;
+  int E, k;
+  float alpha, eps;
+  int norm;
+  const float* scores;
+  const int32_t* idx;
+  const float* dw;
+  const float* coef;
+  const float* dloss;
+  const uint8_t* mask;
+  float* out;
+};
+
+// A group of G lanes per token, lane j holding experts j + G i and, as a slot's owner, slots j + G m. dlogits may be
+// the scores: a group reads its row before it writes it.
+template <int G, int EPL>
+__global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
+  constexpr int SPL = (32 + G - 1) / G;  // slots per lane (k <= 32)
+  const int lane = threadIdx.x % G;
+  const int64_t n = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
+  if (n >= a.N) return;  // whole groups
+  const float* row = a.scores + n * a.E;
+  float s[EPL], ds[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + G * i;
+    s[i] = e < a.E ? row[e] : 0.f;
+    ds[i] = 0.f;
+  }
+  if (a.coef && (!a.mask || a.mask[n] != 0)) {
+    const float* co = a.coef + n / a.T * a.E;
+    const float g = a.dloss ? *a.dloss : 1.0f;
+    float c[EPL], sum = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + G * i;
+      c[i] = e < a.E ? co[e] : 0.f;
+      sum += s[i];
+      dot += c[i] * s[i];
+    }
+    sum = group_sum<G>(sum);
+    dot = group_sum<G>(dot);
+    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) ds[i] = g * inv * (c[i] - dot * inv);
+  }
+  if (a.dw) {
+    int32_t id[SPL];
+    float v[SPL], w[SPL], total = 0.f, dot = 0.f;
+#pragma unroll
+    for (int m = 0; m < SPL; ++m) {
+      const int slot = lane + G * m;
+      id[m] = slot < a.k ? a.idx[n * a.k + slot] : -1;
+      const bool ok = id[m] >= 0 && id[m] < a.E;
+      v[m] = ok ? row[id[m]] : 0.f;
+      w[m] = ok ? a.dw[n * a.k + slot] : 0.f;
+      total += v[m];
+      dot += v[m] * w[m];
+    }
+    if (a.norm) {
+      total = group_sum<G>(total) + a.eps;
+      dot = group_sum<G>(dot);
+      const float r = total != 0.f ? 1.0f / total : 0.f;
+#pragma unroll
+      for (int m = 0; m < SPL; ++m) w[m] = a.alpha * r * (w[m] - dot * r);
+    } else {
+#pragma unroll
+      for (int m = 0; m < SPL; ++m) w[m] *= a.alpha;
+    }
+    // every slot to the lane and value of its expert (an id may come up twice: each adds)
+    for (int slot = 0; slot < a.k; ++slot) {
+      int32_t e = id[0];
+      float b = w[0];
+#pragma unroll
+      for (int m = 1; m < SPL; ++m)
+        if (slot / G == m) {
+          e = id[m];
+          b = w[m];
+        }
+      e = __shfl(e, slot % G, G);
+      b = __shfl(b, slot % G, G);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (e == lane + G * i) ds[i] += b;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + G * i;
+    if (e < a.E) a.out[n * a.E + e] = ds[i] == 0.f ? 0.f : ds[i] * s[i] * (1.0f - s[i]);  // whatever a dead token holds
+  }
+}
+
+// Lanes of a row's group and experts per lane.
+int lanes_of(int E) { return E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64; }
+
+// Calls f with the two as compile-time values.
+template <typename F>
+hipError_t with_shape(int E, F f) {
+  using std::integral_constant;
+  const int G = lanes_of(E);
+  if (G == 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  if (G == 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (G == 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  const integral_constant<int, 64> g{};
+  switch ((E + 63) / 64) {
+    case 1: return f(g, integral_constant<int, 1>{});
+    case 2: return f(g, integral_constant<int, 2>{});
+    case 3: return f(g, integral_constant<int, 3>{});
+    case 4: return f(g, integral_constant<int, 4>{});
+    case 5: return f(g, integral_constant<int, 5>{});
+    case 6: return f(g, integral_constant<int, 6>{});
+    case 7: return f(g, integral_constant<int, 7>{});
+    case 8: return f(g, integral_constant<int, 8>{});
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+// Rows of a block: a few per group of lanes, so that the batch fills the CUs about twice; a sequence is never shared
+// by more than 512 blocks.
+BalancePlan balance_plan(int64_t N, int64_t T, int E) {
+  BalancePlan p{};
+  p.T = T < N ? T : N;
+  if (p.T < 1) p.T = 1;
+  p.S = (N + p.T - 1) / p.T;
+  const int64_t wide = (p.T + 511) / 512;
+  p.chunk = wide > 32 ? wide : 32;
+  if (p.chunk > p.T) p.chunk = p.T;
+  p.chunks = (p.T + p.chunk - 1) / p.chunk;
+  const int64_t rows = 64 / lanes_of(E);  // of a wave at a time
+  const int64_t waves = (p.chunk + 2 * rows - 1) / (2 * rows);
+  p.threads = 64 * (int)(waves < 1 ? 1 : waves > 16 ? 16 : waves);
+  return p;
+}
+
+hipError_t launch_balance(const BalanceCall& c, hipStream_t s) {
+  const BalancePlan p = balance_plan(c.N, c.T, c.E);
+  BalanceArgs a{};
+  a.N = c.N;
+  a.T = p.T;
+  a.E = c.E;
+  a.k = c.k;
+  a.S = p.S;
+  a.chunk = p.chunk;
+  a.chunks = p.chunks;
+  a.weight = c.weight / (float)p.S;
+  a.scores = c.scores;
+  a.idx = c.idx;
+  a.mask = c.mask;
+  a.counts = c.counts;
+  a.coef = c.coef;
+  a.loss = c.loss;
+  a.part_p = c.part_p;
+  a.part_c = c.part_c;
+  a.part_v = c.part_v;
+  a.part_l = c.part_l;
+  hipError_t e = with_shape(c.E, [&](auto g, auto epl) {
+    hipLaunchKernelGGL((balance_chunks<decltype(g)::value, decltype(epl)::value>), dim3((unsigned)(p.S * p.chunks)),
+                       dim3(p.threads), 0, s, a);
+    return hipGetLastError();
+  });
+  if (e == hipSuccess && p.chunks > 1) {
+    hipLaunchKernelGGL(balance_join, dim3((unsigned)p.S), dim3(1024), 0, s, a);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess && p.S > 1) {
+    hipLaunchKernelGGL(balance_total, dim3(1), dim3(1024), 0, s, (const float*)a.part_l, p.S, a.loss);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+int64_t route_backward_blocks(int64_t N, int E) { return (N + 256 / lanes_of(E) - 1) / (256 / lanes_of(E)); }
+
+hipError_t launch_route_backward(const RouteBackCall& c, hipStream_t s) {
+  RouteBackArgs a{c.N, c.T < c.N ? c.T : c.N, c.E, c.k, c.alpha, c.eps, c.norm, c.scores, c.idx, c.dw, c.coef, c.dloss, c.mask,
+                  c.out};
+  return with_shape(c.E, [&](auto g, auto epl) {
+    hipLaunchKernelGGL((route_backward<decltype(g)::value, decltype(epl)::value>),
+                       dim3((unsigned)route_backward_blocks(c.N, c.E)), dim3(256), 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace moe

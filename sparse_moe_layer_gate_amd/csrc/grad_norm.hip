@@ -1,0 +1,258 @@
+// The 2-norm over many tensors, and the tensors scaled to at most a given norm:
+//
+//   norm = sqrt(sum over all values of g^2)      out = g min(1, max_norm / (norm + eps))
+//
+// Squares and sums are float64: a square of a float32 is exact in it and cannot overflow, and the vector unit's
+// float64 rate leaves the pass bound by HBM. Tensors of any length, type and alignment of their own are cut into
+// chunks of kChunk values, one block each; a block finds its tensor in the launch's table (kernel arguments, so
+// nothing has to outlive the call) by bisection. The clip walks the chunks backwards: what the norm's pass read last
+// is still in the last-level cache (256 MiB).
+#include <hip/hip_runtime.h>
+
+#include <utility>
+
+#include "ops_internal.h"
+#include "row_ops.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 8;  // pieces of eight values per thread and chunk
+constexpr int64_t kChunk = (int64_t)kThreads * 8 * kPieces;
+constexpr int kTable = 100;  // tensors per launch: the table stays below the 4 KiB of kernel arguments
+
+struct Table {
+  const void* in[kTable];
+  void* out[kTable];
+  int64_t numel[kTable];
+  int32_t first[kTable + 1];  // first chunk of each tensor; [n]: chunks in all
+  uint8_t in_bf16[kTable], out_bf16[kTable];
+  int n;
+};
+static_assert(sizeof(Table) <= 4000, "kernel arguments");
+
+// Eight values at an address that has the alignment of their type alone.
+template <typename T>
+struct Unaligned8;
+template <>
+struct __attribute__((packed, aligned(2))) Unaligned8<uint16_t> {
+  u32x4 v;
+};
+template <>
+struct __attribute__((packed, aligned(4))) Unaligned8<float> {
+  f32x4v a, b;
+};
+__device__ inline void load8u(const uint16_t* p, float* f) {
+  widen8(Raw8<uint16_t>{((const Unaligned8<uint16_t>*)p)->v}, f);
+}
+__device__ inline void load8u(const float* p, float* f) {
+  const auto* q = (const Unaligned8<float>*)p;
+  widen8(Raw8<float>{q->a, q->b}, f);
+}
+__device__ inline void store8u(uint16_t* p, const float* f) {
+  u32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = bf16_pair(f[2 * i], f[2 * i + 1]);
+  ((Unaligned8<uint16_t>*)p)->v = v;
+}
+__device__ inline void store8u(float* p, const float* f) {
+  auto* q = (Unaligned8<float>*)p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    q->a[i] = f[i];
+    q->b[i] = f[4 + i];
+  }
+}
+__device__ inline float load1(const uint16_t* p) { return bf16_f32(*p); }
+__device__ inline float load1(const float* p) { return *p; }
+__device__ inline void store1(uint16_t* p, float f) { *p = (uint16_t)(bf16_pair(f, 0.f) & 0xffffu); }
+__device__ inline void store1(float* p, float f) { *p = f; }
+
+// The tensor that holds chunk c (uniform over the block).
+__device__ inline int tensor_of(const Table& t, int c) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= c)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+template <typename T>
+__device__ inline double chunk_squares(const T* p, int64_t n) {
+  double s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = 0.0;
+  const int64_t whole = n / 8;
+#pragma unroll
+  for (int v = 0; v < kPieces; ++v) {
+    const int64_t at = threadIdx.x + (int64_t)v * kThreads;
+    if (at < whole) {
+      float f[8];
+      load8u(p + at * 8, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] += (double)f[i] * (double)f[i];
+    }
+  }
+  const int64_t tail = whole * 8 + threadIdx.x;
+  if (tail < n) s[0] += (double)load1(p + tail) * (double)load1(p + tail);
+  return ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+}
+
+// Sum over the block in a fixed order, valid in thread 0.
+__device__ inline double block_sum(double v, double* buf) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double t = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) t += buf[w];
+  return t;
+}
+
+__global__ __launch_bounds__(kThreads) void norm_chunks(Table t, double* part) {
+  __shared__ double buf[kThreads / 64];
+  const int c = blockIdx.x, i = tensor_of(t, c);
+  const int64_t at = (int64_t)(c - t.first[i]) * kChunk, n = min(kChunk, t.numel[i] - at);
+  const double s = t.in_bf16[i] ? chunk_squares((const uint16_t*)t.in[i] + at, n)
+                                : chunk_squares((const float*)t.in[i] + at, n);
+  const double b = block_sum(s, buf);
+  if (threadIdx.x == 0) part[c] = b;
+}
+
+__global__ __launch_bounds__(1024) void norm_total(const double* part, int64_t n, float* norm) {
+  __shared__ double buf[16];
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int64_t i = threadIdx.x; i < n; i += 4096) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + 1024 * j < n) s[j] += part[i + 1024 * j];
+  }
+  const double b = block_sum((s[0] + s[1]) + (s[2] + s[3]), buf);
+  if (threadIdx.x == 0) *norm = (float)sqrt(b);
+}
+
+template <typename T, typename U>
+__device__ inline void scale_chunk(const T* p, U* o, int64_t n, float scale) {
+  const int64_t whole = n / 8;
+#pragma unroll
+  for (int v = 0; v < kPieces; ++v) {
+    const int64_t at = threadIdx.x + (int64_t)v * kThreads;
+    if (at < whole) {
+      float f[8];
+      load8u(p + at * 8, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= scale;
+      store8u(o + at * 8, f);
+    }
+  }
+  const int64_t tail = whole * 8 + threadIdx.x;
+  if (tail < n) store1(o + tail, load1(p + tail) * scale);
+}
+
+__global__ __launch_bounds__(kThreads) void clip_chunks(Table t, const float* norm, float max_norm, float eps,
+                                                        int in_place) {
+  const float ratio = max_norm / (*norm + eps);
+  const float scale = ratio >= 1.0f ? 1.0f : ratio;  // a NaN stays one
+  if (in_place && scale == 1.0f) return;
+  const int c = t.first[t.n] - 1 - (int)blockIdx.x, i = tensor_of(t, c);
+  const int64_t at = (int64_t)(c - t.first[i]) * kChunk, n = min(kChunk, t.numel[i] - at);
+  const uint16_t* pb = (const uint16_t*)t.in[i] + at;
+  const float* pf = (const float*)t.in[i] + at;
+  uint16_t* ob = (uint16_t*)t.out[i] + at;
+  float* of = (float*)t.out[i] + at;
+  if (t.in_bf16[i])
+    t.out_bf16[i] ? scale_chunk(pb, ob, n, scale) : scale_chunk(pb, of, n, scale);
+  else
+    t.out_bf16[i] ? scale_chunk(pf, ob, n, scale) : scale_chunk(pf, of, n, scale);
+}
+
+int64_t chunks_of(const moe_tensor& t) { return (t.numel + kChunk - 1) / kChunk; }
+
+// Tables of up to kTable tensors and kMost chunks (a longer tensor is cut); f(table, the chunks before it). Backwards:
+// the last table first.
+template <typename F>
+hipError_t for_tables(const moe_tensor* in, const moe_tensor* out, int n, bool backwards, F f) {
+  constexpr int64_t kMost = (int64_t)1 << 22;
+  int i = backwards ? n - 1 : 0;  // the tensor at hand, and how many of its chunks earlier tables hold
+  int64_t cut = 0, before = backwards ? tensor_chunks(in, n) : 0;
+  Table t;
+  while (i >= 0 && i < n) {
+    int64_t count = 0, size[kTable];
+    t.n = 0;
+    for (; i >= 0 && i < n && t.n < kTable && count < kMost; ) {
+      const int64_t left = chunks_of(in[i]) - cut, take = left < kMost - count ? left : kMost - count;
+      if (take > 0) {
+        const int j = t.n++;
+        const moe_tensor& o = out ? out[i] : in[i];
+        // whole tables leave the end of a tensor to the next one, or backwards its beginning
+        const int64_t at = (backwards ? left - take : cut) * kChunk;
+        t.in_bf16[j] = in[i].dtype == MOE_BF16;
+        t.out_bf16[j] = o.dtype == MOE_BF16;
+        t.in[j] = (const char*)in[i].data + at * (t.in_bf16[j] ? 2 : 4);
+        t.out[j] = (char*)o.data + at * (t.out_bf16[j] ? 2 : 4);
+        t.numel[j] = in[i].numel - at < take * kChunk ? in[i].numel - at : take * kChunk;
+        size[j] = take;
+        count += take;
+      }
+      if (take < left) {
+        cut += take;
+        break;
+      }
+      cut = 0;
+      i += backwards ? -1 : 1;
+    }
+    if (t.n == 0) break;
+    if (backwards) {
+      for (int a = 0, b = t.n - 1; a < b; ++a, --b) {
+        std::swap(t.in[a], t.in[b]);
+        std::swap(t.out[a], t.out[b]);
+        std::swap(t.numel[a], t.numel[b]);
+        std::swap(t.in_bf16[a], t.in_bf16[b]);
+        std::swap(t.out_bf16[a], t.out_bf16[b]);
+        std::swap(size[a], size[b]);
+      }
+      before -= count;
+    }
+    t.first[0] = 0;
+    for (int j = 0; j < t.n; ++j) t.first[j + 1] = (int32_t)(t.first[j] + size[j]);
+    const hipError_t e = f(t, before, count);
+    if (e != hipSuccess) return e;
+    if (!backwards) before += count;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+int64_t tensor_chunks(const moe_tensor* t, int n) {
+  int64_t c = 0;
+  for (int i = 0; i < n; ++i) c += chunks_of(t[i]);
+  return c;
+}
+
+hipError_t launch_grad_norm(const moe_tensor* t, int n, double* part, float* norm, hipStream_t s) {
+  const hipError_t e = for_tables(t, nullptr, n, false, [&](const Table& tab, int64_t before, int64_t count) {
+    hipLaunchKernelGGL(norm_chunks, dim3((unsigned)count), dim3(kThreads), 0, s, tab, part + before);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(norm_total, dim3(1), dim3(1024), 0, s, (const double*)part, tensor_chunks(t, n), norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(const moe_tensor* t, const moe_tensor* out, int n, const float* norm, float max_norm,
+                            float eps, hipStream_t s) {
+  return for_tables(t, out, n, true, [&](const Table& tab, int64_t, int64_t count) {
+    hipLaunchKernelGGL(clip_chunks, dim3((unsigned)count), dim3(kThreads), 0, s, tab, norm, max_norm, eps,
+                       out ? 0 : 1);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace moe

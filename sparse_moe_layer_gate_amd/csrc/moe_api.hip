@@ -41,7 +41,6 @@ moe_status check_n(const moe_config* c, int64_t N) {
   return MOE_OK;
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // The bf16 prefill GEMM addresses gathered rows of x and each expert matrix with 32-bit byte offsets
 // (gemm_bf16.hip): x of N rows and every [rows, K] weight slab must stay under 4 GiB.
@@ -197,7 +196,9 @@ hipEvent_t next_event() {
 const char* kStageNames[ST_ALL_STAGES] = {"router_split", "router_logits", "router_select",  "dispatch_count",
                                             "dispatch_scan", "dispatch_place", "experts_gate_up", "experts_down",
                                             "combine", "block_norm", "grouped_lists", "grouped_linear", "qlinear",
-                                            "quantize"};
+                                            "quantize",
+                                            "layer_norm", "linear", "balance", "route_backward", "grad_norm",
+                                            "grad_clip"};
 
 // Router. wg is the float32 router weight, or (prepared) the three bf16 pieces of moe_router_prepare;
 // scores is read (MOE_ROUTE_SCORES_IN), written (non-null otherwise) or not kept (null).

@@ -13,17 +13,8 @@ using namespace moe;
 namespace {
 
 constexpr int kMaxE = 512, kMaxK = 32, kMaxNormD = 16384;
-constexpr int64_t kInt31 = (int64_t)1 << 31, kGiB4 = (int64_t)1 << 32;
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-template <typename... P>
-bool all_aligned16(P... p) {
-  return (aligned16(p) && ...);
-}
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
-// A launch holds fewer than 2^32 threads: what would take more is refused here, before anything is launched.
-bool launch_fits(int64_t blocks, int64_t threads) { return blocks <= (kGiB4 - 1) / threads; }
-bool dtype_ok(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
 
 moe_status check_norm(int64_t N, int32_t D, int32_t dtype, float eps, float a) {
   if (N < 0 || D < 1 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;

@@ -1,5 +1,6 @@
 // Internal declarations of the operators around the layer (block norms, combine, grouped products, 4-bit
-// products), shared by their translation units.
+// products) and of a training step (layer norm, linear maps, balance loss, gradient norm), shared by their
+// translation units.
 #pragma once
 
 #include "moe_internal.h"
@@ -13,6 +14,12 @@ enum OpStage {
   ST_GROUPED_LINEAR,                // moe_grouped_linear and its gradients
   ST_QLINEAR,                       // moe_qlinear
   ST_QUANTIZE,                      // moe_quantize
+  ST_LAYER_NORM,                    // moe_layer_norm and its gradients
+  ST_LINEAR,                        // moe_linear and its gradients
+  ST_BALANCE,                       // moe_balance_loss
+  ST_ROUTE_BACKWARD,                // moe_route_backward
+  ST_GRAD_NORM,                     // moe_grad_norm
+  ST_GRAD_CLIP,                     // moe_grad_clip
   ST_ALL_STAGES
 };
 
@@ -24,6 +31,17 @@ enum OpStage {
     prof_after((stage), s);                  \
     if (e_ != hipSuccess) return MOE_ERR_HIP; \
   } while (0)
+
+// ---- argument checks ----
+constexpr int64_t kInt31 = (int64_t)1 << 31, kGiB4 = (int64_t)1 << 32;
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+template <typename... P>
+bool all_aligned16(P... p) {
+  return (aligned16(p) && ...);
+}
+// A launch holds fewer than 2^32 threads: what would take more is refused here, before anything is launched.
+inline bool launch_fits(int64_t blocks, int64_t threads) { return blocks <= (kGiB4 - 1) / threads; }
+inline bool dtype_ok(int32_t t) { return t == MOE_F32 || t == MOE_BF16; }
 
 // ---- combine ----
 int combine_threads(int D);  // of the one block per token
@@ -113,5 +131,94 @@ struct QuantArgs {
 hipError_t launch_qlinear(const QuantArgs& a, hipStream_t s);
 hipError_t launch_quantize(int dtype, const void* w, int64_t rows, int K, int group, uint8_t* q, uint16_t* s,
                            hipStream_t st);
+
+// ---- layer norm ----
+struct LayerNormCall {
+  int64_t N;
+  int D;
+  float eps;
+  const void *x, *residual, *w, *b;  // backward: x is h
+  void *h_out, *y;
+  float* stats;
+  const void *dh_out, *dy;  // backward
+  void* dh;
+  float *dw, *db, *part;
+};
+int layer_norm_threads(int D);  // of a row in the forward pass
+int64_t layer_norm_blocks(int64_t N, int D);
+int64_t layer_norm_runs(int D);  // most runs of rows, each with a partial row of dw and of db
+hipError_t launch_layer_norm(int dtype, const LayerNormCall& c, bool backward, hipStream_t s);
+// dst[c] = sum over rows of src[r, c], in a fixed order, for one or two (src1 not null) arrays [rows, D]; D a multiple
+// of 4
+hipError_t launch_column_sums(const float* src0, float* dst0, const float* src1, float* dst1, int64_t rows, int D,
+                              hipStream_t s);
+
+// ---- linear maps ----
+struct LinearCall {
+  int64_t R;
+  int in, out, act;
+  const void *x, *w, *bias, *residual;
+  void *z, *y;
+  float* part;
+};
+struct LinearPlan {
+  int bm, bn;  // rows and columns of a tile
+  int splits;  // parts of the reduction
+};
+LinearPlan linear_plan(int dtype, int64_t R, int in, int out);
+size_t linear_part_bytes(int dtype, int64_t R, int out);  // workspace; never falls as R grows
+int64_t linear_join_blocks(int64_t R, int out);
+hipError_t launch_linear(int dtype, const LinearCall& c, hipStream_t s);
+struct LinearBackCall {
+  int64_t R;
+  int out, act;
+  const void *dy, *z;
+  void* dz;
+  float *dbias, *part;
+};
+int64_t linear_back_runs(int64_t R);  // partial rows of dbias
+hipError_t launch_linear_back(int dtype, const LinearBackCall& c, hipStream_t s);
+
+// ---- balance loss and the router's gradient ----
+struct BalancePlan {
+  int64_t T, S;           // rows per sequence (at most N), sequences
+  int64_t chunk, chunks;  // rows per block, blocks per sequence
+  int threads;
+};
+BalancePlan balance_plan(int64_t N, int64_t T, int E);
+struct BalanceCall {
+  int64_t N, T;
+  int E, k;
+  float weight;
+  const float* scores;
+  const int32_t* idx;
+  const uint8_t* mask;
+  int32_t* counts;
+  float *coef, *loss;
+  float* part_p;    // [S chunks, E], with more than one chunk
+  int32_t* part_c;  // [S chunks, E]
+  int32_t* part_v;  // [S chunks]
+  float* part_l;    // [S], with more than one sequence
+};
+hipError_t launch_balance(const BalanceCall& c, hipStream_t s);
+struct RouteBackCall {
+  int64_t N, T;
+  int E, k;
+  float alpha, eps;
+  int norm;
+  const float* scores;
+  const int32_t* idx;
+  const float *dw, *coef, *dloss;
+  const uint8_t* mask;
+  float* out;
+};
+int64_t route_backward_blocks(int64_t N, int E);  // of 256 threads
+hipError_t launch_route_backward(const RouteBackCall& c, hipStream_t s);
+
+// ---- gradient norm and clipping ----
+int64_t tensor_chunks(const moe_tensor* t, int n);  // partial sums of a list
+hipError_t launch_grad_norm(const moe_tensor* t, int n, double* part, float* norm, hipStream_t s);
+hipError_t launch_grad_clip(const moe_tensor* t, const moe_tensor* out, int n, const float* norm, float max_norm,
+                            float eps, hipStream_t s);
 
 }  // namespace moe

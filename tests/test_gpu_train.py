@@ -1,0 +1,447 @@
+"""The operators of a training step on the GPU, through the C ABI, against float64 references on the CPU
+(tests/_train.py, where the bounds are derived)."""
+import math
+
+import pytest
+import torch
+
+import sparse_moe_layer_gate_amd as moe
+from tests import _train as R
+from tests._ops import check
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+TYPES = {"bf16": BF, "f32": F32}
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def dev(t):
+    return None if t is None else t.cuda()
+
+
+def f64(t):
+    return None if t is None else t.double()
+
+
+def workspace(n):
+    return torch.empty(max(int(n), 256), dtype=torch.uint8, device="cuda").fill_(0xFF)
+
+
+def rand(g, *shape, std=1.0, mean=0.0, dtype=F32):
+    return (torch.randn(shape, generator=g) * std + mean).to(dtype)
+
+
+# ---------------------------------------------------------------- layer norm
+LN_CASES = [
+    # N, D: one row and many, every width of a group of lanes, its edges, two and four pieces, blocks of one to four
+    (1, 8), (3, 56), (700, 64), (33, 72), (257, 128), (130, 136), (65, 256), (9, 264), (70, 512), (5, 520), (31, 1024),
+    (6, 1032), (40, 2048), (3, 2056), (300, 2560), (1, 6144), (7, 8192), (4, 8200), (2, 16384), (1500, 40),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,D", LN_CASES)
+def test_layer_norm(N, D, dtype):
+    dt, eps = TYPES[dtype], 1e-5
+    print(f"[layer norm] N={N} D={D} {dtype}", flush=True)
+    g = gen(N + D)
+    x, res = rand(g, N, D, std=2.0, mean=0.7, dtype=dt), rand(g, N, D, dtype=dt)
+    w, b = rand(g, D, std=0.2, mean=1.0, dtype=dt), rand(g, D, dtype=dt)
+    dy, dv = rand(g, N, D, dtype=dt), rand(g, N, D, dtype=dt)
+    ws = workspace(moe.moe_layer_norm_workspace_size(N, D, dtype))
+    for residual, ww, bb, dvv in ((res, w, b, dv), (None, w, None, None), (None, None, None, dv), (res, None, b, None)):
+        y = torch.empty((N, D), dtype=dt, device="cuda")
+        h = torch.empty_like(y) if residual is not None else None
+        stats = torch.empty((N, 2), device="cuda")
+        moe.moe_layer_norm(N, dev(x), dev(residual), dev(ww), dev(bb), h, y, stats, eps=eps)
+        torch.cuda.synchronize()
+        ref, bound = R.layer_norm(f64(x), f64(residual), f64(ww), f64(bb), eps)
+        for name, got, r, e in zip(("h", "y", "stats"), (h, y, stats), ref, bound):
+            if r is not None:
+                check(name, got, r, e)
+        y2 = torch.empty_like(y)  # without stats, and in place over x
+        moe.moe_layer_norm(N, (x2 := dev(x).clone()), dev(residual), dev(ww), dev(bb), None if h is None else x2, y2,
+                           eps=eps)
+        assert torch.equal(y, y2) and (h is None or torch.equal(h, x2))
+        # backward, from what the forward left
+        hh = x if h is None else h.cpu()
+        dh, dw, db = torch.empty_like(y), torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+        moe.moe_layer_norm_backward(N, dev(hh), stats, dev(ww), dev(dvv), dev(dy), dh, dw, db, ws)
+        torch.cuda.synchronize()
+        ref, bound = R.layer_norm_backward(f64(hh), f64(stats.cpu()), f64(ww), f64(dvv), f64(dy))
+        for name, got, r, e in zip(("dh", "dw", "db"), (dh, dw, db), ref, bound):
+            check(name, got, r, e)
+        for want in ((True, False), (False, True), (False, False)):  # some of the sums; dh over dh_out
+            dh2 = dev(dvv).clone() if dvv is not None else torch.empty_like(dh)
+            s = [torch.full((D,), 7.0, device="cuda") if v else None for v in want]
+            moe.moe_layer_norm_backward(N, dev(hh), stats, dev(ww), dh2 if dvv is not None else None, dev(dy), dh2, *s,
+                                        ws if any(want) else None)
+            assert torch.equal(dh2, dh)
+            for got, full in zip(s, (dw, db)):
+                assert got is None or torch.equal(got, full)
+
+
+def test_layer_norm_large_mean():
+    """A common offset a million times the spread: the spread is what float32 holds of it, exactly."""
+    N, D = 5, 4096
+    x = (torch.arange(D) % 7 - 3).float()[None] * torch.ones(N, 1) + 2.0 ** 20
+    y, stats = torch.empty((N, D), device="cuda"), torch.empty((N, 2), device="cuda")
+    moe.moe_layer_norm(N, x.cuda(), None, None, None, None, y, stats, eps=0.0)
+    ref, _ = R.layer_norm(f64(x), None, None, None, 0.0)
+    assert (y.cpu().double() - ref[1]).abs().max() < 256 * R.U * ref[1].abs().max()
+    assert (stats[:, 0].cpu().double() - ref[2][:, 0]).abs().max() <= 2.0 ** 20 * R.U
+
+
+def test_layer_norm_constant_rows_and_nan():
+    """A row without spread gives the bias; a NaN or an infinity stays in its row."""
+    N, D = 6, 320
+    for dt in (BF, F32):
+        x = rand(gen(3), N, D, dtype=dt)
+        x[1] = 1.5
+        clean = x.clone()
+        x[2, 7], x[4, 300] = float("nan"), float("inf")
+        w, b = rand(gen(4), D, dtype=dt), rand(gen(5), D, dtype=dt)
+        y, y2 = torch.empty((N, D), dtype=dt, device="cuda"), torch.empty((N, D), dtype=dt, device="cuda")
+        moe.moe_layer_norm(N, x.cuda(), None, w.cuda(), b.cuda(), None, y)
+        moe.moe_layer_norm(N, clean.cuda(), None, w.cuda(), b.cuda(), None, y2)
+        assert torch.equal(y[1].cpu(), b)
+        assert y[2].isnan().all() and y[4].isnan().all()
+        keep = [0, 1, 3, 5]
+        assert torch.equal(y[keep], y2[keep])
+
+
+# ---------------------------------------------------------------- linear maps
+LINEAR_CASES = [
+    # R, in, out: one row to every height of tile, odd rows and widths, split and whole reductions
+    (1, 64, 8), (1, 1024, 136), (1, 4096, 264), (16, 2048, 128), (17, 512, 72), (32, 1024, 1000), (33, 320, 256), (64, 1536, 40),
+    (65, 640, 136), (128, 2048, 264), (129, 1024, 520), (257, 256, 128), (300, 3008, 64), (1000, 192, 384),
+]
+
+
+def check_linear(R_, K, M, act, dtype, seed, parts):
+    dt = TYPES[dtype]
+    g = gen(seed)
+    x, w = rand(g, R_, K, dtype=dt), rand(g, M, K, std=1.5 / math.sqrt(K), dtype=dt)
+    bias = rand(g, M, dtype=dt) if "b" in parts else None
+    res = rand(g, R_, M, dtype=dt) if "r" in parts else None
+    ws = workspace(moe.moe_linear_workspace_size(R_, K, M, dtype))
+    y = torch.empty((R_, M), dtype=dt, device="cuda")
+    z = torch.empty_like(y) if "z" in parts else None
+    moe.moe_linear(dev(x), dev(w), y, ws, bias=dev(bias), residual=dev(res), act=act, z=z)
+    torch.cuda.synchronize()
+    (ry, rz), (ey, ez) = R.linear(f64(x), f64(w), f64(bias), f64(res), act, dt)
+    check("y", y, ry, ey)
+    if z is not None:
+        check("z", z, rz, ez)
+    y2 = dev(res).clone() if res is not None else torch.empty_like(y)  # in place over the residual: the same bits
+    moe.moe_linear(dev(x), dev(w), y2, ws, bias=dev(bias), residual=y2 if res is not None else None, act=act)
+    assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R_,K,M", LINEAR_CASES)
+def test_linear(R_, K, M, dtype):
+    print(f"[linear] R={R_} K={K} M={M} {dtype}", flush=True)
+    acts = list(moe.MOE_ACTIVATIONS)
+    for i, parts in enumerate(("brz", "", "bz", "r")):
+        check_linear(R_, K, M, acts[(i + R_ + M // 8) % 5], dtype, R_ + K + M, parts)
+
+
+@pytest.mark.parametrize("act", list(moe.MOE_ACTIVATIONS))
+@pytest.mark.parametrize("R_,K,M", [(2000, 256, 6152), (1793, 128, 7000)])
+def test_linear_many_tiles(R_, K, M, act):
+    """256 x 256 tiles, the last ones ragged in both directions."""
+    print(f"[linear] R={R_} K={K} M={M} {act}", flush=True)
+    check_linear(R_, K, M, act, "bf16", 5, "brz")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R_,K,M", LINEAR_CASES + [(2100, 192, 5640)])
+def test_linear_exact(R_, K, M, dtype):
+    """Whole numbers whose sums stay below 2^24 leave no error before the one rounding."""
+    dt = TYPES[dtype]
+    g = gen(R_ * 3 + M)
+    x = torch.randint(-4, 5, (R_, K), generator=g).to(dt)
+    w = torch.randint(-4, 5, (M, K), generator=g).to(dt)
+    bias = torch.randint(-100, 101, (M,), generator=g).to(dt)
+    ws = workspace(moe.moe_linear_workspace_size(R_, K, M, dtype))
+    y, z = (torch.full((R_, M), float("nan"), dtype=dt, device="cuda") for _ in range(2))
+    moe.moe_linear(dev(x), dev(w), y, ws, bias=dev(bias), act="relu", z=z)
+    torch.cuda.synchronize()
+    ref = x.float() @ w.float().t() + bias.float()  # exact in float32
+    assert torch.equal(z.cpu(), ref.to(dt)) and torch.equal(y.cpu(), torch.relu(ref).to(dt))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("act", list(moe.MOE_ACTIVATIONS))
+def test_activation_values(act, dtype):
+    """The activations and their slopes over the whole range, its ends and NaN among them: x = z e_0, W = 1 in column 0."""
+    dt, R_ = TYPES[dtype], 512
+    z = torch.cat((torch.linspace(-12, 12, 400), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 3e38, -3e38, 100.0, -100.0]),
+                   torch.logspace(-8, 2, 52), -torch.logspace(-8, 2, 52))).to(dt)
+    assert z.numel() == R_
+    x = torch.zeros((R_, 64), dtype=dt)
+    x[:, 0] = z
+    w = torch.zeros((8, 64), dtype=dt)
+    w[:, 0] = 1
+    y = torch.empty((R_, 8), dtype=dt, device="cuda")
+    ws = workspace(moe.moe_linear_workspace_size(R_, 64, 8, dtype))
+    moe.moe_linear(dev(x), dev(w), y, ws, act=act)
+    ref = R.act(f64(z), act)
+    ref = torch.where(z.double() < -30, torch.zeros_like(ref) if act not in ("none", "silu") else ref, ref)
+    check("act", y[:, 3], ref, R.act_rel(f64(z), act, dt) * ref.abs() + 1e-36)
+    dz, db = torch.empty_like(y), torch.empty(8, device="cuda")
+    zz, dy = z[:, None].repeat(1, 8), torch.full((R_, 8), -2.0, dtype=dt)
+    ws = workspace(moe.moe_linear_backward_workspace_size(R_, 8, dtype))
+    moe.moe_linear_backward(dev(dy), dev(zz), dz, db, ws, act=act)
+    s, mag = R.slope(f64(zz), act)
+    far = zz.double().abs() > 200
+    s = torch.where(far & torch.tensor(act != "none"), (zz > 0).double(), s)
+    mag = torch.where(far, torch.ones_like(s), mag)
+    rel = 2.0 ** -13 if dt == BF else (16 + 8 * f64(zz).clamp(-30, 30) ** 2) * R.U
+    # A sigmoid or exponential below float32's least normal value 2^-126 may come out as 0. What multiplies it is at most
+    # |z| 2 sqrt(2 / pi) (1 + 3 0.044715 z^2) <= 1.6 |z| (1 + 0.135 z^2) (the tanh form's inner slope), and |dy| = 2.
+    zc = f64(zz).clamp(-30, 30).abs()
+    check("slope", dz, -2.0 * s, 2.0 * mag * rel + 2.0 * 2.0 ** -126 * (1 + 1.6 * zc * (1 + 0.135 * zc ** 2)))
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf")], dtype=dt)
+    x = torch.zeros((3, 64), dtype=dt)
+    x[:, 0] = bad
+    y = torch.empty((3, 8), dtype=dt, device="cuda")
+    w0 = torch.ones((8, 64), dtype=dt)
+    moe.moe_linear(dev(x), dev(w0), y, workspace(moe.moe_linear_workspace_size(3, 64, 8, dtype)), act=act)
+    got = y[:, 0].cpu().float()
+    assert got[0].isnan() and got[1] == float("inf") and got[2] == (-float("inf") if act == "none" else 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R_,M", [(1, 8), (3, 72), (64, 512), (65, 520), (200, 1032), (1000, 64), (130, 4104)])
+def test_linear_backward(R_, M, dtype):
+    dt = TYPES[dtype]
+    print(f"[linear backward] R={R_} M={M} {dtype}", flush=True)
+    g = gen(R_ + M)
+    dy, z = rand(g, R_, M, dtype=dt), rand(g, R_, M, std=2.0, dtype=dt)
+    ws = workspace(moe.moe_linear_backward_workspace_size(R_, M, dtype))
+    for act in moe.MOE_ACTIVATIONS:
+        dz, db = torch.empty((R_, M), dtype=dt, device="cuda"), torch.empty(M, device="cuda")
+        moe.moe_linear_backward(dev(dy), dev(z), dz, db, ws, act=act)
+        torch.cuda.synchronize()
+        ref, bound = R.linear_backward(f64(dy), f64(z), act, dt)
+        check("dz", dz, ref[0], bound[0])
+        check("dbias", db, ref[1], bound[1])
+        over_dy, over_z = dev(dy).clone(), dev(z).clone()  # in place, and each output alone
+        db2 = torch.empty_like(db)
+        moe.moe_linear_backward(over_dy, dev(z), over_dy, None, None, act=act)
+        moe.moe_linear_backward(dev(dy), over_z, over_z, None, None, act=act)
+        moe.moe_linear_backward(dev(dy), dev(z) if act != "none" else None, None, db2, ws, act=act)
+        assert torch.equal(over_dy, dz) and torch.equal(over_z, dz) and torch.equal(db2, db)
+
+
+# ---------------------------------------------------------------- balance loss and the router's gradient
+def routed(g, N, E, k, empty=0.0, twice=False):
+    logits = torch.randn((N, E), generator=g) * 2.0
+    idx = logits.topk(k, 1).indices.to(torch.int32)
+    if empty:
+        idx[torch.rand((N, k), generator=g) < empty] = E
+        if N > 1:
+            idx[0, 0], idx[1, 0] = -7, 1 << 30
+    if twice and k > 1:
+        idx[:, 1] = idx[:, 0]
+    return torch.sigmoid(logits), idx
+
+
+BALANCE_CASES = [
+    # N, E, k, rows per sequence
+    (1, 1, 1, 1), (1, 8, 2, 5), (5, 6, 3, 2), (33, 16, 4, 33), (64, 30, 5, 7), (100, 60, 8, 64), (70, 64, 8, 1), (300, 128, 8, 100),
+    (257, 160, 6, 257), (700, 256, 8, 300), (130, 288, 8, 1 << 40), (90, 512, 32, 45), (3000, 16, 1, 1500),
+    (2500, 160, 8, 2400),
+]
+
+
+@pytest.mark.parametrize("N,E,k,T", BALANCE_CASES)
+def test_balance(N, E, k, T):
+    print(f"[balance] N={N} E={E} k={k} T={T}", flush=True)
+    g = gen(N + E + k)
+    t = min(T, N)
+    S = (N + T - 1) // T
+    for empty, masked, norm in ((0.0, False, True), (0.3, True, False), (0.0, True, True)):
+        scores, idx = routed(g, N, E, k, empty, twice=empty > 0)
+        mask = None
+        if masked:
+            mask = torch.rand(N, generator=g) < 0.7
+            mask[:t] = False  # a sequence with nothing in it
+            if N > 2:
+                scores[0], scores[1] = float("nan"), 0.0  # behind the mask: without effect
+        cfg = moe.make_config(64, E, 1, 1, k, 64, alpha=2.5, norm=norm)
+        counts = torch.full((S, E), -1, dtype=torch.int32, device="cuda")
+        coef = torch.full((S, E), float("nan"), device="cuda")
+        loss = torch.full((1,), float("nan"), device="cuda")
+        ws = workspace(moe.moe_balance_workspace_size(cfg, N, T))
+        m = None if mask is None else dev(mask.to(torch.uint8))
+        moe.moe_balance_loss(cfg, N, dev(scores), dev(idx), T, 0.01, counts, coef, loss, ws, token_mask=m)
+        torch.cuda.synchronize()
+        (rl, rc, rco), (bl, bc) = R.balance(f64(scores), idx, t, 0.01, mask)
+        assert torch.equal(counts.cpu().long(), rc)
+        check("loss", loss, rl.view(1), bl * rl.abs())
+        check("coef", coef, rco, bc * rco.abs())
+        loss2 = torch.empty_like(loss)
+        moe.moe_balance_loss(cfg, N, dev(scores), dev(idx), T, 0.01, None, None, loss2, ws,
+                             token_mask=None if mask is None else dev(mask))
+        assert torch.equal(loss, loss2)
+        # the gradient: both parts, each alone, in place over the scores
+        scores = torch.nan_to_num(scores, nan=0.5)
+        dw, dl = rand(g, N, k), torch.tensor([0.25])
+        out = torch.full((N, E), float("nan"), device="cuda")
+        args = dict(seq_rows=T, coef=coef, dloss=dev(dl), token_mask=m)
+        moe.moe_route_backward(cfg, N, dev(scores), dev(idx), dev(dw), out, **args)
+        alone = torch.empty_like(out), torch.empty_like(out)
+        moe.moe_route_backward(cfg, N, dev(scores), dev(idx), dev(dw), alone[0])
+        moe.moe_route_backward(cfg, N, dev(scores), None, None, alone[1], **args)
+        torch.cuda.synchronize()
+        s, w = f64(scores), f64(dw)
+        co = f64(coef.cpu())
+        for got, ref in ((out, R.route_backward(s, idx, w, 2.5, 1e-20, norm, t, co, 0.25, mask)),
+                         (alone[0], R.route_backward(s, idx, w, 2.5, 1e-20, norm)),
+                         (alone[1], R.route_backward(s, idx, None, 2.5, 1e-20, norm, t, co, 0.25, mask))):
+            check("dlogits", got, *ref)
+        over = dev(scores)
+        moe.moe_route_backward(cfg, N, over, dev(idx), dev(dw), over, **args)
+        assert torch.equal(over, out)
+
+
+def test_route_backward_dead_token_without_scores():
+    """A masked token whose scores are not numbers gives zeros when the balance loss alone is asked for."""
+    N, E, k = 9, 96, 4
+    scores, idx = routed(gen(8), N, E, k)
+    scores[4] = float("nan")
+    mask = torch.ones(N, dtype=torch.uint8)
+    mask[4] = 0
+    out = torch.empty((N, E), device="cuda")
+    moe.moe_route_backward(moe.make_config(64, E, 1, 1, k, 64), N, dev(scores), None, None, out, seq_rows=N,
+                           coef=torch.rand((1, E), generator=gen(9)).cuda(), token_mask=dev(mask))
+    assert (out[4] == 0).all() and out.isfinite().all()
+
+
+def test_balance_gradient_by_differences():
+    """d loss / d logits against differences of the float64 loss; the counts stay as they are."""
+    N, E, k, T = 12, 10, 3, 6
+    g = gen(11)
+    logits = torch.randn((N, E), generator=g, dtype=torch.float64)
+    idx = logits.topk(k, 1).indices.to(torch.int32)
+    cfg = moe.make_config(64, E, 1, 1, k, 64)
+    scores = torch.sigmoid(logits).float()
+    coef, loss = torch.empty((2, E), device="cuda"), torch.empty(1, device="cuda")
+    ws = workspace(moe.moe_balance_workspace_size(cfg, N, T))
+    moe.moe_balance_loss(cfg, N, dev(scores), dev(idx), T, 1.0, None, coef, loss, ws)
+    out = torch.empty((N, E), device="cuda")
+    moe.moe_route_backward(cfg, N, dev(scores), None, None, out, seq_rows=T, coef=coef)
+    h = 1e-5
+    for n in range(N):
+        for e in range(E):
+            d = []
+            for sign in (1, -1):
+                z = logits.clone()
+                z[n, e] += sign * h
+                d.append(R.balance(torch.sigmoid(z), idx, T, 1.0, None)[0][0])
+            # central differences: off by h^2 of the third derivative and the loss's rounding over h
+            assert abs(float(out[n, e]) - float(d[0] - d[1]) / (2 * h)) < 1e-6
+
+
+# ---------------------------------------------------------------- gradient norm and clipping
+SIZES = [
+    [1], [7], [16384], [16385], [5, 0, 16383, 1], [1, 2, 3, 4, 5, 6, 7, 8, 9] * 30, [100000, 3, 40000, 77, 0, 0, 65536],
+    [0], [], [300001],
+]
+
+
+@pytest.mark.parametrize("flat", [False, True])
+@pytest.mark.parametrize("dtype,to", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+def test_clip(dtype, to, flat):
+    g = gen(21)
+    for sizes in SIZES:
+        print(f"[clip] {len(sizes)} tensors, {sum(sizes)} values {dtype} -> {to} flat={flat}", flush=True)
+        dt, ot = TYPES[dtype], TYPES[to]
+        total = sum(sizes)
+        if flat:  # views that start anywhere, one value in front of the first
+            grads = list(rand(g, total + 1, std=0.1, dtype=dt).cuda()[1:].split(sizes)) if sizes else []
+            buf = torch.full((total + 2,), 7.0, dtype=ot, device="cuda")
+            out = list(buf[1:-1].split(sizes)) if sizes else []
+        else:
+            grads = [rand(g, n, std=0.1, dtype=dt).cuda() for n in sizes]
+            out = [torch.full((n,), 7.0, dtype=ot, device="cuda") for n in sizes]
+        before = [t.clone() for t in grads]
+        norm = torch.full((1,), float("nan"), device="cuda")
+        ws = workspace(moe.moe_grad_norm_workspace_size(grads))
+        for max_norm in (0.25, 1e9):
+            moe.moe_grad_norm(grads, norm, ws)
+            moe.moe_grad_clip(grads, norm, max_norm, out=out)
+            torch.cuda.synchronize()
+            rn, scale = R.clip([t.cpu() for t in before], max_norm, 1e-6)
+            assert abs(float(norm) - rn) <= 1.0001 * R.U * rn
+            for a, b, o in zip(grads, before, out):
+                assert torch.equal(a, b)
+                check("out", o, b.cpu().double() * scale, 4 * R.U * (b.cpu().double() * scale).abs())
+            if flat and sizes:
+                assert buf[0] == 7 and buf[-1] == 7
+        if dtype == to:  # in place: the same bits as the other way, and untouched where nothing is cut
+            moe.moe_grad_clip(grads, norm, 1e9)
+            for a, b in zip(grads, before):
+                assert torch.equal(a, b)
+            moe.moe_grad_clip(grads, norm, 0.25, out=out)
+            moe.moe_grad_clip(grads, norm, 0.25, out=grads)
+            for a, o in zip(grads, out):
+                assert torch.equal(a, o)
+            grads = [b.clone() for b in before]
+            moe.moe_grad_clip(moe.moe_tensor_list(grads), norm, 0.25)
+            for a, o in zip(grads, out):
+                assert torch.equal(a, o)
+
+
+def test_clip_mixed_types_and_extremes():
+    """Both types in one list; values whose squares no float32 holds; infinities and NaN."""
+    g = gen(22)
+    norm = torch.empty(1, device="cuda")
+    a, b = rand(g, 5000, dtype=BF).cuda(), rand(g, 333, dtype=F32).cuda()
+    ws = workspace(moe.moe_grad_norm_workspace_size([a, b]))
+    for factor in (1.0, 1e30, 1e-30):
+        x, y = (a.float() * factor).to(BF), b * factor
+        moe.moe_grad_norm([x, y], norm, ws)
+        rn, scale = R.clip([x.cpu(), y.cpu()], 3.0 * factor, 0.0)
+        assert abs(float(norm) - rn) <= 1.0001 * R.U * rn
+        moe.moe_grad_clip([x, y], norm, 3.0 * factor, eps=0.0)
+        check("bf16", x, (a.float() * factor).to(BF).cpu().double() * scale, 4 * R.U * x.cpu().double().abs())
+        check("f32", y, (b * factor).cpu().double() * scale, 4 * R.U * y.cpu().double().abs())
+    x = a.clone()
+    x[7] = float("inf")
+    moe.moe_grad_norm([x, b], norm, ws)
+    assert float(norm) == float("inf")
+    y = b.clone()
+    moe.moe_grad_clip([y], norm, 1.0)
+    assert (y == 0).all()
+    y = b.clone()
+    y[100] = float("nan")
+    moe.moe_grad_norm([x, y], norm, ws)
+    assert norm.isnan().all()
+    moe.moe_grad_clip([y], norm, 1.0)
+    assert y.isnan().all()
+
+
+def test_norm_of_many_tensors_in_any_order():
+    """More tensors than one launch's table holds, in the order of no addresses; clipped in place."""
+    g = gen(23)
+    sizes = [1 + (i * 7919) % 3001 for i in range(457)]
+    grads = [rand(g, n, dtype=BF if i % 3 else F32).cuda() for i, n in enumerate(sizes)]
+    order = torch.randperm(len(grads), generator=g).tolist()
+    grads = [grads[i] for i in order]
+    before = [t.clone() for t in grads]
+    norm = torch.empty(1, device="cuda")
+    moe.moe_grad_norm(grads, norm, workspace(moe.moe_grad_norm_workspace_size(grads)))
+    moe.moe_grad_clip(grads, norm, 10.0)
+    rn, scale = R.clip([t.cpu() for t in before], 10.0, 1e-6)
+    assert abs(float(norm) - rn) <= 1.0001 * R.U * rn
+    for t, b in zip(grads, before):
+        r = b.cpu().double() * scale
+        check("out", t, r, 4 * R.U * r.abs())
