@@ -42,27 +42,34 @@ __device__ inline float normal_tail_ratio(float a) {
   return p * t;
 }
 
+// e^(-x^2 / 2)
+template <bool FAST>
+__device__ inline float half_gauss(float x) {
+  if (!FAST) return expf(-0.5f * x * x);
+  const float s = x * 0.84932180028801904f;  // sqrt(log2(e) / 2)
+  return __builtin_amdgcn_exp2f(-s * s);
+}
+
+// Factors are kept finite where the other one has vanished long before, so that an infinite z gives the limit and not a
+// NaN; a NaN passes through the exponential.
 template <bool FAST>
 __device__ inline float act_gelu(float z) {
   // z Phi(z) = max(z, 0) - |z| Phi(-|z|): both tails keep their relative precision
   const float a = fabsf(z);
-  const float q = (FAST ? __expf(-0.5f * a * a) : expf(-0.5f * a * a)) * normal_tail_ratio<FAST>(a);
-  // |z| q vanishes long before |z| does (an infinite z would make it NaN)
-  return a > 30.0f ? fmaxf(z, 0.f) : fmaf(-a, q, fmaxf(z, 0.f));
+  const float q = half_gauss<FAST>(a) * normal_tail_ratio<FAST>(a);
+  return fmaf(-fminf(a, 30.0f), q, fmaxf(z, 0.f));
 }
 
 template <bool FAST>
 __device__ inline float act_gelu_tanh(float z) {
   // (1 + tanh(u)) / 2 = sigmoid(2 u)
   const float u = kGeluTanhA * z * fmaf(kGeluTanhB * z, z, 1.0f);
-  const float y = z * act_sigmoid<FAST>(2.0f * u);
-  return z < -30.0f ? -0.f : y;  // sigmoid is 0 there; the product with an infinity would be NaN
+  return fmaxf(z, -30.0f) * act_sigmoid<FAST>(2.0f * u);
 }
 
 template <bool FAST>
 __device__ inline float act_silu(float z) {
-  const float y = z * act_sigmoid<FAST>(z);
-  return z < -200.0f ? -0.f : y;
+  return fmaxf(z, -200.0f) * act_sigmoid<FAST>(z);
 }
 
 // N values at once: one branch on the activation (the same for every thread) for all of them.
@@ -79,7 +86,7 @@ __device__ inline void act_apply(int act, float* v) {
       break;
     case MOE_ACT_GELU:
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = v[i] != v[i] ? v[i] : act_gelu<FAST>(v[i]);
+      for (int i = 0; i < N; ++i) v[i] = act_gelu<FAST>(v[i]);
       break;
     case MOE_ACT_GELU_TANH:
 #pragma unroll
@@ -96,7 +103,7 @@ __device__ inline float slope_gelu(float z) {
   // Phi(z) + z phi(z)
   const float a = fabsf(z);
   if (a > 30.0f) return z > 0.f ? 1.f : 0.f;
-  const float e = FAST ? __expf(-0.5f * a * a) : expf(-0.5f * a * a);
+  const float e = half_gauss<FAST>(a);
   const float q = e * normal_tail_ratio<false>(a);  // the bias's gradient is a float32 sum of these
   const float d = a * e * kInvSqrt2Pi;
   return z > 0.f ? 1.0f - q + d : q - d;

@@ -3,13 +3,15 @@
 //   z = x W^T + bias      y = act(z) + residual
 //
 // Both operands are contiguous in the reduction index (W is [out, in] row-major). Forms, picked by linear_plan:
+//  - linear_few (both types, up to 16 rows): a stream of W, the reduction split over a block's waves;
 //  - linear_w8 (bfloat16, many rows): 256 x 256 tiles on the eight-wave K loop of the expert GEMMs (gemm_w8.h), a
 //    static walk over the tiles, one block per CU;
-//  - linear_tile (both types): 32 to 256 rows x 128 columns, the reduction split over blocks where the tiles alone
+//  - linear_tile (both types): 64 to 256 rows x 64 or 128 columns, the reduction split over blocks where the tiles alone
 //    would not fill the CUs; linear_join then adds the parts in order and runs the epilogue.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "activation.h"
@@ -90,49 +92,175 @@ __device__ inline void load_bias(const LinArgs<T>& a, int col, float* b) {
   if (a.bias) load_row<N>(a.bias + col, b);
 }
 
-// ---- tiles of 32 to 256 rows x 128 columns ----
+// Cache policy of weights that are read once per call: non-temporal (the NT bit, 2 on gfx950).
+constexpr int kStreamW = 2;
+
+// Waits until at most min(n, MOST) steps of PER loads each are in flight.
+template <int PER, int MOST>
+__device__ inline void wait_steps(int n) {
+  if constexpr (MOST == 0) {
+    wait_vmcnt<0>();
+  } else {
+    if (n >= MOST)
+      wait_vmcnt<PER * MOST>();
+    else
+      wait_steps<PER, MOST - 1>(n);
+  }
+}
+
+// ---- up to 16 rows ----
 //
-// A stage of the ring holds 128 bytes of every row of x and of W that the tile covers (whole lines per load), copied
-// global -> LDS by direct loads, chunk-swizzled as in gemm_w8.h. Each wave multiplies a share of TM x TN tiles of
-// 16 x 16: W rows are the first operand, so that a lane ends up with four consecutive output columns of one row. A
-// lane of both operands holds the 16 bytes of chunk lane / 16 of its row: eight k of v_mfma_f32_16x16x32_bf16, or four k
-// that four steps of v_mfma_f32_16x16x4_f32 take one by one (which k of a chunk meet in one step does not matter as
-// long as both operands agree).
-// One barrier per step: it follows the wait for the step's own loads, and the stage that is refilled behind it was
-// read in the step before.
-template <typename T, int BM_, int WM_, int WN_, int S_>
+// A stream of W: a block holds 16 columns, its waves a run of the reduction each, with a ring of their own and no barrier
+// until the end, where their sums meet in LDS. A step is 128 bytes of every row, whole lines per load, as in the tiles
+// below; of x only the first 8 NX rows are copied, and what the products make of the others is not stored.
+template <typename T, int NX, int NW, int S>
+struct LinFew {
+  static constexpr int STAGE = (2 + NX) * 1024, PER = 2 + NX;
+  static constexpr int LDS = NW * S * STAGE;
+  static_assert(LDS <= 80 * 1024 && LDS >= NW * 1024, "two blocks per CU; the sums");
+};
+
+template <typename T, int NX, int NW, int S>
+__global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
+  using L = LinFew<T, NX, NW, S>;
+  constexpr bool BF16 = std::is_same<T, uint16_t>::value;
+  __shared__ __attribute__((aligned(1024))) char lds[L::LDS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int col0 = (int)blockIdx.x * 16, rows = (int)a.R;
+  const int nk_all = a.K / (128 / (int)sizeof(T));
+  const int k0 = nk_all * wave / NW, nk = nk_all * (wave + 1) / NW - k0;
+  // rows past the end repeat the last one
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, -1, kRawBufferWord3);
+  const __amdgpu_buffer_rsrc_t rb =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + (int64_t)col0 * a.K), (short)0, -1, kRawBufferWord3);
+  auto swz = [](int r) { return (r ^ (r >> 3)) & 7; };
+  uint32_t ox[NX], ow[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 8 * i + (lane >> 3), c = (lane & 7) ^ swz(r);
+    if (i < NX) ox[i] = (uint32_t)min(r, rows - 1) * (uint32_t)(a.K * (int)sizeof(T)) + 16 * c;
+    ow[i] = (uint32_t)min(r, a.M - 1 - col0) * (uint32_t)(a.K * (int)sizeof(T)) + 16 * c;
+  }
+  char* const ring = lds + wave * (S * L::STAGE);
+  int put = 0, get = 0, at = k0 * 128;
+  auto issue = [&] {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(ring + put + i * 1024), 16, (int)ow[i], at, 0, kStreamW);
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(ring + put + (2 + i) * 1024), 16, (int)ox[i], at, 0, 0);
+    put = put == (S - 1) * L::STAGE ? 0 : put + L::STAGE;
+    at += 128;
+  };
+  const int r16 = lane & 15, kq = lane >> 4;
+  int fw[2], fx[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    fw[h] = r16 * 128 + 16 * ((4 * h + kq) ^ swz(r16));
+    fx[h] = 2048 + (NX == 1 ? (r16 & 7) * 128 + 16 * ((4 * h + kq) ^ swz(r16 & 7)) : fw[h]);
+  }
+  typedef typename std::conditional<BF16, bf16x8, f32x4>::type frag;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  auto step = [&](bool refill) {
+    frag w[2], x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[h] = *(const frag*)(ring + get + fw[h]);
+      x[h] = *(const frag*)(ring + get + fx[h]);
+    }
+    get = get == (S - 1) * L::STAGE ? 0 : get + L::STAGE;
+    wait_lgkm0();  // in registers: the stage may be refilled
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    if (refill) issue();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (BF16) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[h], x[h], acc, 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(w[h][u], x[h][u], acc, 0, 0, 0);
+      }
+    }
+  };
+  const int ahead = min(S, nk);
+  for (int t = 0; t < ahead; ++t) issue();
+  int t = 0;
+  for (; t + S < nk; ++t) {
+    wait_vmcnt<(S - 1) * L::PER>();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    step(true);
+  }
+  for (; t < nk; ++t) {
+    wait_steps<L::PER, S - 1>(nk - 1 - t);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    step(false);
+  }
+  __syncthreads();  // every ring has been read
+  f32x4* sums = (f32x4*)lds;
+  sums[wave * 64 + lane] = acc;
+  __syncthreads();
+  const int col = col0 + 4 * kq;
+  if (wave != 0 || r16 >= rows || col >= a.M) return;
+#pragma unroll
+  for (int w = 1; w < NW; ++w) acc += sums[w * 64 + lane];
+  float v[4] = {acc[0], acc[1], acc[2], acc[3]}, bias[4];
+  load_bias<4>(a, col, bias);
+  epilogue<4>(a, r16, col, v, bias);
+}
+
+// ---- tiles of 64 to 256 rows x 64 or 128 columns ----
+//
+// Eight waves, two per SIMD. A step covers 128 bytes of every row of x and of W in the tile (64 k of bfloat16, 32 of
+// float32; whole lines per load), copied global -> LDS by direct loads into a ring of S stages, chunk-swizzled as in
+// gemm_w8.h. Waves 0-3 multiply the first half of each step and waves 4-7 the second, each wave a quarter of the tile,
+// so that a wave's share is as large as the registers allow and LDS is read least; at the end the halves exchange sums.
+//  - One barrier per step: behind it the next step has landed and every wave has read the present one into registers,
+//    so its stage is refilled at once, and the next fragments are read while the present products run.
+//  - The steps that refill run in a loop of their own, free of branches and with a fixed wait: with the conditions of
+//    the last steps inside, a step of little work took 0.42 us of branches alone.
+//  - W rows are the first operand of the products, so that a lane ends up with four consecutive output columns of one
+//    row. A lane of both operands holds the 16 bytes of one chunk of its row: eight k of v_mfma_f32_16x16x32_bf16, or
+//    four k that four steps of v_mfma_f32_16x16x4_f32 take one by one (which k of a chunk meet in one step does not
+//    matter as long as both operands agree).
+template <typename T, int BM_, int BN_>
 struct LinTile {
-  static constexpr int BM = BM_, BN = 128, WM = WM_, WN = WN_, S = S_;
-  static constexpr int NW = WM * WN;
+  static constexpr int BM = BM_, BN = BN_;
+  static constexpr int WM = 2, WN = 2;
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;
   static constexpr int BK = 128 / (int)sizeof(T);  // elements of a 128-byte row
-  static constexpr int NA = BM / 8 / NW, NB = BN / 8 / NW;  // direct loads per wave and step (8 rows each)
+  static constexpr int NA = BM / 64, NB = BN / 64, PER = NA + NB;  // direct loads per wave and step (8 rows each)
   static constexpr int STAGE = (BM + BN) * 128;
-  static_assert(NA * 8 * NW == BM && NB * 8 * NW == BN, "whole loads per wave");
-  static_assert(S * STAGE <= 160 * 1024, "LDS");
+  static constexpr int S = BM == 128 || BN == 64 ? 4 : 3;  // BM = 64: two blocks per CU
+  static constexpr int XCH = 8 * (TM * TN / 2) * 1024;  // the exchange of sums
+  static constexpr int LDS = S * STAGE > XCH ? S * STAGE : XCH;
+  static_assert(LDS <= 160 * 1024 && TM % 2 == 0 && TN % 2 == 0, "LDS; a wave's tiles start at an even one");
   __device__ static int swz(int r) {
     r &= 31;
     return (r ^ (r >> 3)) & 7;
   }
 };
 
-template <typename T, int BM, int WM, int WN, int S>
-__global__ __launch_bounds__(64 * WM * WN) void linear_tile(LinArgs<T> a) {
-  using L = LinTile<T, BM, WM, WN, S>;
-  constexpr int TM = L::TM, TN = L::TN, NW = L::NW, NA = L::NA, NB = L::NB, PER = NA + NB;
-  __shared__ __attribute__((aligned(1024))) char lds[S * L::STAGE];
+template <typename T, int BM, int BN>
+__global__ __launch_bounds__(512) void linear_tile(LinArgs<T> a) {
+  using L = LinTile<T, BM, BN>;
+  constexpr int TM = L::TM, TN = L::TN, NA = L::NA, NB = L::NB, S = L::S;
+  __shared__ __attribute__((aligned(1024))) char lds[L::LDS];
   // splits outermost (an XCD's run of blocks then shares one part of x in its L2), row tiles innermost (blocks on the
   // same rows of W run together)
   const int64_t id = xcd_logical_block(gridDim.x);
   const int64_t rt = id % a.row_tiles, rest = id / a.row_tiles;
   const int ct = (int)(rest % a.col_tiles), split = (int)(rest / a.col_tiles);
   const int64_t row0 = rt * BM;
-  const int col0 = ct * L::BN;
+  const int col0 = ct * BN;
   const int rows = (int)min((int64_t)BM, a.R - row0);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int half = wave >> 2, wm = (wave >> 1) & 1, wn = wave & 1;
+  const int nk_all = a.K / L::BK;
+  const int k0 = (int)((int64_t)nk_all * split / a.splits), nk = (int)((int64_t)nk_all * (split + 1) / a.splits) - k0;
 
-  // rows past the end repeat the last one (never stored); offsets are from the tile's first row and stay below 2^32
+  // A load covers eight rows; this wave's i-th those from (wave + 8 i) 8 on. Rows past the end repeat the last one (never
+  // stored); offsets are from the tile's first row and stay below 2^32.
   const __amdgpu_buffer_rsrc_t ra =
       __builtin_amdgcn_make_buffer_rsrc((void*)(a.x + row0 * a.K), (short)0, -1, kRawBufferWord3);
   const __amdgpu_buffer_rsrc_t rb =
@@ -140,94 +268,161 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile(LinArgs<T> a) {
   uint32_t oa[NA], ob[NB];
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
-    const int r = (wave + NW * i) * 8 + (lane >> 3), c = (lane & 7) ^ L::swz(r);
+    const int r = (wave + 8 * i) * 8 + (lane >> 3), c = (lane & 7) ^ L::swz(r);
     oa[i] = (uint32_t)min(r, rows - 1) * (uint32_t)(a.K * (int)sizeof(T)) + 16 * c;
   }
 #pragma unroll
   for (int i = 0; i < NB; ++i) {
-    const int r = (wave + NW * i) * 8 + (lane >> 3), c = (lane & 7) ^ L::swz(r);
+    const int r = (wave + 8 * i) * 8 + (lane >> 3), c = (lane & 7) ^ L::swz(r);
     ob[i] = (uint32_t)min(r, a.M - 1 - col0) * (uint32_t)(a.K * (int)sizeof(T)) + 16 * c;
   }
-  const int nk_all = a.K / L::BK;
-  const int k0 = (int)((int64_t)nk_all * split / a.splits), nk = (int)((int64_t)nk_all * (split + 1) / a.splits) - k0;
-
-  auto issue = [&](int t) {
-    char* st = lds + (t % S) * L::STAGE;
-    const int off = (k0 + t) * 128;
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(st + (wave + NW * i) * 1024), 16, (int)oa[i], off, 0, 0);
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(st + BM * 128 + (wave + NW * i) * 1024), 16, (int)ob[i],
-                                               off, 0, 0);
+  int put = 0, at = k0 * 128;  // byte offsets: the stage to fill next, the step's place in a row
+  auto load = [&](int i) {  // the i-th of a step's PER loads
+    char* st = lds + put + wave * 1024 + i * 8192;  // W's rows lie behind x's
+    if (i < NA)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)st, 16, (int)oa[i < NA ? i : 0], at, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)st, 16, (int)ob[i < NA ? 0 : i - NA], at, 0, 0);
   };
+  auto loaded = [&] {
+    put = put + L::STAGE == S * L::STAGE ? 0 : put + L::STAGE;
+    at += 128;
+  };
+  auto issue = [&] {
+#pragma unroll
+    for (int i = 0; i < L::PER; ++i) load(i);
+    loaded();
+  };
+
   f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int r16 = lane & 15, kq = lane >> 4;
-  const bool live = wm * TM * 16 < rows;  // this wave has rows at all
-  int arow[TM], brow[TN], asw[TM], bsw[TN];
+  // fragment addresses: 16-row tiles lie 2 KiB apart, and the swizzle alternates with a tile's parity
+  const int chunk = 4 * half + kq;
+  int fa[2], fb[2];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = (wm * TM + i) * 16 + r16;
-    arow[i] = r * 128;
-    asw[i] = L::swz(r);
+  for (int p = 0; p < 2; ++p) {
+    const int c = 16 * (chunk ^ L::swz(p * 16 + r16));
+    fa[p] = wm * TM * 2048 + r16 * 128 + c;
+    fb[p] = BM * 128 + wn * TN * 2048 + r16 * 128 + c;
   }
+  typedef typename std::conditional<std::is_same<T, uint16_t>::value, bf16x8, f32x4>::type frag;
+  frag av[2][TM], bv[2][TN];
+  constexpr int FRAGS = TM + TN;
+  constexpr int PRODUCTS = TM * TN * (std::is_same<T, uint16_t>::value ? 1 : 4);
+  int get = 0;  // byte offset of the stage to read next
+  auto read_one = [&](auto buf, int f) {  // the f-th of a step's FRAGS fragments
+    constexpr int b = decltype(buf)::value;
+    if (f < TN)
+      bv[b][f] = *(const frag*)(lds + get + fb[f & 1] + f * 2048);
+    else
+      av[b][f - TN] = *(const frag*)(lds + get + fa[(f - TN) & 1] + (f - TN) * 2048);
+  };
+  auto got = [&] { get = get + L::STAGE == S * L::STAGE ? 0 : get + L::STAGE; };
+  auto read = [&](auto buf) {
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int r = (wn * TN + j) * 16 + r16;
-    brow[j] = BM * 128 + r * 128;
-    bsw[j] = L::swz(r);
-  }
-  auto step = [&](int t) {
-    const char* st = lds + (t % S) * L::STAGE;
+    for (int f = 0; f < FRAGS; ++f) read_one(buf, f);
+    got();
+  };
+  auto product = [&](auto buf, int m) {  // the m-th of a step's PRODUCTS
+    constexpr int b = decltype(buf)::value;
+    const int i = m % (TM * TN) / TN, j = m % TN;
+    if constexpr (std::is_same<T, uint16_t>::value)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[b][j], av[b][i], acc[i][j], 0, 0, 0);
+    else
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[b][j][m / (TM * TN)], av[b][i][m / (TM * TN)], acc[i][j], 0, 0, 0);
+  };
+  auto products = [&](auto buf) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = 4 * h + kq;
-      if constexpr (std::is_same<T, uint16_t>::value) {
-        bf16x8 av[TM], bv[TN];
+    for (int m = 0; m < PRODUCTS; ++m) product(buf, m);
+  };
+  auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+  // LIVE: the wave has rows at all (one without keeps loading and meeting the others)
+  auto loop = [&](auto live) {
+    constexpr bool LIVE = decltype(live)::value;
+    const int ahead = min(S, nk);
+    for (int t = 0; t < ahead; ++t) issue();
+    wait_steps<L::PER, S - 1>(ahead - 1);
+    bare_barrier();
+    if (LIVE) read(IntC<0>{});
+    int t = 0;
+    auto steady = [&](auto buf) {  // step t is being read into buf; steps up to t + S - 1 are issued
+      wait_lgkm0();
+      wait_vmcnt<L::PER*(S - 2)>();
+      bare_barrier();
+      fence();
+      if (LIVE) {
+        // one fragment read or load at a time, the products spread evenly behind them: the wave would otherwise stand
+        // at its reads until LDS had taken all of them, its matrix core idle
+        constexpr int OPS = FRAGS + L::PER;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) av[i] = *(const bf16x8*)(st + arow[i] + 16 * (c ^ asw[i]));
+        for (int o = 0; o < OPS; ++o) {
+          const int loads = (o + 1) * L::PER / OPS;
+          if (loads != o * L::PER / OPS)
+            load(loads - 1);
+          else
+            read_one(IntC<1 - decltype(buf)::value>{}, o - loads);
+          fence();
 #pragma unroll
-        for (int j = 0; j < TN; ++j) bv[j] = *(const bf16x8*)(st + brow[j] + 16 * (c ^ bsw[j]));
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv[j], av[i], acc[i][j], 0, 0, 0);
+          for (int m = o * PRODUCTS / OPS; m < (o + 1) * PRODUCTS / OPS; ++m) product(buf, m);
+          fence();
+        }
+        loaded();
+        got();
       } else {
-        f32x4 av[TM], bv[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) av[i] = *(const f32x4*)(st + arow[i] + 16 * (c ^ asw[i]));
-#pragma unroll
-        for (int j = 0; j < TN; ++j) bv[j] = *(const f32x4*)(st + brow[j] + 16 * (c ^ bsw[j]));
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[j][u], av[i][u], acc[i][j], 0, 0, 0);
+        issue();
+        got();
       }
+      fence();
+    };
+    for (; t + S + 1 < nk; t += 2) {
+      steady(IntC<0>{});
+      steady(IntC<1>{});
+    }
+    auto tail = [&](int t, auto buf) {
+      if (t + 1 < nk) {
+        wait_lgkm0();
+        wait_steps<L::PER, S - 2>(min(nk - 1, t + S - 1) - (t + 1));
+        bare_barrier();
+        if (t + S < nk) issue();
+        fence();
+        if (LIVE) read(IntC<1 - decltype(buf)::value>{});
+      }
+      fence();
+      if (LIVE) products(buf);
+      fence();
+    };
+    for (; t < nk; t += 2) {
+      tail(t, IntC<0>{});
+      if (t + 1 < nk) tail(t + 1, IntC<1>{});
     }
   };
+  if (wm * TM * 16 < rows)
+    loop(BoolC<true>{});
+  else
+    loop(BoolC<false>{});
+
+  // The halves' sums: waves 0-3 end with the first TM / 2 tile rows, waves 4-7 with the others.
+  constexpr int HT = TM / 2;
+  f32x4* mine = (f32x4*)lds + (wave * HT * TN) * 64 + lane;
+  f32x4* theirs = (f32x4*)lds + ((wave ^ 4) * HT * TN) * 64 + lane;
+  __syncthreads();  // the last fragments have been read
 #pragma unroll
-  for (int t = 0; t < S - 1; ++t)
-    if (t < nk) issue(t);
-  for (int t = 0; t < nk; ++t) {
-    // step t has landed: at most the S - 2 steps behind it are still in flight
-    if (t + S - 1 <= nk)
-      wait_vmcnt<(S - 2) * PER>();
-    else
-      wait_vmcnt<0>();
-    wait_lgkm0();
-    bare_barrier();
-    if (t + S - 1 < nk) issue(t + S - 1);
-    if (live) step(t);
-  }
+  for (int i = 0; i < HT; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) mine[(i * TN + j) * 64] = half == 0 ? acc[i + HT][j] : acc[i][j];
+  __syncthreads();
+  f32x4 sum[HT][TN];
+#pragma unroll
+  for (int i = 0; i < HT; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const f32x4 other = theirs[(i * TN + j) * 64];
+      sum[i][j] = half == 0 ? acc[i][j] + other : other + acc[i + HT][j];
+    }
 
   const bool whole = a.splits == 1;
   float* part = a.part + (int64_t)split * a.R * a.M;
@@ -238,10 +433,10 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_tile(LinArgs<T> a) {
     float bias[4];
     if (whole) load_bias<4>(a, col, bias);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int r = (wm * TM + i) * 16 + r16;
+    for (int i = 0; i < HT; ++i) {
+      const int r = (wm * TM + half * HT + i) * 16 + r16;
       if (r >= rows) continue;
-      float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      float v[4] = {sum[i][j][0], sum[i][j][1], sum[i][j][2], sum[i][j][3]};
       if (whole)
         epilogue<4>(a, row0 + r, col, v, bias);
       else
@@ -288,6 +483,158 @@ __global__ __launch_bounds__(256) void linear_join(LinArgs<T> a) {
 // activation and residual are applied there, with whole 16-byte loads and stores, and y is rounded once.
 constexpr int kStagePitch = 128 + 8;  // floats: rows four apart, which one store writes together, lie 32 banks apart
 
+// The K loop of one wave on the ring of Wave8Tile (two stages of x rows, three of W rows): the wave's 64 rows x 128
+// columns as MI x 4 tiles. Between two barriers a wave multiplies the last 16-wide slice of step kt and the first three
+// of step kt + 1, each while it reads the next slice's fragments, and issues its loads of x for step kt + 2 and of W for
+// step kt + 3, whose stages every wave has left when the barrier opens. One read or load at a time, the products spread
+// behind them: issued together, the reads of a slice hold the wave until LDS has taken all of them, and the matrix core
+// waits. na: the wave's loads of x that reach a valid row (the others are not issued; W's always are, so the newest
+// four loads are W's).
+template <int MI>
+__device__ __attribute__((always_inline)) inline void w8_spread_loop(char* lds, __amdgpu_buffer_rsrc_t ra,
+                                                                     const uint32_t (&oa)[4], int na,
+                                                                     __amdgpu_buffer_rsrc_t rb, const uint32_t (&ob)[4],
+                                                                     f32x16 (&acc)[2][4], int nk, int grp, int q, int lane,
+                                                                     int m0, int wn) {
+  using T = Wave8Tile<false>;
+  constexpr int TN = 4, ROWB = T::ROWB, OPB = T::OPB;
+  const int sw = T::swz(lane & 31);
+  const int a_off = (m0 + (lane & 31)) * ROWB;
+  const int b_off = T::B_BASE + (wn * 128 + (lane & 31)) * ROWB;  // column tiles lie 32 rows apart
+  int coff[4];
+#pragma unroll
+  for (int sl = 0; sl < 4; ++sl) coff[sl] = ((2 * sl + (lane >> 5)) ^ sw) * 16;
+  const int fill = grp * (OPB / 2) + q * 1024;  // this wave's first chunk run in a stage
+  int a_put = 0, b_put = 0, a_at = 0, b_at = 0;  // stages to fill next (bytes), places in a row of their steps
+  auto load_a = [&](int i) {
+    if (i < na)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(lds + a_put + fill + i * 4096), 16, (int)oa[i], a_at, 0, 0);
+  };
+  auto load_b = [&](int i) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(lds + T::B_BASE + b_put + fill + i * 4096), 16, (int)ob[i], b_at,
+                                             0, 0);
+  };
+  auto loaded_a = [&] {
+    a_put ^= OPB;
+    a_at += 128;
+  };
+  auto loaded_b = [&] {
+    b_put = b_put == 2 * OPB ? 0 : b_put + OPB;
+    b_at += 128;
+  };
+  bf16x8 af[2][MI > 0 ? MI : 1], bfr[2][TN];
+  int a_get = 0, b_get = 0;
+  auto read_one = [&](int sl, int f) {  // the f-th fragment of slice sl, into buffer sl % 2
+    if (MI == 0) return;
+    if (f < TN)
+      bfr[sl & 1][f] = *(const bf16x8*)(lds + b_get + b_off + f * 32 * ROWB + coff[sl]);
+    else
+      af[sl & 1][f - TN] = *(const bf16x8*)(lds + a_get + a_off + (f - TN) * 32 * ROWB + coff[sl]);
+  };
+  auto next_stage = [&] {
+    a_get ^= OPB;
+    b_get = b_get == 2 * OPB ? 0 : b_get + OPB;
+  };
+  auto fence = [] { __builtin_amdgcn_sched_barrier(0); };
+  // the products of slice `cur`, the reads of slice `next` and `loads` loads among them
+  auto phase = [&](auto cur_, auto next_, auto loads_, auto&& load) {
+    constexpr int cur = decltype(cur_)::value, next = decltype(next_)::value, loads = decltype(loads_)::value;
+    constexpr int FR = MI > 0 ? MI + TN : 0, OPS = FR + loads > 0 ? FR + loads : 1, P = MI * TN;
+    wait_lgkm0();  // slice `cur` is in registers
+    fence();
+#pragma unroll
+    for (int o = 0; o < OPS; ++o) {
+      if (o < FR)
+        read_one(next, o);
+      else if (o - FR < loads)
+        load(o - FR);
+      fence();
+#pragma unroll
+      for (int m = o * P / OPS; m < (o + 1) * P / OPS; ++m)
+        acc[m / TN][m % TN] =
+            __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[cur & 1][m / TN], bfr[cur & 1][m % TN], acc[m / TN][m % TN], 0, 0, 0);
+      fence();
+    }
+  };
+  auto compute = [&](auto cur_) {
+    constexpr int cur = decltype(cur_)::value;
+#pragma unroll
+    for (int m = 0; m < MI * TN; ++m)
+      acc[m / TN][m % TN] =
+          __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[cur & 1][m / TN], bfr[cur & 1][m % TN], acc[m / TN][m % TN], 0, 0, 0);
+  };
+  auto all_a = [&] {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_a(i);
+    loaded_a();
+  };
+  auto all_b = [&] {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_b(i);
+    loaded_b();
+  };
+  auto none = [](int) {};
+  const IntC<0> c0;
+  const IntC<1> c1;
+  const IntC<2> c2;
+  const IntC<3> c3;
+  const IntC<4> c4;
+
+  // steps 0 and 1 of both operands, step 2 of W; wait for step 0
+  all_a();
+  all_b();
+  if (nk > 1) {
+    all_a();
+    all_b();
+  }
+  if (nk > 2) all_b();
+  // x of step 1 may not have been issued by this wave at all: only W's loads can be counted on
+  if (nk > 2)
+    wait_vmcnt<8>();
+  else if (nk > 1)
+    wait_vmcnt<4>();
+  else
+    wait_vmcnt<0>();
+  bare_barrier();
+#pragma unroll
+  for (int f = 0; f < (MI > 0 ? MI + TN : 0); ++f) read_one(0, f);
+  phase(c0, c1, c0, none);
+  phase(c1, c2, c0, none);
+  phase(c2, c3, c0, none);
+  // steps kt and kt + 1: x of kt + 2 and W of kt + 3 are issued
+  int kt = 0;
+  for (; kt + 3 < nk; ++kt) {
+    wait_lgkm0();
+    wait_vmcnt<4>();  // all but W of step kt + 2 has landed
+    bare_barrier();
+    next_stage();
+    phase(c3, c0, c4, load_a);
+    loaded_a();
+    phase(c0, c1, c2, load_b);
+    phase(c1, c2, c2, [&](int i) { load_b(i + 2); });
+    loaded_b();
+    phase(c2, c3, c0, none);
+  }
+  for (; kt + 1 < nk; ++kt) {
+    wait_lgkm0();
+    if (kt + 2 < nk)
+      wait_vmcnt<4>();
+    else
+      wait_vmcnt<0>();
+    bare_barrier();
+    next_stage();
+    if (kt + 2 < nk) all_a();
+    phase(c3, c0, c0, none);
+    phase(c0, c1, c0, none);
+    phase(c1, c2, c0, none);
+    phase(c2, c3, c0, none);
+  }
+  wait_lgkm0();
+  fence();
+  compute(c3);
+  bare_barrier();  // every wave has read its last fragments
+}
+
 __global__ __launch_bounds__(512, 1) void linear_w8(LinArgs<uint16_t> a) {
   using T = Wave8Tile<false>;
   __shared__ __attribute__((aligned(1024))) char lds[T::RING];
@@ -326,13 +673,13 @@ __global__ __launch_bounds__(512, 1) void linear_w8(LinArgs<uint16_t> a) {
     const int mi = max(0, min(2, (rows - m0 + 31) / 32));
     __syncthreads();  // the previous tile's staged outputs have been read
     if (mi == 2)
-      wave8_loop<false, 2>(lds, ra, oa, na, rb, ob, acc, nk, grp, q, lane, m0, wn);
+      w8_spread_loop<2>(lds, ra, oa, na, rb, ob, acc, nk, grp, q, lane, m0, wn);
     else if (mi == 1)
-      wave8_loop<false, 1>(lds, ra, oa, na, rb, ob, acc, nk, grp, q, lane, m0, wn);
+      w8_spread_loop<1>(lds, ra, oa, na, rb, ob, acc, nk, grp, q, lane, m0, wn);
     else
-      wave8_loop<false, 0>(lds, ra, oa, na, rb, ob, acc, nk, grp, q, lane, m0, wn);
+      w8_spread_loop<0>(lds, ra, oa, na, rb, ob, acc, nk, grp, q, lane, m0, wn);
 
-    // each wave in its own part of the ring (every wave has passed the loop's last barrier, behind the last read)
+    // each wave in its own part of the ring (the loop ends on a barrier behind the last read)
     float* stage = (float*)lds + wave * (32 * kStagePitch);
     const int ch = lane & 15, col = col0 + wn * 128 + ch * 8;
     const bool in = col < a.M;
@@ -360,10 +707,20 @@ __global__ __launch_bounds__(512, 1) void linear_w8(LinArgs<uint16_t> a) {
 }
 
 // Blocks of linear_tile: rows per tile and the parts of the reduction.
-template <typename T, int BM, int WM, int WN, int S>
+template <typename T, int BM, int BN>
 hipError_t run_tile(const LinArgs<T>& a, hipStream_t s) {
   const int64_t blocks = a.row_tiles * a.col_tiles * a.splits;
-  hipLaunchKernelGGL((linear_tile<T, BM, WM, WN, S>), dim3((unsigned)blocks), dim3(64 * WM * WN), 0, s, a);
+  hipLaunchKernelGGL((linear_tile<T, BM, BN>), dim3((unsigned)blocks), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run_few(const LinArgs<T>& a, hipStream_t s) {
+  const dim3 grid((a.M + 15) / 16);
+  if (a.R <= 8)
+    hipLaunchKernelGGL((linear_few<T, 1, 8, 3>), grid, dim3(512), 0, s, a);
+  else
+    hipLaunchKernelGGL((linear_few<T, 2, 4, 4>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -385,17 +742,17 @@ hipError_t linear_t(const LinearCall& c, const LinearPlan& p, hipStream_t s) {
   a.row_tiles = (c.R + p.bm - 1) / p.bm;
   a.col_tiles = (c.out + p.bn - 1) / p.bn;
   hipError_t e = hipErrorInvalidValue;
+  if (p.bm == 16) return run_few<T>(a, s);
   if constexpr (std::is_same<T, uint16_t>::value) {
     if (p.bn == 256) {
       const int64_t grid = std::min((a.row_tiles * a.col_tiles + 7) / 8 * 8, persistent_grid());
       hipLaunchKernelGGL(linear_w8, dim3((unsigned)grid), dim3(512), 0, s, a);
       return hipGetLastError();
     }
-    if (p.bm == 256) e = run_tile<T, 256, 4, 2, 3>(a, s);
+    if (p.bm == 256) e = run_tile<T, 256, 128>(a, s);
   }
-  if (p.bm == 32) e = run_tile<T, 32, 1, 4, 4>(a, s);
-  if (p.bm == 64) e = run_tile<T, 64, 2, 2, 3>(a, s);
-  if (p.bm == 128) e = run_tile<T, 128, 2, 4, 4>(a, s);
+  if (p.bm == 64) e = p.bn == 64 ? run_tile<T, 64, 64>(a, s) : run_tile<T, 64, 128>(a, s);
+  if (p.bm == 128) e = run_tile<T, 128, 128>(a, s);
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL(linear_join<T>, dim3((unsigned)linear_join_blocks(c.R, c.out)), dim3(256), 0, s, a);
   return hipGetLastError();
@@ -465,37 +822,68 @@ int64_t linear_join_blocks(int64_t R, int out) { return (R * (out / 8) + 255) / 
 int64_t linear_back_runs(int64_t R) { return (R + kBackRows - 1) / kBackRows; }
 
 namespace {
-constexpr int kMaxSplits = 16;
-int tile_rows(int dtype, int64_t R) {
-  if (R <= 32) return 32;
-  if (R <= 64) return 64;
-  return R <= 128 || dtype == MOE_F32 ? 128 : 256;
+
+constexpr int kFewRows = 16;
+constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32}, kMostSplits = 32;
+constexpr int64_t kMostPart = (int64_t)1 << 23;  // floats of a split call's parts: 32 MiB of workspace
+
+// What a call takes with tiles of bm x bn, in microseconds, as fitted to 80 bfloat16 shapes (17 to 6,000 rows, 256 to 12,288
+// input and 64 to 16,384 output features) and 44 float32 ones, each timed with every tile and number of parts: rounds of
+// blocks over the CUs, each of a fixed time and a time per step; or the operands from HBM, where that takes longer; and
+// the parts written, read and joined. Its choice is 0.8% (float32 0.2%) slower than the best of them on average, 11% at
+// most. Against always 128 columns and as many parts as fill the CUs once: 2,166 x 640 -> 368 in float32 21 -> 16 us,
+// 1,500 x 2,048 -> 1,400 24 -> 18, 256 x 4,096 -> 4,096 28 -> 23.
+struct TileCost {
+  int bm, bn;
+  double start, step[2];  // bfloat16, float32: 64 k and 32 k
+};
+constexpr TileCost kTiles[] = {{64, 64, 2.0, {0.27, 0.54}},
+                               {64, 128, 2.0, {0.43, 0.96}},
+                               {128, 128, 3.0, {0.49, 1.86}},
+                               {256, 128, 3.7, {0.68, 0}},
+                               {256, 256, 3.6, {1.18, 0}}};  // bfloat16 only: step 0
+constexpr double kTwoBlocks = 1.75;  // a step of two 64-row blocks on one CU over that of one
+
+double tile_cost(const TileCost& c, bool f32, int64_t tiles, int64_t R, int in, int out, int splits) {
+  const int64_t blocks = tiles * splits;
+  const int all = in / (f32 ? 32 : 64), steps = (all + splits - 1) / splits, per_cu = c.bm == 64 ? 2 : 1;
+  const double rounds = (double)(per_cu == 2 ? (blocks + 511) / 512 : (blocks + 255) / 256);
+  const double step = c.step[f32] * (per_cu == 2 && blocks > 256 ? kTwoBlocks : 1.0);
+  const double bytes = (f32 ? 4.0 : 2.0) * in * ((double)out + R);
+  double t = std::max(rounds * (c.start + steps * step), c.start + bytes / 8.5e6);
+  if (splits > 1) t += 2.0 + 0.1 * splits + 8.0 * splits * R * out / 4.0e6;
+  return t;
 }
+
 }  // namespace
 
 LinearPlan linear_plan(int dtype, int64_t R, int in, int out) {
-  LinearPlan p{tile_rows(dtype, R), 128, 1};
-  if (dtype == MOE_BF16 && (R + 255) / 256 * ((out + 255) / 256) >= 192) {
-    p.bn = 256;
-    p.bm = 256;
-    return p;
+  if (R <= kFewRows) return LinearPlan{kFewRows, 16, 1};
+  const bool f32 = dtype == MOE_F32;
+  LinearPlan best{0, 0, 1};
+  double least = 0;
+  for (const TileCost& c : kTiles) {
+    if (c.step[f32] == 0) continue;
+    const int64_t tiles = (R + c.bm - 1) / c.bm * ((out + c.bn - 1) / c.bn);
+    for (int splits : kSplits) {
+      if (splits > 1 && (c.bn == 256 || tiles * splits > 1024 || in / (f32 ? 32 : 64) < splits || splits * R * out > kMostPart))
+        break;
+      const double t = tile_cost(c, f32, tiles, R, in, out, splits);
+      if (best.bm == 0 || t < least) {
+        least = t;
+        best = LinearPlan{c.bm, c.bn, splits};
+      }
+    }
   }
-  const int64_t tiles = (R + p.bm - 1) / p.bm * ((out + 127) / 128);
-  const int64_t slots = p.bm <= 64 ? 512 : 256;
-  const int steps = in / (dtype == MOE_F32 ? 32 : 64);
-  int64_t splits = std::min<int64_t>(slots / tiles, steps / 4);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(splits, kMaxSplits));
-  return p;
+  return best;
 }
 
-// A split call has at most 512 / tiles parts (256 / tiles for tiles of 128 rows and more) of R x out floats, and R x out
-// is at most tiles x the tile's size (linear_plan); kMaxSplits parts at most. Both bounds never fall as R grows.
+// At most kMostSplits parts and kMostPart floats; never falls as R grows.
 size_t linear_part_bytes(int dtype, int64_t R, int out) {
-  const int64_t bm = tile_rows(dtype, R), slots = bm <= 64 ? 512 : 256;
-  const int64_t by_tiles = slots * bm * 128;
-  const int64_t rows = std::min<int64_t>(R, (int64_t)1 << 22);
-  const int64_t by_rows = rows * out * kMaxSplits;
-  return sizeof(float) * (size_t)std::min(by_tiles, by_rows);
+  (void)dtype;
+  if (R <= kFewRows) return 0;
+  const int64_t rows = std::min<int64_t>(R, kMostPart);
+  return sizeof(float) * (size_t)std::min<int64_t>(rows * out * kMostSplits, kMostPart);
 }
 
 hipError_t launch_linear(int dtype, const LinearCall& c, hipStream_t s) {

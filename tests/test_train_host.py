@@ -62,7 +62,7 @@ def lin_bwd(R=4, M=128, dt=moe.MOE_BF16, act=1, dy=p(0), z=p(1), dz=p(2), db=p(3
     (lin, dict(act=5), INV), (lin, dict(act=-1), INV), (lin, dict(x=None), INV), (lin, dict(w=None), INV),
     (lin, dict(y=None), INV), (lin, dict(y=p(0)), INV), (lin, dict(y=p(1)), INV), (lin, dict(y=p(2)), INV),
     (lin, dict(y=p(4)), INV), (lin, dict(z=p(3)), INV), (lin, dict(z=p(0)), INV), (lin, dict(b=ODD), INV),
-    (lin, dict(ws=None), WS), (lin, dict(n=1024), WS), (lin, dict(ws=ctypes.c_void_p(24)), WS),
+    (lin, dict(R=40, ws=None), WS), (lin, dict(R=40, n=1024), WS), (lin, dict(R=40, ws=ctypes.c_void_p(24)), WS),
     (lin, dict(R=0, x=None, ws=None), OK), (lin, dict(dt=moe.MOE_F32, R=(1 << 31) - 1, M=504), UNS),
     (lin_bwd, dict(R=-1), INV), (lin_bwd, dict(M=4), UNS), (lin_bwd, dict(act=9), INV), (lin_bwd, dict(dy=None), INV),
     (lin_bwd, dict(z=None), INV), (lin_bwd, dict(dz=None, db=None), INV), (lin_bwd, dict(db=ODD), INV),
