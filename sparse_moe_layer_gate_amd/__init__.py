@@ -179,30 +179,46 @@ def moe_status_str(status: int) -> str:
     return lib().moe_status_str(int(status)).decode()
 
 
+_torch = None  # the torch module, from the first call that needs it (an import statement costs 0.2 us a time)
+
+
+def _import_torch():
+    global _torch
+    import torch
+
+    _torch = torch
+    return torch
+
+
 def _ptr(t, name, dtype=None, shape=None, required=True):
     if t is None:
         if required:
             raise ValueError(f"{name} is required")
         return None
-    import torch
-
+    torch = _torch or _import_torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a device tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _stream(stream):
-    import torch
+def _device() -> int:
+    """The current device's index, without the checks of torch.cuda.current_device()."""
+    torch = _torch or _import_torch()
+    get = getattr(torch._C, "_cuda_getDevice", None)
+    return get() if get and torch.cuda.is_initialized() else torch.cuda.current_device()
 
+
+def _stream(stream):
     if stream is None:
+        torch = _torch or _import_torch()
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # no Stream object: a third of the time
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        return raw(_device()) if raw else torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -397,13 +413,14 @@ def moe_dense_forward(N: int, x, gate, up, down, y, workspace, limit: float = 0.
 
 # ---- the operators around the experts ----
 def _tensor_dtype(t, name) -> int:
-    import torch
-
+    torch = _torch or _import_torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a device tensor")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    return MOE_F32 if t.dtype == torch.float32 else MOE_BF16
+    if t.dtype is torch.bfloat16:
+        return MOE_BF16
+    if t.dtype is torch.float32:
+        return MOE_F32
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
 
 
 _NO_CHANGE = contextlib.nullcontext()
@@ -411,8 +428,6 @@ _NO_CHANGE = contextlib.nullcontext()
 
 def _same_device(what, *tensors):
     """The tensors' one device, made the current one for the launch (and its current stream the default)."""
-    import torch
-
     index = None
     for t in tensors:
         if t is None:
@@ -423,13 +438,15 @@ def _same_device(what, *tensors):
         if index is not None and i != index:
             raise ValueError(f"{what}: tensors on more than one device: {index} and {i}")
         index = i
-    return _NO_CHANGE if index == torch.cuda.current_device() else torch.cuda.device(index)
+    if index is None or index == _device():
+        return _NO_CHANGE
+    return _torch.cuda.device(index)
 
 
 def _ws(workspace):
-    import torch
-
-    return (_ptr(workspace, "workspace", torch.uint8, required=False), 0 if workspace is None else workspace.numel())
+    if workspace is None:
+        return None, 0
+    return _ptr(workspace, "workspace", (_torch or _import_torch()).uint8), workspace.numel()
 
 
 def moe_block_norm_workspace_size(N: int, D: int, dtype="bf16", gate_rows: int = 0) -> int:
@@ -462,8 +479,7 @@ def moe_block_norm_backward(N: int, h_out, o, w_post, gate, gate_rows, w_pre, dh
     """Gradients of moe_block_norm from its tensors (h_out: the forward's h when o is None) and the gradients
     dh_out (or None) and du. Writes dh, d_o and, where given, the float32 sums dw_post, dgate, dw_pre;
     workspace: moe_block_norm_workspace_size(N, D, dtype, gate_rows) bytes, or None without sums."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(dh, "dh")
     t, f, D, T = dh.dtype, torch.float32, dh.shape[-1], int(gate_rows or 0)
     groups = (N + T - 1) // T if T > 0 else 0
@@ -486,8 +502,7 @@ def moe_block_norm_backward(N: int, h_out, o, w_post, gate, gate_rows, w_pre, dh
 def moe_combine(N: int, k: int, rows, inv_row, topk_w, shared, y, alpha: float = 1.0, stream=None):
     """y[n] = alpha sum_s topk_w[n, s] rows[inv_row[n, s]] + shared[n]; topk_w None: ones, shared None: nothing
     added. inv_row (N * k int32) as moe_dispatch writes it; entries outside rows are empty slots."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(rows, "rows")
     t, (R, D) = rows.dtype, rows.shape
     with _same_device("moe_combine", rows, inv_row, topk_w, shared, y):
@@ -503,8 +518,7 @@ def moe_combine(N: int, k: int, rows, inv_row, topk_w, shared, y, alpha: float =
 def moe_combine_backward(N: int, k: int, dy, rows, inv_row, topk_w, drows, dtopk_w, alpha: float = 1.0, stream=None):
     """drows[inv_row[n, s]] = alpha topk_w[n, s] dy[n] and dtopk_w[n, s] = alpha <dy[n], rows[inv_row[n, s]]>.
     dtopk_w (and with it rows) may be None; rows that no slot names keep what they held in drows."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(drows, "drows")
     t, (R, D) = drows.dtype, drows.shape
     with _same_device("moe_combine_backward", dy, rows, inv_row, topk_w, drows, dtopk_w):
@@ -523,8 +537,7 @@ def moe_grouped_workspace_size(E: int, R: int, dtype="bf16") -> int:
 def moe_grouped_linear(x, w, offsets, y, workspace, row_index=None, index_div: int = 1, stream=None):
     """y[r] = w[e] x[src(r)] for the rows r in [offsets[e], offsets[e + 1]); w [E, out, in], y [R, out].
     src(r) = row_index[r] // index_div (moe_dispatch's sorted_pair and k), or r without row_index."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(x, "x")
     t, (E, M, K), R = x.dtype, w.shape, y.shape[0]
     ws, ws_bytes = _ws(workspace)
@@ -539,8 +552,7 @@ def moe_grouped_linear(x, w, offsets, y, workspace, row_index=None, index_div: i
 
 def moe_grouped_linear_dgrad(dy, w, offsets, dx, workspace, stream=None):
     """dx[r] = w[e]^T dy[r], one row per grouped row."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(dy, "dy")
     t, (E, M, K), R = dy.dtype, w.shape, dx.shape[0]
     ws, ws_bytes = _ws(workspace)
@@ -554,8 +566,7 @@ def moe_grouped_linear_dgrad(dy, w, offsets, dx, workspace, stream=None):
 
 def moe_grouped_linear_wgrad(dy, x, offsets, dw, workspace, row_index=None, index_div: int = 1, stream=None):
     """dw[e] = sum of dy[r] x[src(r)]^T over the rows of expert e (zeros without rows)."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(dy, "dy")
     t, (E, M, K), R = dy.dtype, dw.shape, dy.shape[0]
     ws, ws_bytes = _ws(workspace)
@@ -571,8 +582,7 @@ def moe_qlinear(x, wq, scales, y, offsets=None, row_index=None, index_div: int =
                 limit: float = 0.0, stream=None):
     """moe_grouped_linear with 4-bit weights: wq [E, out, in / 2] uint8, scales [E, out, in / group] bf16
     (moe_quantize). offsets None (E = 1): all rows. swiglu: y [R, out / 2] = SiLU(gate half) * up half."""
-    import torch
-
+    torch = _torch or _import_torch()
     E, M, half = wq.shape
     K = 2 * half
     if scales.dim() != 3 or scales.shape[2] < 1 or K % scales.shape[2]:
@@ -591,8 +601,7 @@ def moe_qlinear(x, wq, scales, y, offsets=None, row_index=None, index_div: int =
 def moe_quantize(w, group: int, wq=None, scales=None, stream=None):
     """(wq, scales) of w [..., in] for moe_qlinear: uint8 [..., in / 2] and bf16 [..., in / group], allocated here
     when None."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(w, "w")
     K, lead = w.shape[-1], tuple(w.shape[:-1])
     if group < 1 or K % group:
@@ -620,8 +629,7 @@ def moe_layer_norm(N: int, x, residual, w, b, h_out, y, stats=None, eps: float =
     """h = x + residual and y = (h - mean(h)) / std(h) * w + b over each row; std with eps under the root. residual
     (and with it h_out, which receives h), w and b may be None; stats [N, 2] float32 receives mean and 1 / std for
     moe_layer_norm_backward."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(x, "x")
     t, D = x.dtype, x.shape[-1]
     with _same_device("moe_layer_norm", x, residual, w, b, h_out, y, stats):
@@ -637,8 +645,7 @@ def moe_layer_norm_backward(N: int, h, stats, w, dh_out, dy, dh, dw, db, workspa
     """Gradients of moe_layer_norm from its h (h_out, or x without a residual) and stats: dh [N, D] (of x and residual
     alike, dh_out added when given) and, where given, the float32 sums dw and db; workspace:
     moe_layer_norm_workspace_size(N, D, dtype) bytes, or None without sums."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(h, "h")
     t, f, D = h.dtype, torch.float32, h.shape[-1]
     ws, ws_bytes = _ws(workspace)
@@ -685,8 +692,7 @@ def moe_linear_backward_workspace_size(R: int, M: int, dtype="bf16") -> int:
 def moe_linear_backward(dy, z, dz, dbias, workspace=None, act="none", stream=None):
     """dz = dy * act'(z) and the float32 dbias = sum of its rows, each where given; z may be None for act "none". dx and
     dw follow from dz with moe_grouped_linear_dgrad and moe_grouped_linear_wgrad (one expert, offsets [0, R])."""
-    import torch
-
+    torch = _torch or _import_torch()
     dt = _tensor_dtype(dy, "dy")
     t, (R, M) = dy.dtype, dy.shape
     ws, ws_bytes = _ws(workspace)
@@ -707,8 +713,7 @@ def moe_balance_loss(cfg: MoeConfig, N: int, scores, topk_idx, seq_rows: int, we
     """loss[0] = weight * mean over sequences (runs of seq_rows rows) of sum_i f_i P_i, f_i = E / (k V) times the slots
     that name expert i, P_i the mean of the normalised scores, over the V live tokens (token_mask [N] uint8 or bool).
     counts [S, E] int32 and coef [S, E] float32 (d loss / d normalised score, for moe_route_backward) may be None."""
-    import torch
-
+    torch = _torch or _import_torch()
     E, k, f = cfg.n_routed_experts, cfg.num_experts_per_tok, torch.float32
     S = (N + seq_rows - 1) // seq_rows if seq_rows > 0 else 0
     mask = _token_mask(token_mask, N)
@@ -723,8 +728,7 @@ def moe_balance_loss(cfg: MoeConfig, N: int, scores, topk_idx, seq_rows: int, we
 
 
 def _token_mask(t, N):
-    import torch
-
+    torch = _torch or _import_torch()
     return _ptr(t, "token_mask", torch.bool if t is not None and t.dtype == torch.bool else torch.uint8, (N,),
                 required=False)
 
@@ -733,8 +737,7 @@ def moe_route_backward(cfg: MoeConfig, N: int, scores, topk_idx, dtopk_w, dlogit
                        dloss=None, token_mask=None, stream=None):
     """dlogits [N, E] float32 of the router from the gradient of the mixture weights (dtopk_w [N, k], or None) and of the
     balance loss (coef [S, E] of moe_balance_loss with its seq_rows and token_mask, or None; dloss [1] float32, None: 1)."""
-    import torch
-
+    torch = _torch or _import_torch()
     E, k, f = cfg.n_routed_experts, cfg.num_experts_per_tok, torch.float32
     S = (N + seq_rows - 1) // seq_rows if seq_rows > 0 else 0
     mask = _token_mask(token_mask, N)
@@ -779,8 +782,7 @@ def moe_grad_norm_workspace_size(tensors) -> int:
 def moe_grad_norm(tensors, norm, workspace, stream=None):
     """norm[0] = the 2-norm over all values of the tensors (a sequence or a MoeTensorList); workspace:
     moe_grad_norm_workspace_size(tensors) bytes."""
-    import torch
-
+    torch = _torch or _import_torch()
     t = moe_tensor_list(tensors)
     ws, ws_bytes = _ws(workspace)
     with _same_device("moe_grad_norm", *t.tensors[:1], norm, workspace):
@@ -792,8 +794,7 @@ def moe_grad_norm(tensors, norm, workspace, stream=None):
 def moe_grad_clip(tensors, norm, max_norm: float, out=None, eps: float = 1e-6, stream=None):
     """out[i] = tensors[i] * min(1, max_norm / (norm[0] + eps)), read on the device; out None: in place. out may have
     types of its own (bfloat16 gradients clipped into float32 ones)."""
-    import torch
-
+    torch = _torch or _import_torch()
     t = moe_tensor_list(tensors)
     o = None if out is None else moe_tensor_list(out)
     if o is not None and len(o) != len(t):
