@@ -43,6 +43,7 @@ struct BalanceArgs {
   int32_t* part_c;  // [S chunks, E] slots
   int32_t* part_v;  // [S chunks] live tokens
   float* part_l;    // [S] losses of the sequences
+  int32_t* done;    // blocks of balance_join that have ended
 };
 
 // The end of a sequence: f and P of one expert from its sums; returns f P weight / S.
@@ -74,6 +75,7 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
   __shared__ int32_t hist[G * EPL];
   __shared__ int32_t live_rows;
   __shared__ float buf[16];
+  if (a.chunks > 1 && blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;  // for balance_join, the next launch
   const int64_t q = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks;
   const int64_t first = q * a.T + ch * a.chunk;
   const int64_t last = min(min(first + a.chunk, (q + 1) * a.T), a.N);
@@ -87,24 +89,40 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
-  for (int64_t n = first + threadIdx.x / G; n < last; n += groups) {
-    if (a.mask && a.mask[n] == 0) continue;  // the same for the lanes of a group
-    float v[EPL], s = 0.f;
+  // two rows at a time, all their loads first: a block has only a few rows per group, each a trip to memory
+  for (int64_t n0 = first + threadIdx.x / G; n0 < last; n0 += 2 * groups) {
+    float v[2][EPL], sum[2];
+    int32_t id[2];
+    bool live[2];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = lane + G * i;
-      v[i] = e < a.E ? a.scores[n * a.E + e] : 0.f;
-      s += v[i];
-    }
-    s = group_sum<G>(s);
-    const float inv = s != 0.f ? 1.0f / s : 0.f;
+    for (int u = 0; u < 2; ++u) {
+      const int64_t n = n0 + u * groups;
+      const bool have = n < last;
+      live[u] = have && (!a.mask || a.mask[n] != 0);
+      id[u] = have && lane < a.k ? a.idx[n * a.k + lane] : -1;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) acc[i] += v[i] * inv;
-    for (int m = lane; m < a.k; m += G) {
-      const int32_t e = a.idx[n * a.k + m];
-      if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
+      for (int i = 0; i < EPL; ++i) {
+        const int e = lane + G * i;
+        v[u][i] = have && e < a.E ? a.scores[n * a.E + e] : 0.f;
+      }
     }
-    mine += lane == 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (!live[u]) continue;  // the same for the lanes of a group
+      sum[u] = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) sum[u] += v[u][i];
+      sum[u] = group_sum<G>(sum[u]);
+      const float inv = sum[u] != 0.f ? 1.0f / sum[u] : 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) acc[i] += v[u][i] * inv;
+      if (id[u] >= 0 && id[u] < a.E) atomicAdd(&hist[id[u]], 1);
+      for (int m = lane + G; m < a.k; m += G) {  // more slots than lanes
+        const int32_t e = a.idx[(n0 + u * groups) * a.k + m];
+        if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
+      }
+      mine += lane == 0;
+    }
   }
   if (mine) atomicAdd(&live_rows, mine);
   // the groups of a wave, then the waves in order
@@ -134,31 +152,45 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
   }
 }
 
-// The chunks of one sequence, in order: E experts x 1024 / E lanes.
+// The chunks of one sequence, in order: E experts x 1024 / E lanes. The block that ends last adds the sequences' losses,
+// in order.
 __global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
   __shared__ float sp[1024];
   __shared__ int32_t sc[1024];
   __shared__ int32_t sv[16];
   __shared__ float buf[16];
+  __shared__ int last;
   const int64_t q = blockIdx.x, base = q * a.chunks;
-  int v = 0;
-  for (int64_t ch = threadIdx.x; ch < a.chunks; ch += blockDim.x) v += a.part_v[base + ch];
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  if ((threadIdx.x & 63) == 0) sv[threadIdx.x >> 6] = v;
   const int lanes = 1024 / a.E;  // at least 2
   const int e = threadIdx.x % a.E, l = threadIdx.x / a.E;
   float p = 0.f;
-  int32_t c = 0;
+  int32_t c = 0, v = 0;
   if (l < lanes) {
-#pragma unroll 8
-    for (int64_t ch = l; ch < a.chunks; ch += lanes) {
-      p += a.part_p[(base + ch) * a.E + e];
-      c += a.part_c[(base + ch) * a.E + e];
+    for (int64_t ch = l; ch < a.chunks; ch += 8 * lanes) {
+      float rp[8];
+      int32_t rc[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const bool have = ch + u * lanes < a.chunks;
+        const int64_t at = (base + ch + u * lanes) * a.E + e;
+        rp[u] = have ? a.part_p[at] : 0.f;
+        rc[u] = have ? a.part_c[at] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        p += rp[u];
+        c += rc[u];
+      }
     }
+  }
+  for (int64_t ch = threadIdx.x; ch < a.chunks; ch += blockDim.x) v += a.part_v[base + ch];
+  if (l < lanes) {
     sp[l * a.E + e] = p;
     sc[l * a.E + e] = c;
   }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
+  if ((threadIdx.x & 63) == 0) sv[threadIdx.x >> 6] = v;
   __syncthreads();
   float loss = 0.f;
   if (threadIdx.x < a.E) {
@@ -172,7 +204,22 @@ __global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
     loss = finish_expert(a, q, e, p, c, v);
   }
   loss = block_total(loss, buf);
-  if (threadIdx.x == 0) (a.S == 1 ? a.loss : a.part_l + q)[0] = loss;
+  if (a.S == 1) {
+    if (threadIdx.x == 0) *a.loss = loss;
+    return;
+  }
+  if (threadIdx.x == 0) {
+    a.part_l[q] = loss;
+    __threadfence();  // before the count, so that the block that sees it full sees every loss
+    last = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  float s = 0.f;
+  for (int64_t i = threadIdx.x; i < a.S; i += 1024) s += __hip_atomic_load(a.part_l + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  s = block_total(s, buf);
+  if (threadIdx.x == 0) *a.loss = s;
 }
 
 __global__ __launch_bounds__(1024) void balance_total(const float* part, int64_t n, float* loss) {
@@ -205,22 +252,32 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
   const int lane = threadIdx.x % G;
   const int64_t n = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
   if (n >= a.N) return;  // whole groups
+  // every load first
   const float* row = a.scores + n * a.E;
-  float s[EPL], ds[EPL];
+  const float* co = a.coef ? a.coef + n / a.T * a.E : nullptr;
+  float s[EPL], c[EPL], ds[EPL];
+  int32_t id[SPL];
+  float w[SPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + G * i;
     s[i] = e < a.E ? row[e] : 0.f;
+    c[i] = co && e < a.E ? co[e] : 0.f;
     ds[i] = 0.f;
   }
-  if (a.coef && (!a.mask || a.mask[n] != 0)) {
-    const float* co = a.coef + n / a.T * a.E;
-    const float g = a.dloss ? *a.dloss : 1.0f;
-    float c[EPL], sum = 0.f, dot = 0.f;
+#pragma unroll
+  for (int m = 0; m < SPL; ++m) {
+    const int slot = lane + G * m;
+    const bool have = a.dw && slot < a.k;
+    id[m] = have ? a.idx[n * a.k + slot] : -1;
+    w[m] = have ? a.dw[n * a.k + slot] : 0.f;
+  }
+  const bool live = !a.mask || a.mask[n] != 0;
+  const float g = a.dloss ? *a.dloss : 1.0f;
+  if (co && live) {
+    float sum = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = lane + G * i;
-      c[i] = e < a.E ? co[e] : 0.f;
       sum += s[i];
       dot += c[i] * s[i];
     }
@@ -231,17 +288,20 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
     for (int i = 0; i < EPL; ++i) ds[i] = g * inv * (c[i] - dot * inv);
   }
   if (a.dw) {
-    int32_t id[SPL];
-    float v[SPL], w[SPL], total = 0.f, dot = 0.f;
+    float total = 0.f, dot = 0.f;
 #pragma unroll
     for (int m = 0; m < SPL; ++m) {
-      const int slot = lane + G * m;
-      id[m] = slot < a.k ? a.idx[n * a.k + slot] : -1;
+      if (G * m >= a.k) continue;
       const bool ok = id[m] >= 0 && id[m] < a.E;
-      v[m] = ok ? row[id[m]] : 0.f;
-      w[m] = ok ? a.dw[n * a.k + slot] : 0.f;
-      total += v[m];
-      dot += v[m] * w[m];
+      float v = 0.f;  // the score of the slot's expert, from the lane that holds it
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const float o = __shfl(s[i], id[m] & (G - 1), G);
+        if (ok && id[m] / G == i) v = o;
+      }
+      if (!ok) w[m] = 0.f;
+      total += v;
+      dot += v * w[m];
     }
     if (a.norm) {
       total = group_sum<G>(total) + a.eps;
@@ -342,6 +402,7 @@ hipError_t launch_balance(const BalanceCall& c, hipStream_t s) {
   a.part_c = c.part_c;
   a.part_v = c.part_v;
   a.part_l = c.part_l;
+  a.done = c.done;
   hipError_t e = with_shape(c.E, [&](auto g, auto epl) {
     hipLaunchKernelGGL((balance_chunks<decltype(g)::value, decltype(epl)::value>), dim3((unsigned)(p.S * p.chunks)),
                        dim3(p.threads), 0, s, a);
@@ -351,7 +412,7 @@ hipError_t launch_balance(const BalanceCall& c, hipStream_t s) {
     hipLaunchKernelGGL(balance_join, dim3((unsigned)p.S), dim3(1024), 0, s, a);
     e = hipGetLastError();
   }
-  if (e == hipSuccess && p.S > 1) {
+  if (e == hipSuccess && p.chunks == 1 && p.S > 1) {
     hipLaunchKernelGGL(balance_total, dim3(1), dim3(1024), 0, s, (const float*)a.part_l, p.S, a.loss);
     e = hipGetLastError();
   }

@@ -149,7 +149,9 @@ __global__ __launch_bounds__(G ? kRowThreads : kBackwardThreads) void layer_norm
 #pragma unroll
     for (int i = 0; i < 8; ++i) aw[v][i] = ab[v][i] = 0.f;
   Raw8<T> rw[VPT];
-  // the next row's pieces: its loads run under this row's sums
+  // The next row's pieces: its loads run under this row's sums. Not with four pieces per thread (rows of more than 8,192
+  // features), whose registers hold one row only: there each row's loads are waited for.
+  constexpr bool AHEAD = VPT < 4;
   Raw8<T> nh[VPT], ny[VPT], nd[VPT];
   float mean = 0.f, rstd = 0.f;
   auto fetch = [&](int64_t n) {
@@ -173,7 +175,8 @@ __global__ __launch_bounds__(G ? kRowThreads : kBackwardThreads) void layer_norm
   int64_t n = run + (G ? threadIdx.x / GG : 0);
   if (n < last) fetch(n);
   for (int it = 0; n < last; n += rows_at_once, ++it) {
-    float h[VPT][8], y[VPT][8], d[VPT][8];
+    float h[VPT][8], y[VPT][8];
+    Raw8<T> rd[VPT];
     const float m = mean, r = rstd;
     float s[2] = {0.f, 0.f};
 #pragma unroll
@@ -181,14 +184,9 @@ __global__ __launch_bounds__(G ? kRowThreads : kBackwardThreads) void layer_norm
       if ((t + v * step) * 8 >= p.D) continue;
       widen8(nh[v], h[v]);
       widen8(ny[v], y[v]);
-      if (p.dh_out)
-        widen8(nd[v], d[v]);
-      else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[v][i] = 0.f;
-      }
+      rd[v] = nd[v];
     }
-    if (n + rows_at_once < last) fetch(n + rows_at_once);
+    if (AHEAD && n + rows_at_once < last) fetch(n + rows_at_once);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       if ((t + v * step) * 8 >= p.D) continue;
@@ -210,10 +208,13 @@ __global__ __launch_bounds__(G ? kRowThreads : kBackwardThreads) void layer_norm
     for (int v = 0; v < VPT; ++v) {
       const int c = (t + v * step) * 8;
       if (c >= p.D) continue;
+      float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (p.dh_out) widen8(rd[v], d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[v][i] += r * (y[v][i] - c0 - h[v][i] * c1);
-      raw_store8(p.dh + n * p.D + c, d[v]);
+      for (int i = 0; i < 8; ++i) d[i] += r * (y[v][i] - c0 - h[v][i] * c1);
+      raw_store8(p.dh + n * p.D + c, d);
     }
+    if (!AHEAD && n + rows_at_once < last) fetch(n + rows_at_once);
   }
   if (p.want == 0) return;
   if constexpr (G != 0) {

@@ -199,6 +199,7 @@ struct BalanceCall {
   int32_t* part_c;  // [S chunks, E]
   int32_t* part_v;  // [S chunks]
   float* part_l;    // [S], with more than one sequence
+  int32_t* done;    // [1], with more than one chunk
 };
 hipError_t launch_balance(const BalanceCall& c, hipStream_t s);
 struct RouteBackCall {

@@ -50,7 +50,7 @@ moe_status check_routing(const moe_config* cfg, int64_t N, int64_t seq_rows) {
 }
 
 struct BalanceLayout {
-  size_t part_p, part_c, part_v, part_l, total;
+  size_t part_p, part_c, part_v, part_l, done, total;
 };
 BalanceLayout balance_layout(const BalancePlan& p, int E) {
   BalanceLayout w{};
@@ -65,6 +65,7 @@ BalanceLayout balance_layout(const BalancePlan& p, int E) {
   w.part_c = take(4 * parts * E);
   w.part_v = take(4 * parts);
   w.part_l = take(p.S > 1 ? 4 * (size_t)p.S : 0);
+  w.done = take(parts ? 4 : 0);
   w.total = o;
   return w;
 }
@@ -283,7 +284,7 @@ moe_status moe_balance_loss(const moe_config* cfg, int64_t N, int64_t seq_rows, 
   char* ws = (char*)workspace;
   const BalanceCall c{N, seq_rows, E, cfg->num_experts_per_tok, weight, scores, topk_idx, token_mask, counts, coef, loss,
                       (float*)(ws + L.part_p), (int32_t*)(ws + L.part_c), (int32_t*)(ws + L.part_v),
-                      (float*)(ws + L.part_l)};
+                      (float*)(ws + L.part_l), (int32_t*)(ws + L.done)};
   MOE_TRY(ST_BALANCE, launch_balance(c, s));
   return MOE_OK;
 }
