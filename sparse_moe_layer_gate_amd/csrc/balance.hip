@@ -164,7 +164,7 @@ __global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
   const int lanes = 1024 / a.E;  // at least 2
   const int e = threadIdx.x % a.E, l = threadIdx.x / a.E;
   float p = 0.f;
-  int32_t c = 0, v = 0;
+  int32_t c = 0, v = threadIdx.x < a.chunks ? a.part_v[base + threadIdx.x] : 0;  // at most 512 chunks
   if (l < lanes) {
     for (int64_t ch = l; ch < a.chunks; ch += 8 * lanes) {
       float rp[8];
@@ -183,7 +183,6 @@ __global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
       }
     }
   }
-  for (int64_t ch = threadIdx.x; ch < a.chunks; ch += blockDim.x) v += a.part_v[base + ch];
   if (l < lanes) {
     sp[l * a.E + e] = p;
     sc[l * a.E + e] = c;
