@@ -357,9 +357,9 @@ moe_status moe_quantize(int32_t dtype, int64_t rows, int32_t in, int32_t group, 
  *   residual NULL: h = x, and h_out is NULL. Otherwise h_out receives h.
  *   stats [N, 2] float32: mean and rstd of each row, for moe_layer_norm_backward, or NULL.
  * Float32 arithmetic; h_out and y are each rounded once, y from the unrounded h. h_out may be x or residual (in
- * place); no other overlap. D: a multiple of 8, at most 16384; N below 2^31, and N * T below 2^32 with T the threads of
- * a row: the least power of two of at least D / 8, from 8 to 64, for D up to 2048; above, D / 8 (D / 16 above 8192)
- * rounded up to a multiple of 64. N = 0 launches nothing. */
+ * place); no other overlap. D: a multiple of 8, at most 16384; N below 2^31, and the launch below 2^32 threads: of a row
+ * the least power of two of at least D / 8, from 8 to 64, for D up to 2048; above, D / 8 (D / 16 above 8192) rounded up to
+ * a multiple of 64. N = 0 launches nothing. */
 moe_status moe_layer_norm(int64_t N, int32_t D, int32_t dtype, float eps, const void* x, const void* residual,
                           const void* w, const void* b, void* h_out, void* y, float* stats, void* stream);
 
@@ -395,7 +395,8 @@ typedef enum {
  *           never falls as R grows.
  * Float32 sums over the whole reduction and float32 epilogue; z and y are each rounded once, y from the unrounded z.
  * y may be residual (in place); no other overlap. in: a multiple of 64, out: a multiple of 8, both up to 2^22,
- * in * out below 2^31; R below 2^31 and R * out below 2^40. R = 0 launches nothing. */
+ * in * out below 2^31; R below 2^31 and R * out below 2^40; MOE_ERR_UNSUPPORTED also where the tiles of
+ * y, of 64 x 64 or more with 512 threads each, would take 2^32 threads. R = 0 launches nothing. */
 size_t moe_linear_workspace_size(int64_t R, int32_t in, int32_t out, int32_t dtype);
 moe_status moe_linear(int64_t R, int32_t in, int32_t out, int32_t dtype, int32_t activation, const void* x,
                       const void* w, const void* bias, const void* residual, void* z, void* y, void* workspace,
@@ -408,7 +409,8 @@ moe_status moe_linear(int64_t R, int32_t in, int32_t out, int32_t dtype, int32_t
  *   dz or dbias may be NULL (not wanted), not both; z may be NULL for MOE_ACT_NONE (dz is then a copy of dy).
  *   workspace: at least moe_linear_backward_workspace_size(R, out, dtype) bytes (may be NULL without dbias). The size
  *           never falls as R grows.
- * dz may be dy or z (in place); no other overlap. Sizes as for moe_linear. R = 0 writes zeros to dbias. */
+ * dz may be dy or z (in place); no other overlap. Sizes as for moe_linear, and ceil(R / 64) * ceil(out / 512) below 2^24.
+ * R = 0 writes zeros to dbias. */
 size_t moe_linear_backward_workspace_size(int64_t R, int32_t out, int32_t dtype);
 moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t activation, const void* dy,
                                const void* z, void* dz, float* dbias, void* workspace, size_t ws_bytes, void* stream);
@@ -459,7 +461,8 @@ typedef struct {
 /* The 2-norm over all values of n tensors: norm[0] = sqrt(sum of squares), float32 on the device. Squares and sums are
  * float64, in a fixed order, so neither overflows nor vanishes where the norm itself is a float32; a NaN gives NaN, an
  * infinity without one infinity. n = 0 or no values: 0.
- *   workspace: at least moe_grad_norm_workspace_size(tensors, n) bytes, 16-byte aligned
+ *   workspace: at least moe_grad_norm_workspace_size(tensors, n) bytes, 16-byte aligned; the size depends on the tensors'
+ *           lengths alone
  * n up to 65536, 2^40 values in all. */
 size_t moe_grad_norm_workspace_size(const moe_tensor* tensors, int32_t n);
 moe_status moe_grad_norm(const moe_tensor* tensors, int32_t n, float* norm, void* workspace, size_t ws_bytes,
@@ -468,8 +471,8 @@ moe_status moe_grad_norm(const moe_tensor* tensors, int32_t n, float* norm, void
 /* Clipping by that norm: out = tensor * scale with scale = max_norm / (norm[0] + eps) where that is below 1, else 1,
  * in float32, rounded once. norm is read on the device. out: n tensors of the same numel, each of its own dtype, or NULL:
  * in place (with a scale of 1 the tensors are then left as they are). A norm of infinity gives the scale 0 and a NaN the
- * scale NaN: look at norm before the optimizer's step. No tensor written overlaps another of either list, but out[i] may
- * be tensors[i] exactly. max_norm >= 0 and eps >= 0, finite. */
+ * scale NaN: look at norm before the optimizer's step. No tensor written overlaps norm or another of either list, but
+ * out[i] may be tensors[i] exactly. max_norm >= 0 and eps >= 0, finite. */
 moe_status moe_grad_clip(const moe_tensor* tensors, const moe_tensor* out, int32_t n, const float* norm, float max_norm,
                          float eps, void* stream);
 

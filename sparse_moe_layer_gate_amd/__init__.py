@@ -665,6 +665,13 @@ def _activation(act) -> int:
     return int(code)
 
 
+def _rows_columns(t, name):
+    shape = getattr(t, "shape", ())
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a tensor of two dimensions")
+    return shape
+
+
 def moe_linear_workspace_size(R: int, K: int, M: int, dtype="bf16") -> int:
     """Bytes of workspace of moe_linear for R rows, K input and M output features."""
     return int(lib().moe_linear_workspace_size(int(R), int(K), int(M), _dtype_code(dtype)))
@@ -674,7 +681,7 @@ def moe_linear(x, w, y, workspace=None, bias=None, residual=None, act="none", z=
     """y = act(x w^T + bias) + residual; x [R, in], w [out, in], y [R, out]. z [R, out] receives x w^T + bias for
     moe_linear_backward. act: a key of MOE_ACTIVATIONS. workspace: moe_linear_workspace_size(R, in, out, dtype) bytes."""
     dt = _tensor_dtype(x, "x")
-    t, (R, M), K = x.dtype, y.shape, x.shape[-1]
+    t, (R, M), K = x.dtype, _rows_columns(y, "y"), x.shape[-1]
     ws, ws_bytes = _ws(workspace)
     with _same_device("moe_linear", x, w, y, workspace, bias, residual, z):
         st = lib().moe_linear(
@@ -694,7 +701,7 @@ def moe_linear_backward(dy, z, dz, dbias, workspace=None, act="none", stream=Non
     dw follow from dz with moe_grouped_linear_dgrad and moe_grouped_linear_wgrad (one expert, offsets [0, R])."""
     torch = _torch or _import_torch()
     dt = _tensor_dtype(dy, "dy")
-    t, (R, M) = dy.dtype, dy.shape
+    t, (R, M) = dy.dtype, _rows_columns(dy, "dy")
     ws, ws_bytes = _ws(workspace)
     with _same_device("moe_linear_backward", dy, z, dz, dbias, workspace):
         st = lib().moe_linear_backward(

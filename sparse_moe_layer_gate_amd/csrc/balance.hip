@@ -91,7 +91,7 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
   for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
   // two rows at a time, all their loads first: a block has only a few rows per group, each a trip to memory
   for (int64_t n0 = first + threadIdx.x / G; n0 < last; n0 += 2 * groups) {
-    float v[2][EPL], sum[2];
+    float v[2][EPL];
     int32_t id[2];
     bool live[2];
 #pragma unroll
@@ -109,11 +109,11 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (!live[u]) continue;  // the same for the lanes of a group
-      sum[u] = 0.f;
+      float total = 0.f;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) sum[u] += v[u][i];
-      sum[u] = group_sum<G>(sum[u]);
-      const float inv = sum[u] != 0.f ? 1.0f / sum[u] : 0.f;
+      for (int i = 0; i < EPL; ++i) total += v[u][i];
+      total = group_sum<G>(total);
+      const float inv = total != 0.f ? 1.0f / total : 0.f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) acc[i] += v[u][i] * inv;
       if (id[u] >= 0 && id[u] < a.E) atomicAdd(&hist[id[u]], 1);

@@ -365,10 +365,7 @@ hipError_t layer_norm_t(const LayerNormCall& c, bool backward, hipStream_t s) {
 
 }  // namespace
 
-int layer_norm_threads(int D) {
-  const Shape sh = shape_of(D, 1024);
-  return sh.lanes ? sh.lanes : sh.threads;
-}
+int layer_norm_threads(int D) { return shape_of(D, 1024).threads; }
 int64_t layer_norm_blocks(int64_t N, int D) {
   const Shape sh = shape_of(D, 1024);
   return sh.lanes ? (N + kRowThreads / sh.lanes - 1) / (kRowThreads / sh.lanes) : N;

@@ -765,8 +765,8 @@ hipError_t linear_t(const LinearCall& c, const LinearPlan& p, hipStream_t s) {
 constexpr int kBackRows = 64;
 
 template <typename T>
-__global__ __launch_bounds__(256) void linear_back(int64_t R, int M, int act, const T* __restrict__ dy, const T* z, T* dz,
-                                                   float* part, int64_t runs) {
+__global__ __launch_bounds__(256) void linear_back(int64_t R, int M, int act, const T* dy, const T* z, T* dz, float* part,
+                                                   int64_t runs) {
   __shared__ float join[4][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t run = blockIdx.x % runs;
@@ -879,8 +879,7 @@ LinearPlan linear_plan(int dtype, int64_t R, int in, int out) {
 }
 
 // At most kMostSplits parts and kMostPart floats; never falls as R grows.
-size_t linear_part_bytes(int dtype, int64_t R, int out) {
-  (void)dtype;
+size_t linear_part_bytes(int64_t R, int out) {
   if (R <= kFewRows) return 0;
   const int64_t rows = std::min<int64_t>(R, kMostPart);
   return sizeof(float) * (size_t)std::min<int64_t>(rows * out * kMostSplits, kMostPart);

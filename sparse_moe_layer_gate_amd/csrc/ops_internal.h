@@ -144,7 +144,7 @@ struct LayerNormCall {
   void* dh;
   float *dw, *db, *part;
 };
-int layer_norm_threads(int D);  // of a row in the forward pass
+int layer_norm_threads(int D);  // of a block of the forward pass
 int64_t layer_norm_blocks(int64_t N, int D);
 int64_t layer_norm_runs(int D);  // most runs of rows, each with a partial row of dw and of db
 hipError_t launch_layer_norm(int dtype, const LayerNormCall& c, bool backward, hipStream_t s);
@@ -166,7 +166,7 @@ struct LinearPlan {
   int splits;  // parts of the reduction
 };
 LinearPlan linear_plan(int dtype, int64_t R, int in, int out);
-size_t linear_part_bytes(int dtype, int64_t R, int out);  // workspace; never falls as R grows
+size_t linear_part_bytes(int64_t R, int out);  // workspace; never falls as R grows
 int64_t linear_join_blocks(int64_t R, int out);
 hipError_t launch_linear(int dtype, const LinearCall& c, hipStream_t s);
 struct LinearBackCall {
@@ -217,7 +217,7 @@ int64_t route_backward_blocks(int64_t N, int E);  // of 256 threads
 hipError_t launch_route_backward(const RouteBackCall& c, hipStream_t s);
 
 // ---- gradient norm and clipping ----
-int64_t tensor_chunks(const moe_tensor* t, int n);  // partial sums of a list
+int64_t most_tensor_chunks(const moe_tensor* t, int n);  // partial sums of a list of such lengths, wherever it lies
 hipError_t launch_grad_norm(const moe_tensor* t, int n, double* part, float* norm, hipStream_t s);
 hipError_t launch_grad_clip(const moe_tensor* t, const moe_tensor* out, int n, const float* norm, float max_norm,
                             float eps, hipStream_t s);

@@ -26,7 +26,7 @@ bool workspace_ok(const void* p, size_t have, size_t need) {
 moe_status check_layer_norm(int64_t N, int32_t D, int32_t dtype) {
   if (N < 0 || D < 1 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
   if (D % 8 != 0 || D > 16384 || N >= kInt31) return MOE_ERR_UNSUPPORTED;
-  if (N > 0 && !launch_fits(N, layer_norm_threads(D))) return MOE_ERR_UNSUPPORTED;
+  if (!launch_fits(layer_norm_blocks(N, D), layer_norm_threads(D))) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -208,7 +208,7 @@ moe_status moe_layer_norm_backward(int64_t N, int32_t D, int32_t dtype, const vo
 // ---- linear maps ----
 size_t moe_linear_workspace_size(int64_t R, int32_t in, int32_t out, int32_t dtype) {
   if (check_linear(R, in, out, dtype) != MOE_OK) return 0;
-  return linear_part_bytes(dtype, R, out);
+  return linear_part_bytes(R, out);
 }
 
 moe_status moe_linear(int64_t R, int32_t in, int32_t out, int32_t dtype, int32_t activation, const void* x,
@@ -224,7 +224,7 @@ moe_status moe_linear(int64_t R, int32_t in, int32_t out, int32_t dtype, int32_t
   if (!x || !w || !y || !all_aligned16(x, w, bias, residual, z, y)) return MOE_ERR_INVALID_ARG;
   if (y == x || y == w || y == bias || y == z || (z && (z == x || z == w || z == bias || z == residual)))
     return MOE_ERR_INVALID_ARG;
-  if (!workspace_ok(workspace, ws_bytes, linear_part_bytes(dtype, R, out))) return MOE_ERR_WORKSPACE;
+  if (!workspace_ok(workspace, ws_bytes, linear_part_bytes(R, out))) return MOE_ERR_WORKSPACE;
   hipStream_t s = (hipStream_t)stream;
   const LinearCall c{R, in, out, activation, x, w, bias, residual, z, y, (float*)workspace};
   MOE_TRY(ST_LINEAR, launch_linear(dtype, c, s));
@@ -311,7 +311,7 @@ moe_status moe_route_backward(const moe_config* cfg, int64_t N, const float* sco
 // ---- gradient norm and clipping ----
 size_t moe_grad_norm_workspace_size(const moe_tensor* tensors, int32_t n) {
   if (check_tensors(tensors, n) != MOE_OK) return 0;
-  return align_up(sizeof(double) * std::max<int64_t>(1, tensor_chunks(tensors, n)));
+  return align_up(sizeof(double) * std::max<int64_t>(1, most_tensor_chunks(tensors, n)));
 }
 
 moe_status moe_grad_norm(const moe_tensor* tensors, int32_t n, float* norm, void* workspace, size_t ws_bytes,
@@ -336,6 +336,11 @@ moe_status moe_grad_clip(const moe_tensor* tensors, const moe_tensor* out, int32
       if (out[i].numel != tensors[i].numel) return MOE_ERR_INVALID_ARG;
   }
   if (!norm || (uintptr_t)norm % 4 != 0) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {  // a block might read the norm after another one has scaled it
+    const moe_tensor& w = out ? out[i] : tensors[i];
+    const uintptr_t begin = (uintptr_t)w.data, end = begin + w.numel * value_bytes(w);
+    if ((uintptr_t)norm < end && (uintptr_t)norm + 4 > begin) return MOE_ERR_INVALID_ARG;
+  }
   const Overlap o = clip_overlap(tensors, out, n);
   if (o != Overlap::None) return o == Overlap::Some ? MOE_ERR_INVALID_ARG : MOE_ERR_UNSUPPORTED;
   hipStream_t s = (hipStream_t)stream;

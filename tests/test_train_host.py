@@ -129,12 +129,23 @@ def norm(ts, n=None, out=p(0), ws=p(1), size=BIG):
     return moe.lib().moe_grad_norm(tensors(*ts), len(ts) if n is None else n, out, ws, size, None)
 
 
-def clip(ts, out=None, n=None, norm=p(0), m=1.0, eps=1e-6):
+def clip(ts, out=None, n=None, norm=p(1 << 20), m=1.0, eps=1e-6):
     return moe.lib().moe_grad_clip(tensors(*ts), None if out is None else tensors(*out), len(ts) if n is None else n, norm, m, eps,
                                    None)
 
 
 F, B = moe.MOE_F32, moe.MOE_BF16
+
+
+def test_tensor_list_workspace_of_any_alignment():
+    """A workspace sized for a list serves the same lengths elsewhere."""
+    size = moe.lib().moe_grad_norm_workspace_size
+    lengths = [2048 * 700, 1, 2047, 2049, 16384 * 40]
+    for dt, step in ((F, 4), (B, 2)):
+        for scale in (1, 16):
+            at = [size(tensors(*((1 << 30 | (off + 8 * i) * step, scale * n, dt) for i, n in enumerate(lengths))), len(lengths))
+                  for off in (0, 1, 31, 63)]
+            assert len(set(at)) == 1
 
 
 @pytest.mark.parametrize("fn,args,kw,status", [
@@ -153,6 +164,10 @@ F, B = moe.MOE_F32, moe.MOE_BF16
     (clip, [[(4096, 4, F), (8192, 4, F)]], dict(out=[(1 << 20, 4, F), (1 << 20, 4, F)]), INV),
     (clip, [[(4096, 4, F)]], dict(out=[(4096, 4, B)]), INV), (clip, [[(4096, 4, F)]], dict(out=[(4100, 4, F)]), INV),
     (clip, [[(1 << 20, 4, B), (4096, 4, F)]], dict(out=[((1 << 20) + 2, 4, B), (4096, 4, F)]), INV),
+    # the norm in a tensor that is written, its first and last value and one that half covers it; beside it and in one only read
+    (clip, [[(4096, 4, F)]], dict(norm=ctypes.c_void_p(4096)), INV), (clip, [[(4096, 4, F)]], dict(norm=ctypes.c_void_p(4108)), INV),
+    (clip, [[(4098, 4, B)]], dict(norm=ctypes.c_void_p(4096)), INV),
+    (clip, [[(1 << 20, 4, F)]], dict(out=[(4096, 4, B)], norm=ctypes.c_void_p(4100)), INV),
     (clip, [[]], {}, OK), (clip, [[(None, 0, F), (None, 0, B)]], {}, OK),
 ])
 def test_tensor_list_errors(fn, args, kw, status):
@@ -167,6 +182,9 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         moe.moe_linear(t, t, t)
     with pytest.raises(TypeError):
         moe.moe_linear_backward(t, t, t, None)
+    for y in (None, t[0], 3):
+        with pytest.raises((TypeError, ValueError)):
+            moe.moe_linear(t, t, y)
     with pytest.raises(TypeError):
         moe.moe_balance_loss(CFG, 4, t, t, 4, 0.1, None, None, t, None)
     with pytest.raises(TypeError):
