@@ -358,8 +358,8 @@ moe_status moe_quantize(int32_t dtype, int64_t rows, int32_t in, int32_t group, 
  *   stats [N, 2] float32: mean and rstd of each row, for moe_layer_norm_backward, or NULL.
  * Float32 arithmetic; h_out and y are each rounded once, y from the unrounded h. h_out may be x or residual (in
  * place); no other overlap. D: a multiple of 8, at most 16384; N below 2^31, and the launch below 2^32 threads: of a row
- * the least power of two of at least D / 8, from 8 to 64, for D up to 2048; above, D / 8 (D / 16 above 8192) rounded up to
- * a multiple of 64. N = 0 launches nothing. */
+ * the least power of two of at least D / 8, from 8 to 64, for D up to 2048; above, D / 32 (D / 24 from 8200 to 12288)
+ * rounded up to a multiple of 64. N = 0 launches nothing. */
 moe_status moe_layer_norm(int64_t N, int32_t D, int32_t dtype, float eps, const void* x, const void* residual,
                           const void* w, const void* b, void* h_out, void* y, float* stats, void* stream);
 
@@ -409,8 +409,7 @@ moe_status moe_linear(int64_t R, int32_t in, int32_t out, int32_t dtype, int32_t
  *   dz or dbias may be NULL (not wanted), not both; z may be NULL for MOE_ACT_NONE (dz is then a copy of dy).
  *   workspace: at least moe_linear_backward_workspace_size(R, out, dtype) bytes (may be NULL without dbias). The size
  *           never falls as R grows.
- * dz may be dy or z (in place); no other overlap. Sizes as for moe_linear, and ceil(R / 64) * ceil(out / 512) below 2^24.
- * R = 0 writes zeros to dbias. */
+ * dz may be dy or z (in place); no other overlap. Sizes as for moe_linear. R = 0 writes zeros to dbias. */
 size_t moe_linear_backward_workspace_size(int64_t R, int32_t out, int32_t dtype);
 moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t activation, const void* dy,
                                const void* z, void* dz, float* dbias, void* workspace, size_t ws_bytes, void* stream);
@@ -427,7 +426,8 @@ moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t ac
  *   counts [S, E] int32, coef [S, E] float32 (for moe_route_backward): written, or NULL where not wanted
  *   loss [1] float32, written
  *   workspace: at least moe_balance_workspace_size(cfg, N, seq_rows) bytes
- * Sums in a fixed order. N k below 2^31, N E below 2^40. N = 0 writes 0 to loss. */
+ * Sums in a fixed order. N k below 2^31, N E below 2^40, the launch below 2^32 threads (any N below 2^26). N = 0 writes 0
+ * to loss. */
 size_t moe_balance_workspace_size(const moe_config* cfg, int64_t N, int64_t seq_rows);
 moe_status moe_balance_loss(const moe_config* cfg, int64_t N, int64_t seq_rows, float weight, const float* scores,
                             const int32_t* topk_idx, const uint8_t* token_mask, int32_t* counts, float* coef,

@@ -11,6 +11,7 @@
 // caches, by latency: a row belongs to a group of 8 to 64 lanes, so that its sums are shuffles.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "ops_internal.h"
@@ -42,8 +43,8 @@ struct BalanceArgs {
   float* part_p;    // [S chunks, E] sums of p
   int32_t* part_c;  // [S chunks, E] slots
   int32_t* part_v;  // [S chunks] live tokens
-  float* part_l;    // [S] losses of the sequences
-  int32_t* done;    // blocks of balance_join that have ended
+  float* part_l;    // losses of the sequences, or of the blocks of balance_join
+  int32_t* done;    // blocks of balance_join that have ended; nullptr: balance_total adds their shares
 };
 
 // The end of a sequence: f and P of one expert from its sums; returns f P weight / S.
@@ -66,32 +67,54 @@ __device__ inline float block_total(float v, float* buf) {
   return t;
 }
 
-// One chunk of a sequence's rows: a group of G lanes per row, lane j holding experts j + G i. Live tokens add to the
-// sums in registers, the slots to a histogram in LDS (whole numbers: the order does not matter). A sequence of one
-// chunk is finished here.
-template <int G, int EPL>
+// The scores of a row lie with a group of G lanes: piece i of lane j holds the V experts from V (j + G i) on, one load of V
+// floats. V = 4 needs E to be a multiple of 4; 16 lanes then take a row of up to 64 experts in one load and a wave four
+// rows (one row of 64 lanes and single floats: 1 M rows of 64 experts, gradient 407 us against PLACEHOLDER).
+template <int G, int PL, int V>
+struct Row {
+  static constexpr int N = PL * V;  // values per lane
+  __device__ static int expert(int lane, int x) { return V * (lane + G * (x / V)) + x % V; }
+  __device__ static void load(const float* row, int E, int lane, float* v) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i) {
+      const int e = V * (lane + G * i);
+      if constexpr (V == 4) {
+        const f32x4v q = e < E ? *(const f32x4v*)(row + e) : f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * i + j] = q[j];
+      } else {
+        v[i] = e < E ? row[e] : 0.f;
+      }
+    }
+  }
+};
+
+// One chunk of a sequence's rows. Live tokens add to the sums in registers, the slots to a histogram in LDS (whole numbers:
+// the order does not matter). A sequence of one chunk is finished here.
+template <int G, int PL, int V>
 __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
-  __shared__ float sum[16][G * EPL];
-  __shared__ int32_t hist[G * EPL];
+  using R = Row<G, PL, V>;
+  __shared__ float sum[16][G * R::N];
+  __shared__ int32_t hist[G * R::N];
   __shared__ int32_t live_rows;
   __shared__ float buf[16];
-  if (a.chunks > 1 && blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;  // for balance_join, the next launch
+  if (a.done && blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;  // for balance_join, the next launch
   const int64_t q = blockIdx.x / a.chunks, ch = blockIdx.x % a.chunks;
   const int64_t first = q * a.T + ch * a.chunk;
   const int64_t last = min(min(first + a.chunk, (q + 1) * a.T), a.N);
   const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < G * EPL; e += blockDim.x) hist[e] = 0;
+  for (int e = threadIdx.x; e < G * R::N; e += blockDim.x) hist[e] = 0;
   if (threadIdx.x == 0) live_rows = 0;
   __syncthreads();
   const int lane = threadIdx.x % G;
   const int groups = blockDim.x / G;
-  float acc[EPL];
+  float acc[R::N];
   int mine = 0;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) acc[i] = 0.f;
+  for (int i = 0; i < R::N; ++i) acc[i] = 0.f;
   // two rows at a time, all their loads first: a block has only a few rows per group, each a trip to memory
   for (int64_t n0 = first + threadIdx.x / G; n0 < last; n0 += 2 * groups) {
-    float v[2][EPL];
+    float v[2][R::N];
     int32_t id[2];
     bool live[2];
 #pragma unroll
@@ -100,22 +123,18 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
       const bool have = n < last;
       live[u] = have && (!a.mask || a.mask[n] != 0);
       id[u] = have && lane < a.k ? a.idx[n * a.k + lane] : -1;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = lane + G * i;
-        v[u][i] = have && e < a.E ? a.scores[n * a.E + e] : 0.f;
-      }
+      if (have) R::load(a.scores + n * a.E, a.E, lane, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (!live[u]) continue;  // the same for the lanes of a group
       float total = 0.f;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) total += v[u][i];
+      for (int i = 0; i < R::N; ++i) total += v[u][i];
       total = group_sum<G>(total);
       const float inv = total != 0.f ? 1.0f / total : 0.f;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) acc[i] += v[u][i] * inv;
+      for (int i = 0; i < R::N; ++i) acc[i] += v[u][i] * inv;
       if (id[u] >= 0 && id[u] < a.E) atomicAdd(&hist[id[u]], 1);
       for (int m = lane + G; m < a.k; m += G) {  // more slots than lanes
         const int32_t e = a.idx[(n0 + u * groups) * a.k + m];
@@ -127,10 +146,10 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
   if (mine) atomicAdd(&live_rows, mine);
   // the groups of a wave, then the waves in order
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
+  for (int i = 0; i < R::N; ++i) {
 #pragma unroll
     for (int off = G; off < 64; off <<= 1) acc[i] += __shfl_xor(acc[i], off);
-    if ((threadIdx.x & 63) < G) sum[wave][lane + G * i] = acc[i];
+    if ((threadIdx.x & 63) < G) sum[wave][R::expert(lane, i)] = acc[i];
   }
   __syncthreads();
   float loss = 0.f;
@@ -152,20 +171,22 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
   }
 }
 
-// The chunks of one sequence, in order: E experts x 1024 / E lanes. The block that ends last adds the sequences' losses,
-// in order.
-__global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
+// The chunks of one sequence, in order: a block takes kJoin experts, up to 32 lanes each, so that few of its loads wait
+// for one another (512 chunks of 256 experts: 4 rounds of PLACEHOLDER). Of a few blocks the one that
+// ends last adds their shares of the loss, in order; many would wait for their fences (512 blocks: 40 us).
+constexpr int kJoin = 32, kFencedBlocks = 128;
+__global__ __launch_bounds__(1024) void balance_join(BalanceArgs a, int parts) {
   __shared__ float sp[1024];
   __shared__ int32_t sc[1024];
   __shared__ int32_t sv[16];
   __shared__ float buf[16];
   __shared__ int last;
-  const int64_t q = blockIdx.x, base = q * a.chunks;
-  const int lanes = 1024 / a.E;  // at least 2
-  const int e = threadIdx.x % a.E, l = threadIdx.x / a.E;
+  const int64_t q = blockIdx.x / parts, base = q * a.chunks;
+  const int lanes = blockDim.x / kJoin;
+  const int e = (int)(blockIdx.x % parts) * kJoin + threadIdx.x % kJoin, l = threadIdx.x / kJoin;
   float p = 0.f;
-  int32_t c = 0, v = threadIdx.x < a.chunks ? a.part_v[base + threadIdx.x] : 0;  // at most 512 chunks
-  if (l < lanes) {
+  int32_t c = 0, v = threadIdx.x < a.chunks ? a.part_v[base + threadIdx.x] : 0;  // no more chunks than threads
+  if (e < a.E) {
     for (int64_t ch = l; ch < a.chunks; ch += 8 * lanes) {
       float rp[8];
       int32_t rc[8];
@@ -183,40 +204,35 @@ __global__ __launch_bounds__(1024) void balance_join(BalanceArgs a) {
       }
     }
   }
-  if (l < lanes) {
-    sp[l * a.E + e] = p;
-    sc[l * a.E + e] = c;
-  }
+  sp[threadIdx.x] = p;
+  sc[threadIdx.x] = c;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
   if ((threadIdx.x & 63) == 0) sv[threadIdx.x >> 6] = v;
   __syncthreads();
   float loss = 0.f;
-  if (threadIdx.x < a.E) {
+  if (threadIdx.x < kJoin && e < a.E) {
     for (int i = 1; i < lanes; ++i) {
-      p += sp[i * a.E + e];
-      c += sc[i * a.E + e];
+      p += sp[i * kJoin + threadIdx.x];
+      c += sc[i * kJoin + threadIdx.x];
     }
     v = 0;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) v += sv[w];
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) v += sv[w];
     loss = finish_expert(a, q, e, p, c, v);
   }
-  loss = block_total(loss, buf);
-  if (a.S == 1) {
-    if (threadIdx.x == 0) *a.loss = loss;
-    return;
-  }
+  if (threadIdx.x < 64) loss = wave_sum(loss);
+  if (threadIdx.x == 0) a.part_l[blockIdx.x] = loss;
+  if (!a.done) return;
   if (threadIdx.x == 0) {
-    a.part_l[q] = loss;
-    __threadfence();  // before the count, so that the block that sees it full sees every loss
+    __threadfence();  // before the count, so that the block that sees it full sees every share
     last = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
   float s = 0.f;
-  for (int64_t i = threadIdx.x; i < a.S; i += 1024) s += __hip_atomic_load(a.part_l + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int64_t i = threadIdx.x; i < gridDim.x; i += blockDim.x)
+    s += __hip_atomic_load(a.part_l + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   s = block_total(s, buf);
   if (threadIdx.x == 0) *a.loss = s;
 }
@@ -243,10 +259,12 @@ struct RouteBackArgs {
   float* out;
 };
 
-// A group of G lanes per token, lane j holding experts j + G i and, as a slot's owner, slots j + G m. dlogits may be
-// the scores: a group reads its row before it writes it.
-template <int G, int EPL>
+// A group of G lanes per token, a slot's owner lane m % G. The slots' scores are read again (they have just been loaded),
+// their gradients go to the lanes of their experts one slot after the other. dlogits may be the scores: a group reads its
+// row before it writes it.
+template <int G, int PL, int V>
 __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
+  using R = Row<G, PL, V>;
   constexpr int SPL = (32 + G - 1) / G;  // slots per lane (k <= 32)
   const int lane = threadIdx.x % G;
   const int64_t n = (int64_t)blockIdx.x * (256 / G) + threadIdx.x / G;
@@ -254,16 +272,9 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
   // every load first
   const float* row = a.scores + n * a.E;
   const float* co = a.coef ? a.coef + n / a.T * a.E : nullptr;
-  float s[EPL], c[EPL], ds[EPL];
+  float s[R::N], c[R::N], ds[R::N];
   int32_t id[SPL];
-  float w[SPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + G * i;
-    s[i] = e < a.E ? row[e] : 0.f;
-    c[i] = co && e < a.E ? co[e] : 0.f;
-    ds[i] = 0.f;
-  }
+  float w[SPL], sw[SPL];
 #pragma unroll
   for (int m = 0; m < SPL; ++m) {
     const int slot = lane + G * m;
@@ -271,12 +282,22 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
     id[m] = have ? a.idx[n * a.k + slot] : -1;
     w[m] = have ? a.dw[n * a.k + slot] : 0.f;
   }
+  R::load(row, a.E, lane, s);
+#pragma unroll
+  for (int i = 0; i < R::N; ++i) c[i] = ds[i] = 0.f;
+  if (co) R::load(co, a.E, lane, c);
+#pragma unroll
+  for (int m = 0; m < SPL; ++m) {
+    const bool ok = id[m] >= 0 && id[m] < a.E;
+    sw[m] = ok ? row[id[m]] : 0.f;
+    if (!ok) w[m] = 0.f;
+  }
   const bool live = !a.mask || a.mask[n] != 0;
   const float g = a.dloss ? *a.dloss : 1.0f;
   if (co && live) {
     float sum = 0.f, dot = 0.f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
+    for (int i = 0; i < R::N; ++i) {
       sum += s[i];
       dot += c[i] * s[i];
     }
@@ -284,25 +305,16 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
     dot = group_sum<G>(dot);
     const float inv = sum != 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) ds[i] = g * inv * (c[i] - dot * inv);
+    for (int i = 0; i < R::N; ++i) ds[i] = g * inv * (c[i] - dot * inv);
   }
   if (a.dw) {
-    float total = 0.f, dot = 0.f;
-#pragma unroll
-    for (int m = 0; m < SPL; ++m) {
-      if (G * m >= a.k) continue;
-      const bool ok = id[m] >= 0 && id[m] < a.E;
-      float v = 0.f;  // the score of the slot's expert, from the lane that holds it
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const float o = __shfl(s[i], id[m] & (G - 1), G);
-        if (ok && id[m] / G == i) v = o;
-      }
-      if (!ok) w[m] = 0.f;
-      total += v;
-      dot += v * w[m];
-    }
     if (a.norm) {
+      float total = 0.f, dot = 0.f;
+#pragma unroll
+      for (int m = 0; m < SPL; ++m) {
+        total += sw[m];
+        dot += sw[m] * w[m];
+      }
       total = group_sum<G>(total) + a.eps;
       dot = group_sum<G>(dot);
       const float r = total != 0.f ? 1.0f / total : 0.f;
@@ -313,70 +325,85 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
       for (int m = 0; m < SPL; ++m) w[m] *= a.alpha;
     }
     // every slot to the lane and value of its expert (an id may come up twice: each adds)
-    for (int slot = 0; slot < a.k; ++slot) {
-      int32_t e = id[0];
-      float b = w[0];
 #pragma unroll
-      for (int m = 1; m < SPL; ++m)
-        if (slot / G == m) {
-          e = id[m];
-          b = w[m];
-        }
-      e = __shfl(e, slot % G, G);
-      b = __shfl(b, slot % G, G);
+    for (int m = 0; m < SPL; ++m) {
+      for (int l = 0; l < G && l + G * m < a.k; ++l) {
+        const int32_t e = __shfl(id[m], l, G);
+        const float b = __shfl(w[m], l, G);
+        const int vec = e / V, at = e >= 0 && vec % G == lane ? vec / G * V + e % V : -1;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (e == lane + G * i) ds[i] += b;
+        for (int i = 0; i < R::N; ++i) ds[i] += at == i ? b : 0.f;
+      }
     }
   }
+  float* out = a.out + n * a.E;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane + G * i;
-    if (e < a.E) a.out[n * a.E + e] = ds[i] == 0.f ? 0.f : ds[i] * s[i] * (1.0f - s[i]);  // whatever a dead token holds
+  for (int i = 0; i < R::N; ++i) ds[i] = ds[i] == 0.f ? 0.f : ds[i] * s[i] * (1.0f - s[i]);  // whatever a dead token holds
+#pragma unroll
+  for (int i = 0; i < PL; ++i) {
+    const int e = V * (lane + G * i);
+    if (e >= a.E) continue;
+    if constexpr (V == 4)
+      *(f32x4v*)(out + e) = f32x4v{ds[4 * i], ds[4 * i + 1], ds[4 * i + 2], ds[4 * i + 3]};
+    else
+      out[e] = ds[i];
   }
 }
 
-// Lanes of a row's group and experts per lane.
-int lanes_of(int E) { return E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64; }
+// Lanes of a row's group.
+int lanes_of(int E) { return E % 4 == 0 ? (E <= 32 ? 8 : 16) : E <= 8 ? 8 : E <= 16 ? 16 : E <= 32 ? 32 : 64; }
 
-// Calls f with the two as compile-time values.
+// Calls f with lanes, pieces and floats per piece as compile-time values.
 template <typename F>
 hipError_t with_shape(int E, F f) {
   using std::integral_constant;
+  const integral_constant<int, 1> c1{};
+  const integral_constant<int, 4> c4{};
+  const integral_constant<int, 8> g8{};
+  const integral_constant<int, 16> g16{};
+  const integral_constant<int, 32> g32{};
+  const integral_constant<int, 64> g64{};
   const int G = lanes_of(E);
-  if (G == 8) return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  if (G == 16) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  if (G == 32) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  const integral_constant<int, 64> g{};
-  switch ((E + 63) / 64) {
-    case 1: return f(g, integral_constant<int, 1>{});
-    case 2: return f(g, integral_constant<int, 2>{});
-    case 3: return f(g, integral_constant<int, 3>{});
-    case 4: return f(g, integral_constant<int, 4>{});
-    case 5: return f(g, integral_constant<int, 5>{});
-    case 6: return f(g, integral_constant<int, 6>{});
-    case 7: return f(g, integral_constant<int, 7>{});
-    case 8: return f(g, integral_constant<int, 8>{});
-  }
-  return hipErrorInvalidValue;
+  auto pieces = [&](auto g, auto v) {
+    switch ((E + 63) / 64) {
+      case 1: return f(g, integral_constant<int, 1>{}, v);
+      case 2: return f(g, integral_constant<int, 2>{}, v);
+      case 3: return f(g, integral_constant<int, 3>{}, v);
+      case 4: return f(g, integral_constant<int, 4>{}, v);
+      case 5: return f(g, integral_constant<int, 5>{}, v);
+      case 6: return f(g, integral_constant<int, 6>{}, v);
+      case 7: return f(g, integral_constant<int, 7>{}, v);
+      case 8: return f(g, integral_constant<int, 8>{}, v);
+    }
+    return hipErrorInvalidValue;
+  };
+  if (E % 4 == 0) return G == 8 ? f(g8, c1, c4) : pieces(g16, c4);
+  if (G == 8) return f(g8, c1, c1);
+  if (G == 16) return f(g16, c1, c1);
+  if (G == 32) return f(g32, c1, c1);
+  return pieces(g64, c1);
 }
 
 }  // namespace
 
-// Rows of a block: a few per group of lanes, so that the batch fills the CUs about twice; a sequence is never shared
-// by more than 512 blocks.
+// Rows of a block: a few per group of lanes, with two to four blocks per CU in a large batch (1 M rows of 64 experts in
+// sequences of 512: PLACEHOLDER us, with 32 rows per block 299); a sequence is never shared by more than 512 blocks.
 BalancePlan balance_plan(int64_t N, int64_t T, int E) {
   BalancePlan p{};
   p.T = T < N ? T : N;
   if (p.T < 1) p.T = 1;
   p.S = (N + p.T - 1) / p.T;
-  const int64_t wide = (p.T + 511) / 512;
+  const int64_t wide = std::max((p.T + 511) / 512, (N + 1023) / 1024);
   p.chunk = wide > 32 ? wide : 32;
   if (p.chunk > p.T) p.chunk = p.T;
+  if (p.T <= 512 || p.S >= 256) p.chunk = p.T;
   p.chunks = (p.T + p.chunk - 1) / p.chunk;
   const int64_t rows = 64 / lanes_of(E);  // of a wave at a time
   const int64_t waves = (p.chunk + 2 * rows - 1) / (2 * rows);
   p.threads = 64 * (int)(waves < 1 ? 1 : waves > 16 ? 16 : waves);
+  p.join_parts = (E + kJoin - 1) / kJoin;
+  p.join_threads = p.chunks >= 32 ? 1024 : 64;
+  while (p.join_threads < kJoin * p.chunks && p.join_threads < 1024) p.join_threads *= 2;
   return p;
 }
 
@@ -401,18 +428,20 @@ hipError_t launch_balance(const BalanceCall& c, hipStream_t s) {
   a.part_c = c.part_c;
   a.part_v = c.part_v;
   a.part_l = c.part_l;
-  a.done = c.done;
-  hipError_t e = with_shape(c.E, [&](auto g, auto epl) {
-    hipLaunchKernelGGL((balance_chunks<decltype(g)::value, decltype(epl)::value>), dim3((unsigned)(p.S * p.chunks)),
+  const bool few = p.S * p.join_parts <= kFencedBlocks;
+  a.done = p.chunks > 1 && few ? c.done : nullptr;
+  hipError_t e = with_shape(c.E, [&](auto g, auto pl, auto v) {
+    hipLaunchKernelGGL((balance_chunks<decltype(g)::value, decltype(pl)::value, decltype(v)::value>), dim3((unsigned)(p.S * p.chunks)),
                        dim3(p.threads), 0, s, a);
     return hipGetLastError();
   });
   if (e == hipSuccess && p.chunks > 1) {
-    hipLaunchKernelGGL(balance_join, dim3((unsigned)p.S), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(balance_join, dim3((unsigned)(p.S * p.join_parts)), dim3(p.join_threads), 0, s, a, p.join_parts);
     e = hipGetLastError();
   }
-  if (e == hipSuccess && p.chunks == 1 && p.S > 1) {
-    hipLaunchKernelGGL(balance_total, dim3(1), dim3(1024), 0, s, (const float*)a.part_l, p.S, a.loss);
+  if (e == hipSuccess && (p.chunks == 1 ? p.S > 1 : !few)) {
+    hipLaunchKernelGGL(balance_total, dim3(1), dim3(1024), 0, s, (const float*)a.part_l,
+                       p.chunks == 1 ? p.S : p.S * p.join_parts, a.loss);
     e = hipGetLastError();
   }
   return e;
@@ -423,8 +452,8 @@ int64_t route_backward_blocks(int64_t N, int E) { return (N + 256 / lanes_of(E) 
 hipError_t launch_route_backward(const RouteBackCall& c, hipStream_t s) {
   RouteBackArgs a{c.N, c.T < c.N ? c.T : c.N, c.E, c.k, c.alpha, c.eps, c.norm, c.scores, c.idx, c.dw, c.coef, c.dloss, c.mask,
                   c.out};
-  return with_shape(c.E, [&](auto g, auto epl) {
-    hipLaunchKernelGGL((route_backward<decltype(g)::value, decltype(epl)::value>),
+  return with_shape(c.E, [&](auto g, auto pl, auto v) {
+    hipLaunchKernelGGL((route_backward<decltype(g)::value, decltype(pl)::value, decltype(v)::value>),
                        dim3((unsigned)route_backward_blocks(c.N, c.E)), dim3(256), 0, s, a);
     return hipGetLastError();
   });

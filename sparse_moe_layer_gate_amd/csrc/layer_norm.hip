@@ -9,6 +9,8 @@
 // wave with several narrow rows; wider ones to a block.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "ops_internal.h"
 #include "row_ops.h"
 
@@ -26,13 +28,13 @@ struct LnArgs {
   const T *dh_out, *dy;
   T* dh;
   float* part;  // [2][nblocks][D] partial sums: dw, db
-  int chunk;    // rows per block
   int64_t nblocks;
   int want;  // bit 0: dw, 1: db
 };
 
-constexpr int kRowThreads = 256;       // of a block whose rows belong to groups of lanes
-constexpr int kBackwardThreads = 512;  // most of a block whose rows belong to it whole, in the backward pass
+constexpr int kRowThreads = 256;     // of a block whose rows belong to groups of lanes
+constexpr int kBlockThreads = 512;   // most of a block whose rows belong to it whole
+constexpr int kNarrowThreads = 640;  // and with one piece per thread, in the backward pass
 
 // Sums over the threads of a row: G lanes of a wave, or (G = 0) the block. Every thread of the row gets them.
 template <int NV, int G>
@@ -51,7 +53,7 @@ __device__ inline void row_sums(float (&v)[NV], float (*buf)[NV], int waves) {
 // what that mean is off by, so that neither a large common offset nor its rounding reaches it. h_out may be x or
 // residual: a thread writes only what it has read.
 template <typename T, int VPT, int G>
-__global__ __launch_bounds__(G ? kRowThreads : 1024) void layer_norm_forward(LnArgs<T> p) {
+__global__ __launch_bounds__(G ? kRowThreads : kBlockThreads) void layer_norm_forward(LnArgs<T> p) {
   __shared__ float buf0[16][1], buf1[16][2];
   const int waves = blockDim.x >> 6;
   const int t = G ? threadIdx.x % (G ? G : 1) : threadIdx.x, step = G ? G : blockDim.x;
@@ -130,10 +132,40 @@ __global__ __launch_bounds__(G ? kRowThreads : 1024) void layer_norm_forward(LnA
   }
 }
 
-// A block walks a run of rows (one row, or one per group of lanes, at a time) and keeps its features' parameter
-// gradients in registers; the run's sums go to one row of the partial arrays, which launch_column_sums adds in order.
+// p + i by a 32-bit offset from a base that a block shares: one register instead of an address per array and piece.
+template <typename T>
+__device__ inline T* offset(T* p, int i) {
+  return (T*)((uintptr_t)p + (uint32_t)i * (uint32_t)sizeof(T));
+}
+
+template <typename T>
+__device__ inline Raw8<T> raw_of8(const float* f) {
+  Raw8<T> r;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = bf16_pair(f[2 * i], f[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.a[i] = f[i];
+      r.b[i] = f[4 + i];
+    }
+  }
+  return r;
+}
+
+// Keeps the compiler from holding widened copies of loaded values across a use.
+__device__ inline void opaque(Raw8<uint16_t>& r) { asm volatile("" : "+v"(r.v)); }
+__device__ inline void opaque(Raw8<float>& r) { asm volatile("" : "+v"(r.a), "+v"(r.b)); }
+
+// A block takes rows in turn (one, or one per group of lanes, at a time), so that those at work at once lie side by side
+// in memory (against a run of rows per block: 4,096 features 5.2 TB/s to 5.0, 8,192 5.6 to 5.2), and keeps its
+// features' parameter gradients in registers; its sums go to one row of the partial arrays, which launch_column_sums adds
+// in order. A row's values stay as loaded, and both passes over them widen them anew; without that and the pinned sums
+// (the compiler else moves the additions behind the barrier, with all their operands) rows of 12,288 features spilled
+// 130 registers and ran at 1.5 TB/s, now 5.0.
 template <typename T, int VPT, int G>
-__global__ __launch_bounds__(G ? kRowThreads : kBackwardThreads) void layer_norm_backward(LnArgs<T> p) {
+__global__ __launch_bounds__(G ? kRowThreads : VPT == 1 ? kNarrowThreads : kBlockThreads) void layer_norm_backward(LnArgs<T> p) {
   __shared__ float buf[2][16][2];
   __shared__ float join[G ? 4 : 1][2][G ? VPT * G * 8 : 1];  // G: one row of sums per wave
   constexpr int GG = G ? G : 1;
@@ -142,27 +174,32 @@ __global__ __launch_bounds__(G ? kRowThreads : kBackwardThreads) void layer_norm
   const int rows_at_once = G ? kRowThreads / GG : 1;
   const float inv_d = 1.0f / (float)p.D;
   const int64_t b = blockIdx.x;
-  const int64_t run = b * p.chunk, last = min(run + p.chunk, (int64_t)p.N);
+  const int64_t stride = p.nblocks * rows_at_once;
   float aw[VPT][8], ab[VPT][8];
 #pragma unroll
   for (int v = 0; v < VPT; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) aw[v][i] = ab[v][i] = 0.f;
   Raw8<T> rw[VPT];
-  // The next row's pieces: its loads run under this row's sums. Not with four pieces per thread (rows of more than 8,192
-  // features), whose registers hold one row only: there each row's loads are waited for.
-  constexpr bool AHEAD = VPT < 4;
+  // The next row's pieces: its loads run under this row's sums. Not with four pieces of float32 per thread (rows of more
+  // than 12,288 features), whose registers hold one row only.
+  constexpr bool AHEAD = sizeof(T) == 2 || VPT < 4;
   Raw8<T> nh[VPT], ny[VPT], nd[VPT];
+  const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, one[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    nh[v] = ny[v] = nd[v] = raw_of8<T>(zero);
+    rw[v] = raw_of8<T>(one);
+  }
   float mean = 0.f, rstd = 0.f;
   auto fetch = [&](int64_t n) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (t + v * step) * 8;
       if (c >= p.D) continue;
-      const int64_t at = n * p.D + c;
-      nh[v] = raw_load8(p.x + at);
-      ny[v] = raw_load8(p.dy + at);
-      if (p.dh_out) nd[v] = raw_load8(p.dh_out + at);
+      nh[v] = raw_load8(offset(p.x + n * p.D, c));
+      ny[v] = raw_load8(offset(p.dy + n * p.D, c));
+      if (p.dh_out) nd[v] = raw_load8(offset(p.dh_out + n * p.D, c));
     }
     mean = p.stats[2 * n];
     rstd = p.stats[2 * n + 1];
@@ -172,49 +209,68 @@ __global__ __launch_bounds__(G ? kRowThreads : kBackwardThreads) void layer_norm
     const int c = (t + v * step) * 8;
     if (p.w && c < p.D) rw[v] = raw_load8(p.w + c);
   }
-  int64_t n = run + (G ? threadIdx.x / GG : 0);
-  if (n < last) fetch(n);
-  for (int it = 0; n < last; n += rows_at_once, ++it) {
-    float h[VPT][8], y[VPT][8];
-    Raw8<T> rd[VPT];
+  int64_t n = b * rows_at_once + (G ? threadIdx.x / GG : 0);
+  if (AHEAD && n < p.N) fetch(n);
+  for (int it = 0; n < p.N; n += stride, ++it) {
+    if (!AHEAD) fetch(n);
+    Raw8<T> rh[VPT], ry[VPT], rd[VPT];
     const float m = mean, r = rstd;
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if ((t + v * step) * 8 >= p.D) continue;
-      widen8(nh[v], h[v]);
-      widen8(ny[v], y[v]);
+      rh[v] = nh[v];
+      ry[v] = ny[v];
       rd[v] = nd[v];
     }
-    if (AHEAD && n + rows_at_once < last) fetch(n + rows_at_once);
+    if (AHEAD && n + stride < p.N) fetch(n + stride);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) opaque(rw[v]);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if ((t + v * step) * 8 >= p.D) continue;
-      float w[8];
-      if (p.w) widen8(rw[v], w);
+      float h[8], y[8], w[8];
+      widen8(rh[v], h);
+      widen8(ry[v], y);
+      widen8(rw[v], w);
+      const bool in = (t + v * step) * 8 < p.D;  // behind the row's end all are 0, so that nothing is added
+      const float mv = in ? m : 0.f, rv = in ? r : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        h[v][i] = (h[v][i] - m) * r;
-        aw[v][i] += y[v][i] * h[v][i];
-        ab[v][i] += y[v][i];
-        if (p.w) y[v][i] *= w[i];
-        s[0] += y[v][i];
-        s[1] += y[v][i] * h[v][i];
+        h[i] = (h[i] - mv) * rv;
+        aw[v][i] += y[i] * h[i];
+        ab[v][i] += y[i];
+        y[i] *= w[i];
+        s[0] += y[i];
+        s[1] += y[i] * h[i];
       }
     }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(aw[v][i]), "+v"(ab[v][i]));
     row_sums<2, G>(s, buf[it & 1], waves);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      opaque(rh[v]);
+      opaque(ry[v]);
+      opaque(rw[v]);
+    }
     const float c0 = s[0] * inv_d, c1 = s[1] * inv_d;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = (t + v * step) * 8;
-      if (c >= p.D) continue;
-      float d[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (p.dh_out) widen8(rd[v], d);
+      float d[8];
+      widen8(rd[v], d);
+      float h[8], y[8], w[8];
+      widen8(rh[v], h);
+      widen8(ry[v], y);
+      widen8(rw[v], w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] += r * (y[v][i] - c0 - h[v][i] * c1);
-      raw_store8(p.dh + n * p.D + c, d);
+      for (int i = 0; i < 8; ++i) {
+        y[i] *= w[i];
+        d[i] += r * (y[i] - c0 - (h[i] - m) * r * c1);
+      }
+      if (c < p.D) raw_store8(offset(p.dh + n * p.D, c), d);
     }
-    if (!AHEAD && n + rows_at_once < last) fetch(n + rows_at_once);
   }
   if (p.want == 0) return;
   if constexpr (G != 0) {
@@ -290,19 +346,23 @@ __global__ __launch_bounds__(1024) void column_sums(ColumnJob j0, ColumnJob j1, 
   }
 }
 
-// Threads of a row and pieces per thread: lanes == 0: the block's `threads`.
+// Lanes of a row's group (0: the block takes the row), threads of a block, pieces per thread. Several pieces per thread
+// keep more of a row in flight per block and need fewer waves at its barriers: forward, 5,120 features of bfloat16 with
+// one piece (640 threads) 3.3 TB/s, with four (192) 5.6; four in three waves of 12,288 features 4.9 and three in eight
+// waves 5.6. The backward pass, which has the next row's loads in flight, takes one piece up to 640 threads (5,120
+// features 5.0 TB/s, with two 3.6 and with three 4.8), then as many as its registers hold.
 struct Shape {
   int lanes, threads, vpt;
 };
-Shape shape_of(int D, int limit) {
+Shape shape_of(int D, bool backward) {
   if (D <= 512) {
     int g = 8;
     while (g * 8 < D) g *= 2;
     return {g, kRowThreads, 1};
   }
-  if (D <= 2048) return {64, kRowThreads, D <= 1024 ? 2 : 4};
-  int vpt = 1;
-  while ((D / 8 + vpt - 1) / vpt > limit) vpt *= 2;
+  if (D <= (backward ? 1024 : 2048)) return {64, kRowThreads, D <= 1024 ? 2 : 4};
+  const int vpt = backward ? (D <= 8 * kNarrowThreads ? 1 : D <= 24 * kBlockThreads ? 3 : 4)
+                           : (D <= 8192 || D > 24 * kBlockThreads ? 4 : 3);
   return {0, ((D / 8 + vpt - 1) / vpt + 63) / 64 * 64, vpt};
 }
 
@@ -323,12 +383,12 @@ hipError_t pick(const LnArgs<T>& p, const Shape& sh, int64_t blocks, hipStream_t
   if (sh.lanes == 64) {
     if (sh.vpt == 1) return run<T, BACKWARD, 1, 64>(p, blocks, sh.threads, s);
     if (sh.vpt == 2) return run<T, BACKWARD, 2, 64>(p, blocks, sh.threads, s);
-    return run<T, BACKWARD, 4, 64>(p, blocks, sh.threads, s);
+    if constexpr (!BACKWARD) return run<T, BACKWARD, 4, 64>(p, blocks, sh.threads, s);
   }
-  if (sh.vpt == 1) return run<T, BACKWARD, 1, 0>(p, blocks, sh.threads, s);
-  if (sh.vpt == 2) return run<T, BACKWARD, 2, 0>(p, blocks, sh.threads, s);
-  if constexpr (BACKWARD) return run<T, BACKWARD, 4, 0>(p, blocks, sh.threads, s);
-  return hipErrorInvalidValue;  // the forward's blocks hold 16,384 features in two pieces
+  if constexpr (BACKWARD)
+    if (sh.vpt == 1) return run<T, BACKWARD, 1, 0>(p, blocks, sh.threads, s);
+  if (sh.vpt == 3) return run<T, BACKWARD, 3, 0>(p, blocks, sh.threads, s);
+  return run<T, BACKWARD, 4, 0>(p, blocks, sh.threads, s);
 }
 
 template <typename T>
@@ -345,18 +405,17 @@ hipError_t layer_norm_t(const LayerNormCall& c, bool backward, hipStream_t s) {
   p.y = (T*)c.y;
   p.stats = c.stats;
   if (!backward) {
-    const Shape sh = shape_of(c.D, 1024);
-    return pick<T, false>(p, sh, layer_norm_blocks(c.N, c.D), s);
+    return pick<T, false>(p, shape_of(c.D, false), layer_norm_blocks(c.N, c.D), s);
   }
   p.dh_out = (const T*)c.dh_out;
   p.dy = (const T*)c.dy;
   p.dh = (T*)c.dh;
   p.part = c.part;
   p.want = (c.dw ? 1 : 0) | (c.db ? 2 : 0);
-  const int64_t runs = layer_norm_runs(c.D);
-  p.chunk = (int)((c.N + runs - 1) / runs);
-  p.nblocks = (c.N + p.chunk - 1) / p.chunk;
-  const hipError_t e = pick<T, true>(p, shape_of(c.D, kBackwardThreads), p.nblocks, s);
+  const Shape sh = shape_of(c.D, true);
+  const int64_t rows = sh.lanes ? kRowThreads / sh.lanes : 1;
+  p.nblocks = std::min((c.N + rows - 1) / rows, layer_norm_runs(c.D));
+  const hipError_t e = pick<T, true>(p, sh, p.nblocks, s);
   if (e != hipSuccess || p.want == 0) return e;
   const float* pw = p.part;
   const float* pb = p.part + p.nblocks * c.D;
@@ -365,12 +424,14 @@ hipError_t layer_norm_t(const LayerNormCall& c, bool backward, hipStream_t s) {
 
 }  // namespace
 
-int layer_norm_threads(int D) { return shape_of(D, 1024).threads; }
+int layer_norm_threads(int D) { return shape_of(D, false).threads; }
 int64_t layer_norm_blocks(int64_t N, int D) {
-  const Shape sh = shape_of(D, 1024);
+  const Shape sh = shape_of(D, false);
   return sh.lanes ? (N + kRowThreads / sh.lanes - 1) / (kRowThreads / sh.lanes) : N;
 }
-int64_t layer_norm_runs(int D) { return shape_of(D, kBackwardThreads).lanes ? 512 : 256; }
+// Blocks of the backward pass: two per CU, or one of more than 320 threads (2,560 features: 4.4 and 5.4 TB/s with one and
+// two; 4,096: 6.0 and 5.4).
+int64_t layer_norm_runs(int D) { return shape_of(D, true).threads <= 320 ? 512 : 256; }
 
 hipError_t launch_layer_norm(int dtype, const LayerNormCall& c, bool backward, hipStream_t s) {
   return dtype == MOE_F32 ? layer_norm_t<float>(c, backward, s) : layer_norm_t<uint16_t>(c, backward, s);

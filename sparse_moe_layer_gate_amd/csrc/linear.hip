@@ -760,57 +760,71 @@ hipError_t linear_t(const LinearCall& c, const LinearPlan& p, hipStream_t s) {
 
 // ---- the gradients of the epilogue ----
 //
-// Eight columns per thread; the four waves of a block take rows in turn of a run of kBackRows, and the run's column sums
-// go to one row of the partial array, which launch_column_sums adds in order.
-constexpr int kBackRows = 64;
+// Eight columns per thread, up to 64 lanes per row, several rows per wave where the rows are narrower. A block takes every
+// runs-th piece of the rows, four rows of a lane in flight; its column sums go to one row of the partial array, which
+// launch_column_sums adds in order.
+// 65,536 x 2,048 in bfloat16: 179 us, with twice the blocks 213; 131,072 x 1,024 in float32 354 and 396.
+constexpr int kBackBlocks = 1024;
+
+int back_lanes(int M) {
+  int lanes = 1;
+  while (lanes < 64 && lanes * 8 < M) lanes *= 2;
+  return lanes;
+}
+
+// Rows of a piece: a step of the block, four rows of each lane.
+__host__ __device__ inline int back_rows(int lanes) { return 1024 / lanes; }
 
 template <typename T>
 __global__ __launch_bounds__(256) void linear_back(int64_t R, int M, int act, const T* dy, const T* z, T* dz, float* part,
-                                                   int64_t runs) {
+                                                   int64_t runs, int lanes) {
   __shared__ float join[4][512];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wave = threadIdx.x >> 6, rows = 256 / lanes, piece = back_rows(lanes);  // rows at a time, of a piece
   const int64_t run = blockIdx.x % runs;
-  const int col = (int)(blockIdx.x / runs) * 512 + lane * 8;
-  const int64_t first = run * kBackRows, last = min(first + kBackRows, R);
+  const int first_col = (int)(blockIdx.x / runs) * 512, c8 = (threadIdx.x & (lanes - 1)) * 8, col = first_col + c8;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (col < M) {
-    for (int64_t n = first + wave; n < last; n += 16) {
+    for (int64_t n = run * piece + threadIdx.x / lanes; n < R; n += runs * piece) {
       Raw8<T> rd[4], rz[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (n + 4 * u < last) {
-          rd[u] = raw_load8(dy + (n + 4 * u) * M + col);
-          if (act != MOE_ACT_NONE) rz[u] = raw_load8(z + (n + 4 * u) * M + col);
+        if (n + u * rows < R) {
+          rd[u] = raw_load8(dy + (n + u * rows) * M + col);
+          if (act != MOE_ACT_NONE) rz[u] = raw_load8(z + (n + u * rows) * M + col);
         }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (n + 4 * u < last) {
+        if (n + u * rows < R) {
           float d[8], v[8];
           widen8(rd[u], d);
           if (act != MOE_ACT_NONE) {
             widen8(rz[u], v);
             act_slope_times<std::is_same<T, uint16_t>::value, 8>(act, v, d);
           }
-          if (dz) raw_store8<false>(dz + (n + 4 * u) * M + col, d);
+          if (dz) raw_store8<false>(dz + (n + u * rows) * M + col, d);
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum[i] += d[i];
         }
     }
   }
   if (!part) return;
-  raw_store8<false>(&join[wave][lane * 8], sum);
+  for (int off = lanes; off < 64; off <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += __shfl_xor(sum[i], off);
+  }
+  if ((threadIdx.x & 63) < lanes) raw_store8<false>(&join[wave][c8], sum);
   __syncthreads();
   for (int c = threadIdx.x; c < 512; c += 256) {
-    const int at = (int)(blockIdx.x / runs) * 512 + c;
-    if (at < M) part[run * M + at] = ((join[0][c] + join[1][c]) + join[2][c]) + join[3][c];
+    if (first_col + c < M) part[run * M + first_col + c] = ((join[0][c] + join[1][c]) + join[2][c]) + join[3][c];
   }
 }
 
 template <typename T>
 hipError_t linear_back_t(const LinearBackCall& c, hipStream_t s) {
-  const int64_t runs = linear_back_runs(c.R);
+  const int64_t pieces = (c.R + back_rows(back_lanes(c.out)) - 1) / back_rows(back_lanes(c.out));
+  const int64_t most = linear_back_runs(c.R, c.out), each = (pieces + most - 1) / most, runs = (pieces + each - 1) / each;
   hipLaunchKernelGGL(linear_back<T>, dim3((unsigned)(runs * ((c.out + 511) / 512))), dim3(256), 0, s, c.R, c.out, c.act,
-                     (const T*)c.dy, (const T*)c.z, (T*)c.dz, c.dbias ? c.part : nullptr, runs);
+                     (const T*)c.dy, (const T*)c.z, (T*)c.dz, c.dbias ? c.part : nullptr, runs, back_lanes(c.out));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !c.dbias) return e;
   return launch_column_sums(c.part, c.dbias, nullptr, nullptr, runs, c.out, s);
@@ -819,7 +833,11 @@ hipError_t linear_back_t(const LinearBackCall& c, hipStream_t s) {
 }  // namespace
 
 int64_t linear_join_blocks(int64_t R, int out) { return (R * (out / 8) + 255) / 256; }
-int64_t linear_back_runs(int64_t R) { return (R + kBackRows - 1) / kBackRows; }
+int64_t linear_back_runs(int64_t R, int out) {
+  const int64_t columns = (out + 511) / 512, most = std::max<int64_t>(64, kBackBlocks / columns);
+  const int piece = back_rows(back_lanes(out));
+  return std::min((R + piece - 1) / piece, most);
+}
 
 namespace {
 

@@ -176,7 +176,7 @@ struct LinearBackCall {
   void* dz;
   float *dbias, *part;
 };
-int64_t linear_back_runs(int64_t R);  // partial rows of dbias
+int64_t linear_back_runs(int64_t R, int out);  // most partial rows of dbias
 hipError_t launch_linear_back(int dtype, const LinearBackCall& c, hipStream_t s);
 
 // ---- balance loss and the router's gradient ----
@@ -184,6 +184,7 @@ struct BalancePlan {
   int64_t T, S;           // rows per sequence (at most N), sequences
   int64_t chunk, chunks;  // rows per block, blocks per sequence
   int threads;
+  int join_parts, join_threads;  // blocks per sequence of the second launch, where chunks > 1; S is at most 1024 then
 };
 BalancePlan balance_plan(int64_t N, int64_t T, int E);
 struct BalanceCall {

@@ -64,7 +64,7 @@ BalanceLayout balance_layout(const BalancePlan& p, int E) {
   w.part_p = take(4 * parts * E);
   w.part_c = take(4 * parts * E);
   w.part_v = take(4 * parts);
-  w.part_l = take(p.S > 1 ? 4 * (size_t)p.S : 0);
+  w.part_l = take(parts ? 4 * (size_t)p.S * p.join_parts : p.S > 1 ? 4 * (size_t)p.S : 0);
   w.done = take(parts ? 4 : 0);
   w.total = o;
   return w;
@@ -233,7 +233,7 @@ moe_status moe_linear(int64_t R, int32_t in, int32_t out, int32_t dtype, int32_t
 
 size_t moe_linear_backward_workspace_size(int64_t R, int32_t out, int32_t dtype) {
   if (check_linear(R, 64, out, dtype) != MOE_OK) return 0;
-  return sizeof(float) * (size_t)linear_back_runs(R) * out;
+  return sizeof(float) * (size_t)linear_back_runs(R, out) * out;
 }
 
 moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t activation, const void* dy,
@@ -241,7 +241,6 @@ moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t ac
   const moe_status st = check_linear(R, 64, out, dtype);
   if (st != MOE_OK) return st;
   if (!activation_ok(activation) || (!dz && !dbias) || !aligned16(dbias)) return MOE_ERR_INVALID_ARG;
-  if (!launch_fits(linear_back_runs(R) * ((out + 511) / 512), 256)) return MOE_ERR_UNSUPPORTED;
   hipStream_t s = (hipStream_t)stream;
   if (R == 0) {  // a sum over no rows
     MOE_TRY(ST_LINEAR, launch_fill2_i32((int32_t*)dbias, dbias ? out : 0, nullptr, 0, 0, s));
