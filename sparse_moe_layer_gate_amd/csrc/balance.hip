@@ -69,7 +69,7 @@ __device__ inline float block_total(float v, float* buf) {
 
 // The scores of a row lie with a group of G lanes: piece i of lane j holds the V experts from V (j + G i) on, one load of V
 // floats. V = 4 needs E to be a multiple of 4; 16 lanes then take a row of up to 64 experts in one load and a wave four
-// rows (one row of 64 lanes and single floats: 1 M rows of 64 experts, gradient 407 us against PLACEHOLDER).
+// rows (one row of 64 lanes and single floats: 1 M rows of 64 experts, gradient 407 us, so 140).
 template <int G, int PL, int V>
 struct Row {
   static constexpr int N = PL * V;  // values per lane
@@ -172,12 +172,14 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
 }
 
 // The chunks of one sequence, in order: a block takes kJoin experts, up to 32 lanes each, so that few of its loads wait
-// for one another (512 chunks of 256 experts: 4 rounds of PLACEHOLDER). Of a few blocks the one that
-// ends last adds their shares of the loss, in order; many would wait for their fences (512 blocks: 40 us).
-constexpr int kJoin = 32, kFencedBlocks = 128;
+// for one another (32,768 x 256 in one sequence: 27 -> 24 us). Of a few blocks the one that
+// ends last adds their shares of the loss, in order (0.5 us less than one more launch); more take balance_total, since they
+// would wait at the count (512 blocks: 25 us for 21).
+constexpr int kJoin = 32, kCountedBlocks = 128;
+static_assert(kJoin == 32, "two lanes of every expert per wave");
 __global__ __launch_bounds__(1024) void balance_join(BalanceArgs a, int parts) {
-  __shared__ float sp[1024];
-  __shared__ int32_t sc[1024];
+  __shared__ float sp[16][kJoin];
+  __shared__ int32_t sc[16][kJoin];
   __shared__ int32_t sv[16];
   __shared__ float buf[16];
   __shared__ int last;
@@ -204,32 +206,43 @@ __global__ __launch_bounds__(1024) void balance_join(BalanceArgs a, int parts) {
       }
     }
   }
-  sp[threadIdx.x] = p;
-  sc[threadIdx.x] = c;
+  // the two lanes of a wave, then the waves
+  const int waves = blockDim.x >> 6, wave = threadIdx.x >> 6;
+  p += __shfl_xor(p, kJoin);
+  c += __shfl_xor(c, kJoin);
+  if ((threadIdx.x & 63) < kJoin) {
+    sp[wave][threadIdx.x % kJoin] = p;
+    sc[wave][threadIdx.x % kJoin] = c;
+  }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off);
-  if ((threadIdx.x & 63) == 0) sv[threadIdx.x >> 6] = v;
+  if ((threadIdx.x & 63) == 0) sv[wave] = v;
   __syncthreads();
   float loss = 0.f;
   if (threadIdx.x < kJoin && e < a.E) {
-    for (int i = 1; i < lanes; ++i) {
-      p += sp[i * kJoin + threadIdx.x];
-      c += sc[i * kJoin + threadIdx.x];
-    }
-    v = 0;
-    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) v += sv[w];
+    v = sv[0];
+#pragma unroll
+    for (int w = 1; w < 16; ++w)
+      if (w < waves) {
+        p += sp[w][threadIdx.x];
+        c += sc[w][threadIdx.x];
+        v += sv[w];
+      }
     loss = finish_expert(a, q, e, p, c, v);
   }
   if (threadIdx.x < 64) loss = wave_sum(loss);
-  if (threadIdx.x == 0) a.part_l[blockIdx.x] = loss;
-  if (!a.done) return;
   if (threadIdx.x == 0) {
-    __threadfence();  // before the count, so that the block that sees it full sees every share
-    last = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
+    // the one value that another block reads goes past the caches of this XCD and is there before the count rises; a fence
+    // would write back all that they hold (9.4 us for the launch at 8,192 x 256 in sequences of 1,024, 5.8 without)
+    __hip_atomic_store(a.part_l + blockIdx.x, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (a.done) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+    }
   }
+  if (!a.done) return;
   __syncthreads();
   if (!last) return;
-  __threadfence();
   float s = 0.f;
   for (int64_t i = threadIdx.x; i < gridDim.x; i += blockDim.x)
     s += __hip_atomic_load(a.part_l + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -387,7 +400,8 @@ hipError_t with_shape(int E, F f) {
 }  // namespace
 
 // Rows of a block: a few per group of lanes, with two to four blocks per CU in a large batch (1 M rows of 64 experts in
-// sequences of 512: PLACEHOLDER us, with 32 rows per block 299); a sequence is never shared by more than 512 blocks.
+// sequences of 512: 57 us, with 32 rows per block 299); one block takes a sequence of up to 512 rows or of
+// 256 and more sequences (65,536 x 256 in sequences of 512: 17 us, with 64 rows per block 42); a sequence is never shared by more than 512 blocks.
 BalancePlan balance_plan(int64_t N, int64_t T, int E) {
   BalancePlan p{};
   p.T = T < N ? T : N;
@@ -428,7 +442,7 @@ hipError_t launch_balance(const BalanceCall& c, hipStream_t s) {
   a.part_c = c.part_c;
   a.part_v = c.part_v;
   a.part_l = c.part_l;
-  const bool few = p.S * p.join_parts <= kFencedBlocks;
+  const bool few = p.S * p.join_parts <= kCountedBlocks;
   a.done = p.chunks > 1 && few ? c.done : nullptr;
   hipError_t e = with_shape(c.E, [&](auto g, auto pl, auto v) {
     hipLaunchKernelGGL((balance_chunks<decltype(g)::value, decltype(pl)::value, decltype(v)::value>), dim3((unsigned)(p.S * p.chunks)),
