@@ -330,9 +330,10 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
       }
       total = group_sum<G>(total) + a.eps;
       dot = group_sum<G>(dot);
-      const float r = total != 0.f ? 1.0f / total : 0.f;
+      // divided, not multiplied by a rounded reciprocal: with one slot the two terms are equal
+      const float mean = total != 0.f ? dot / total : 0.f, scale = total != 0.f ? a.alpha / total : 0.f;
 #pragma unroll
-      for (int m = 0; m < SPL; ++m) w[m] = a.alpha * r * (w[m] - dot * r);
+      for (int m = 0; m < SPL; ++m) w[m] = scale * (w[m] - mean);
     } else {
 #pragma unroll
       for (int m = 0; m < SPL; ++m) w[m] *= a.alpha;
@@ -400,8 +401,9 @@ hipError_t with_shape(int E, F f) {
 }  // namespace
 
 // Rows of a block: a few per group of lanes, with two to four blocks per CU in a large batch (1 M rows of 64 experts in
-// sequences of 512: 57 us, with 32 rows per block 299); one block takes a sequence of up to 512 rows or of
-// 256 and more sequences (65,536 x 256 in sequences of 512: 17 us, with 64 rows per block 42); a sequence is never shared by more than 512 blocks.
+// sequences of 512: 57 us, with 32 rows per block 299). One block takes a sequence of up to 512 rows, or one of 256
+// sequences and more (65,536 x 256 in sequences of 512: 17 us, with 64 rows per block 42). A sequence is never shared by
+// more than 512 blocks.
 BalancePlan balance_plan(int64_t N, int64_t T, int E) {
   BalancePlan p{};
   p.T = T < N ? T : N;
