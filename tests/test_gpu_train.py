@@ -37,9 +37,11 @@ def rand(g, *shape, std=1.0, mean=0.0, dtype=F32):
 
 # ---------------------------------------------------------------- layer norm
 LN_CASES = [
-    # N, D: one row and many, every width of a group of lanes, its edges, two and four pieces, blocks of one to four
+    # N, D: one row and many, every width of a group of lanes, its edges, two and four pieces, blocks of one to four;
+    # more rows than the backward pass takes at once
     (1, 8), (3, 56), (700, 64), (33, 72), (257, 128), (130, 136), (65, 256), (9, 264), (70, 512), (5, 520), (31, 1024),
     (6, 1032), (40, 2048), (3, 2056), (300, 2560), (1, 6144), (7, 8192), (4, 8200), (2, 16384), (1500, 40),
+    (17000, 64), (2100, 1024), (1100, 2560), (600, 5120), (530, 5128), (300, 12288), (270, 12296), (260, 16384),
 ]
 
 
@@ -240,6 +242,22 @@ def test_linear_backward(R_, M, dtype):
         assert torch.equal(over_dy, dz) and torch.equal(over_z, dz) and torch.equal(db2, db)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R_,M,act", [(66000, 128, "gelu"), (1100, 12296, "silu"), (1050000, 8, "gelu_tanh")])
+def test_linear_backward_more_rows_than_at_once(R_, M, act, dtype):
+    dt = TYPES[dtype]
+    print(f"[linear backward] R={R_} M={M} {dtype}", flush=True)
+    g = gen(R_ + M)
+    dy, z = rand(g, R_, M, dtype=dt), rand(g, R_, M, std=2.0, dtype=dt)
+    ws = workspace(moe.moe_linear_backward_workspace_size(R_, M, dtype))
+    dz, db = torch.empty((R_, M), dtype=dt, device="cuda"), torch.empty(M, device="cuda")
+    moe.moe_linear_backward(dev(dy), dev(z), dz, db, ws, act=act)
+    torch.cuda.synchronize()
+    ref, bound = R.linear_backward(f64(dy), f64(z), act, dt)
+    check("dz", dz, ref[0], bound[0])
+    check("dbias", db, ref[1], bound[1])
+
+
 # ---------------------------------------------------------------- balance loss and the router's gradient
 def routed(g, N, E, k, empty=0.0, twice=False):
     logits = torch.randn((N, E), generator=g) * 2.0
@@ -310,6 +328,54 @@ def test_balance(N, E, k, T):
         over = dev(scores)
         moe.moe_route_backward(cfg, N, over, dev(idx), dev(dw), over, **args)
         assert torch.equal(over, out)
+
+
+@pytest.mark.parametrize("N,E,k,T", [
+    # one sequence of many blocks; few and many sequences of several; 256 of one block each; single floats, wide and narrow
+    (40000, 64, 6, 40000), (40000, 64, 6, 1024), (70000, 256, 8, 1024), (30000, 60, 4, 100), (20000, 6, 2, 600),
+    (20000, 130, 8, 3000), (9000, 512, 8, 9000), (300000, 8, 2, 1000), (270000, 32, 12, 270000),
+])
+def test_balance_many_rows(N, E, k, T):
+    print(f"[balance] N={N} E={E} k={k} T={T}", flush=True)
+    g = gen(N + E)
+    scores, idx = routed(g, N, E, k, empty=0.1)
+    mask = torch.rand(N, generator=g) < 0.8
+    S, weight, alpha = (N + T - 1) // T, 0.01, 2.5
+    cfg = moe.make_config(64, E, 1, 1, k, 64, alpha=alpha)
+    counts = torch.full((S, E), -1, dtype=torch.int32, device="cuda")
+    coef, loss, out = torch.empty((S, E), device="cuda"), torch.empty(1, device="cuda"), torch.empty((N, E), device="cuda")
+    ws = workspace(moe.moe_balance_workspace_size(cfg, N, T))
+    moe.moe_balance_loss(cfg, N, dev(scores), dev(idx), T, weight, counts, coef, loss, ws, token_mask=dev(mask))
+    dw = rand(g, N, k)
+    moe.moe_route_backward(cfg, N, dev(scores), dev(idx), dev(dw), out, seq_rows=T, coef=coef, token_mask=dev(mask))
+    torch.cuda.synchronize()
+    s, seq, live = f64(scores), torch.arange(N) // T, mask.double()
+    V = torch.zeros(S, dtype=torch.float64).index_add_(0, seq, live).clamp_min(1)[:, None]
+    ok = (idx >= 0) & (idx < E)
+    i = torch.where(ok, idx, 0).long()
+    hit = torch.zeros((N, E), dtype=torch.float64).scatter_add_(1, i, ok.double()) * live[:, None]
+    c = torch.zeros((S, E), dtype=torch.float64).index_add_(0, seq, hit)
+    total = s.sum(1, keepdim=True)
+    P = torch.zeros((S, E), dtype=torch.float64).index_add_(0, seq, s / total * live[:, None])
+    f = E * c / (k * V)
+    assert torch.equal(counts.cpu().double(), c)
+    ref = (weight / S * (f * P / V).sum()).view(1)
+    check("loss", loss, ref, (T + E + S + 200) * R.U * ref.abs())
+    check("coef", coef, weight / S * f / V, 8 * R.U * (weight / S * f / V))
+    # the gradient, from the float32 coef: each of its sums has at most E or k terms
+    w = f64(dw) * ok
+    sw = s.gather(1, i) * ok
+    D = sw.sum(1, keepdim=True) + 1e-20
+    mean = (w * sw).sum(1, keepdim=True) / D
+    back = alpha / D * (w - mean) * ok
+    ds = torch.zeros_like(s).scatter_add_(1, i, back)
+    mag = torch.zeros_like(s).scatter_add_(1, i, alpha / D * (w.abs() + (w.abs() * sw).sum(1, keepdim=True) / D) * ok)
+    co = f64(coef.cpu())[seq]
+    pull = (co * s).sum(1, keepdim=True) / total
+    ds += live[:, None] * (co - pull) / total
+    mag += live[:, None] * (co + pull) / total
+    d = s * (1 - s)
+    check("dlogits", out, ds * d, ((2 * E + 40) * mag * d + 2 * ds.abs() * s) * R.U)
 
 
 def test_route_backward_dead_token_without_scores():
