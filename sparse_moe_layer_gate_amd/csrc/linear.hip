@@ -6,7 +6,7 @@
 //  - linear_few (both types, up to 16 rows): a stream of W, the reduction split over a block's waves;
 //  - linear_w8 (bfloat16, many rows): 256 x 256 tiles on the eight-wave K loop of the expert GEMMs (gemm_w8.h), a
 //    static walk over the tiles, one block per CU;
-//  - linear_tile (both types): 64 to 256 rows x 64 or 128 columns, the reduction split over blocks where the tiles alone
+//  - linear_tile (both types): 64 rows (bfloat16: to 256) x 64 or 128 columns, the reduction split over blocks where the tiles alone
 //    would not fill the CUs; linear_join then adds the parts in order and runs the epilogue.
 #include <hip/hip_runtime.h>
 
@@ -750,9 +750,9 @@ hipError_t linear_t(const LinearCall& c, const LinearPlan& p, hipStream_t s) {
       return hipGetLastError();
     }
     if (p.bm == 256) e = run_tile<T, 256, 128>(a, s);
+    if (p.bm == 128) e = run_tile<T, 128, 128>(a, s);
   }
   if (p.bm == 64) e = p.bn == 64 ? run_tile<T, 64, 64>(a, s) : run_tile<T, 64, 128>(a, s);
-  if (p.bm == 128) e = run_tile<T, 128, 128>(a, s);
   if (e != hipSuccess || p.splits == 1) return e;
   hipLaunchKernelGGL(linear_join<T>, dim3((unsigned)linear_join_blocks(c.R, c.out)), dim3(256), 0, s, a);
   return hipGetLastError();
@@ -857,9 +857,9 @@ struct TileCost {
 };
 constexpr TileCost kTiles[] = {{64, 64, 2.0, {0.27, 0.54}},
                                {64, 128, 2.0, {0.43, 0.96}},
-                               {128, 128, 3.0, {0.49, 1.86}},
+                               {128, 128, 3.0, {0.49, 0}},
                                {256, 128, 3.7, {0.68, 0}},
-                               {256, 256, 3.6, {1.18, 0}}};  // bfloat16 only: step 0
+                               {256, 256, 3.6, {1.18, 0}}};  // step 0: bfloat16 only (two blocks of 64 rows do as much)
 constexpr double kTwoBlocks = 1.75;  // a step of two 64-row blocks on one CU over that of one
 
 double tile_cost(const TileCost& c, bool f32, int64_t tiles, int64_t R, int in, int out, int splits) {

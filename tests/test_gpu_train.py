@@ -121,6 +121,9 @@ LINEAR_CASES = [
     # R, in, out: one row to every height of tile, odd rows and widths, split and whole reductions
     (1, 64, 8), (1, 1024, 136), (1, 4096, 264), (16, 2048, 128), (17, 512, 72), (32, 1024, 1000), (33, 320, 256), (64, 1536, 40),
     (65, 640, 136), (128, 2048, 264), (129, 1024, 520), (257, 256, 128), (300, 3008, 64), (1000, 192, 384),
+    # tiles of 64 to 256 rows and 64 or 128 columns (256 columns: below), each with one part of the reduction and several
+    (66, 64, 8304), (17, 1280, 5472), (145, 256, 11000), (66, 1792, 8352), (325, 64, 11208), (133, 3456, 5528),
+    (132, 64, 10960), (18, 768, 11016),
 ]
 
 
@@ -176,6 +179,65 @@ def test_linear_exact(R_, K, M, dtype):
     torch.cuda.synchronize()
     ref = x.float() @ w.float().t() + bias.float()  # exact in float32
     assert torch.equal(z.cpu(), ref.to(dt)) and torch.equal(y.cpu(), torch.relu(ref).to(dt))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R_", [3, 40])
+def test_linear_longest_reduction(R_, dtype):
+    """2^22 features: signs, whose sums float32 holds exactly."""
+    K, M, dt = 1 << 22, 504, TYPES[dtype]
+    g = torch.Generator(device="cuda").manual_seed(6)
+
+    def signs(n):
+        t = torch.empty((n, K), dtype=dt, device="cuda")
+        for i in range(0, n, 64):
+            t[i:i + 64] = torch.randint(0, 2, t[i:i + 64].shape, generator=g, device="cuda", dtype=torch.int8) * 2 - 1
+        return t
+    x, w = signs(R_), signs(M)
+    y = torch.empty((R_, M), dtype=dt, device="cuda")
+    moe.moe_linear(x, w, y, workspace(moe.moe_linear_workspace_size(R_, K, M, dtype)))
+    for rows in (slice(0, 8), slice(M - 8, M)):
+        ref = sum(x[:, i:i + (1 << 20)].double() @ w[rows, i:i + (1 << 20)].double().t() for i in range(0, K, 1 << 20))
+        assert torch.equal(y[:, rows], ref.to(dt))
+
+
+def test_gradients_by_differences():
+    """Layer norm's and every activation's gradients against central differences of the float64 formulas: off by h^2 of the
+    third derivative and by the rounding of a sum of about 100 over h, both below 1e-6, and by float32's 1e-5."""
+    N, D, h, g = 3, 24, 1e-5, gen(12)
+    x, w, b, dy, dv = rand(g, N, D), 1 + rand(g, D, std=0.2), rand(g, D), rand(g, N, D), rand(g, N, D)
+    y, stats, dh = torch.empty((N, D), device="cuda"), torch.empty((N, 2), device="cuda"), torch.empty((N, D), device="cuda")
+    dw, db = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    moe.moe_layer_norm(N, dev(x), None, dev(w), dev(b), None, y, stats)
+    moe.moe_layer_norm_backward(N, dev(x), stats, dev(w), dev(dv), dev(dy), dh, dw, db,
+                                workspace(moe.moe_layer_norm_workspace_size(N, D, "f32")))
+
+    def differences(f, args, i):
+        out = torch.empty_like(args[i])
+        for j in range(out.numel()):
+            d = []
+            for sign in (1, -1):
+                a = [t.clone() for t in args]
+                a[i].view(-1)[j] += sign * h
+                d.append(float(f(*a)))
+            out.view(-1)[j] = (d[0] - d[1]) / (2 * h)
+        return out
+
+    def loss(x, w, b):
+        return (R.layer_norm(x, None, w, b, 1e-5)[0][1] * f64(dy)).sum() + (x * f64(dv)).sum()
+    args = [f64(x), f64(w), f64(b)]
+    for i, got in enumerate((dh, dw, db)):
+        ref = differences(loss, args, i)
+        assert (got.cpu().double() - ref).abs().max() < 1e-5 * (1 + ref.abs().max())
+    z = rand(g, N, D, std=2.0)
+    z[z.abs() < 0.01] = 0.5  # away from relu's kink
+    for act in moe.MOE_ACTIVATIONS:
+        dz, dbias = torch.empty((N, D), device="cuda"), torch.empty(D, device="cuda")
+        moe.moe_linear_backward(dev(dy), dev(z), dz, dbias, workspace(moe.moe_linear_backward_workspace_size(N, D, "f32")),
+                                act=act)
+        ref = differences(lambda z: (R.act(z, act) * f64(dy)).sum(), [f64(z)], 0)
+        assert (dz.cpu().double() - ref).abs().max() < 1e-5 * (1 + ref.abs().max())
+        assert (dbias.cpu().double() - ref.sum(0)).abs().max() < 1e-5 * (1 + ref.abs().max())
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
