@@ -3,7 +3,8 @@
 //   z = x W^T + bias      y = act(z) + residual
 //
 // Both operands are contiguous in the reduction index (W is [out, in] row-major). Forms, picked by linear_plan:
-//  - linear_few (both types, up to 16 rows): a stream of W, the reduction split over a block's waves;
+//  - linear_few (both types, up to 16 rows, and up to 64 where x is small): a stream of W, the reduction split over a
+//    block's waves;
 //  - linear_w8 (bfloat16, many rows): 256 x 256 tiles on the eight-wave K loop of the expert GEMMs (gemm_w8.h), a
 //    static walk over the tiles, one block per CU;
 //  - linear_tile (both types): 64 rows (bfloat16: to 256) x 64 or 128 columns, the reduction split over blocks where the tiles alone
@@ -108,7 +109,7 @@ __device__ inline void wait_steps(int n) {
   }
 }
 
-// ---- up to 16 rows ----
+// ---- up to 64 rows ----
 //
 // A stream of W: a block holds 16 columns, its waves a run of the reduction each, with a ring of their own and no barrier
 // until the end, where their sums meet in LDS. A step is 128 bytes of every row, whole lines per load, as in the tiles
@@ -117,7 +118,8 @@ template <typename T, int NX, int NW, int S>
 struct LinFew {
   static constexpr int STAGE = (2 + NX) * 1024, PER = 2 + NX;
   static constexpr int LDS = NW * S * STAGE;
-  static_assert(LDS <= 80 * 1024 && LDS >= NW * 1024, "two blocks per CU; the sums");
+  static constexpr int TM = (NX + 1) / 2;  // 16-row tiles
+  static_assert(LDS <= 80 * 1024 && LDS >= NW * TM * 1024 && TM <= NW, "two blocks per CU; the sums, a tile per wave");
 };
 
 template <typename T, int NX, int NW, int S>
@@ -134,11 +136,16 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
   const __amdgpu_buffer_rsrc_t rb =
       __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + (int64_t)col0 * a.K), (short)0, -1, kRawBufferWord3);
   auto swz = [](int r) { return (r ^ (r >> 3)) & 7; };
+  constexpr int TM = L::TM;
   uint32_t ox[NX], ow[2];
+#pragma unroll
+  for (int i = 0; i < NX; ++i) {
+    const int r = 8 * i + (lane >> 3), c = (lane & 7) ^ swz(r);
+    ox[i] = (uint32_t)min(r, rows - 1) * (uint32_t)(a.K * (int)sizeof(T)) + 16 * c;
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = 8 * i + (lane >> 3), c = (lane & 7) ^ swz(r);
-    if (i < NX) ox[i] = (uint32_t)min(r, rows - 1) * (uint32_t)(a.K * (int)sizeof(T)) + 16 * c;
     ow[i] = (uint32_t)min(r, a.M - 1 - col0) * (uint32_t)(a.K * (int)sizeof(T)) + 16 * c;
   }
   char* const ring = lds + wave * (S * L::STAGE);
@@ -154,20 +161,27 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
     at += 128;
   };
   const int r16 = lane & 15, kq = lane >> 4;
-  int fw[2], fx[2];
+  int fw[2], fx[TM][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     fw[h] = r16 * 128 + 16 * ((4 * h + kq) ^ swz(r16));
-    fx[h] = 2048 + (NX == 1 ? (r16 & 7) * 128 + 16 * ((4 * h + kq) ^ swz(r16 & 7)) : fw[h]);
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int r = NX == 1 ? r16 & 7 : 16 * j + r16;
+      fx[j][h] = 2048 + r * 128 + 16 * ((4 * h + kq) ^ swz(r));
+    }
   }
   typedef typename std::conditional<BF16, bf16x8, f32x4>::type frag;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto step = [&](bool refill) {
-    frag w[2], x[2];
+    frag w[2], x[TM][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       w[h] = *(const frag*)(ring + get + fw[h]);
-      x[h] = *(const frag*)(ring + get + fx[h]);
+#pragma unroll
+      for (int j = 0; j < TM; ++j) x[j][h] = *(const frag*)(ring + get + fx[j][h]);
     }
     get = get == (S - 1) * L::STAGE ? 0 : get + L::STAGE;
     wait_lgkm0();  // in registers: the stage may be refilled
@@ -175,12 +189,15 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
     if (refill) issue();
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if constexpr (BF16) {
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[h], x[h], acc, 0, 0, 0);
-      } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(w[h][u], x[h][u], acc, 0, 0, 0);
-      }
+      for (int u = 0; u < (BF16 ? 1 : 4); ++u)
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          if constexpr (BF16)
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[h], x[j][h], acc[j], 0, 0, 0);
+          else
+            acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[h][u], x[j][h][u], acc[j], 0, 0, 0);
+        }
     }
   };
   const int ahead = min(S, nk);
@@ -198,15 +215,17 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
   }
   __syncthreads();  // every ring has been read
   f32x4* sums = (f32x4*)lds;
-  sums[wave * 64 + lane] = acc;
-  __syncthreads();
-  const int col = col0 + 4 * kq;
-  if (wave != 0 || r16 >= rows || col >= a.M) return;
 #pragma unroll
-  for (int w = 1; w < NW; ++w) acc += sums[w * 64 + lane];
-  float v[4] = {acc[0], acc[1], acc[2], acc[3]}, bias[4];
+  for (int j = 0; j < TM; ++j) sums[(wave * TM + j) * 64 + lane] = acc[j];
+  __syncthreads();
+  const int col = col0 + 4 * kq, row = 16 * wave + r16;  // wave j ends the j-th tile
+  if (wave >= TM || row >= rows || col >= a.M) return;
+  f32x4 sum = sums[wave * 64 + lane];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) sum += sums[(w * TM + wave) * 64 + lane];
+  float v[4] = {sum[0], sum[1], sum[2], sum[3]}, bias[4];
   load_bias<4>(a, col, bias);
-  epilogue<4>(a, r16, col, v, bias);
+  epilogue<4>(a, row, col, v, bias);
 }
 
 // ---- tiles of 64 to 256 rows x 64 or 128 columns ----
@@ -719,6 +738,12 @@ hipError_t run_few(const LinArgs<T>& a, hipStream_t s) {
   const dim3 grid((a.M + 15) / 16);
   if (a.R <= 8)
     hipLaunchKernelGGL((linear_few<T, 1, 8, 3>), grid, dim3(512), 0, s, a);
+  else if (a.R > 48)
+    hipLaunchKernelGGL((linear_few<T, 8, 4, 2>), grid, dim3(256), 0, s, a);
+  else if (a.R > 32)
+    hipLaunchKernelGGL((linear_few<T, 6, 4, 2>), grid, dim3(256), 0, s, a);
+  else if (a.R > 16)
+    hipLaunchKernelGGL((linear_few<T, 4, 4, 3>), grid, dim3(256), 0, s, a);
   else
     hipLaunchKernelGGL((linear_few<T, 2, 4, 4>), grid, dim3(256), 0, s, a);
   return hipGetLastError();
@@ -841,7 +866,7 @@ int64_t linear_back_runs(int64_t R, int out) {
 
 namespace {
 
-constexpr int kFewRows = 16;
+constexpr int kFewRows = 16, kMostFewRows = 64;
 constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32}, kMostSplits = 32;
 constexpr int64_t kMostPart = (int64_t)1 << 23;  // floats of a split call's parts: 32 MiB of workspace
 
@@ -876,7 +901,8 @@ double tile_cost(const TileCost& c, bool f32, int64_t tiles, int64_t R, int in, 
 }  // namespace
 
 LinearPlan linear_plan(int dtype, int64_t R, int in, int out) {
-  if (R <= kFewRows) return LinearPlan{kFewRows, 16, 1};
+  const LinearPlan few{16, 16, 1};
+  if (R <= kFewRows) return few;
   const bool f32 = dtype == MOE_F32;
   LinearPlan best{0, 0, 1};
   double least = 0;
@@ -892,6 +918,15 @@ LinearPlan linear_plan(int dtype, int64_t R, int in, int out) {
         best = LinearPlan{c.bm, c.bn, splits};
       }
     }
+  }
+  // Up to 64 rows the tiles and linear_few come close, and the weights of a usual call are not in the caches: tiles draw
+  // them at no more than 4.5 TB/s then, linear_few at 5.5; but it reads x again for every 16 columns, at 55 GB/s into a
+  // CU's LDS and 12 TB/s into all. Fitted to 118 shapes of 17 to 64 rows: 0.5% slower than the better one on average (tiles
+  // alone 29%, linear_few alone 8%).
+  if (R <= kMostFewRows) {
+    const double size = f32 ? 4.0 : 2.0, weights = size * in * out, blocks = (out + 15) / 16, each = (16.0 + R) * size * in;
+    const double stream = std::max({std::ceil(blocks / 256) * each / 5.5e4, blocks * each / 1.2e7, weights / 5.5e6});
+    if (2.0 + stream < std::max(1.3 * least, 2.0 + (best.splits > 1 ? 3.0 : 0.0) + weights / 4.5e6)) return few;
   }
   return best;
 }

@@ -123,7 +123,7 @@ LINEAR_CASES = [
     (65, 640, 136), (128, 2048, 264), (129, 1024, 520), (257, 256, 128), (300, 3008, 64), (1000, 192, 384),
     # tiles of 64 to 256 rows and 64 or 128 columns (256 columns: below), each with one part of the reduction and several
     (66, 64, 8304), (17, 1280, 5472), (145, 256, 11000), (66, 1792, 8352), (325, 64, 11208), (133, 3456, 5528),
-    (132, 64, 10960), (18, 768, 11016),
+    (132, 64, 10960), (18, 768, 11016), (20, 14080, 1800), (50, 896, 72), (40, 704, 328), (64, 64, 8),
 ]
 
 
