@@ -35,7 +35,8 @@ P_F32 = 157.3e12
 HBM = 8.0e12  # B/s
 METRIC = "MoE-layer tokens/s + % bf16 MFMA peak (prefill), % HBM BW (decode)"
 DOMINANT = "experts_gate_up"
-KERNEL_SOURCES = ["sparse_moe_layer_gate_amd/csrc/gemm_bf16.hip", "sparse_moe_layer_gate_amd/csrc/gemm_decode.hip",
+KERNEL_SOURCES = ["sparse_moe_layer_gate_amd/csrc/gemm_bf16.hip", "sparse_moe_layer_gate_amd/csrc/gemm_w8.h",
+                  "sparse_moe_layer_gate_amd/csrc/gemm_decode.hip",
                   "sparse_moe_layer_gate_amd/csrc/gemm.hip", "sparse_moe_layer_gate_amd/csrc/dispatch.hip",
                   "sparse_moe_layer_gate_amd/csrc/moe_internal.h"]  # kernels, launch choice, tile lists
 

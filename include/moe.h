@@ -425,7 +425,8 @@ moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t ac
  *   token_mask [N] uint8 or NULL; the scores of a dead token are read but have no effect, whatever they hold
  *   counts [S, E] int32, coef [S, E] float32 (for moe_route_backward): written, or NULL where not wanted
  *   loss [1] float32, written
- *   workspace: at least moe_balance_workspace_size(cfg, N, seq_rows) bytes
+ *   workspace: at least moe_balance_workspace_size(cfg, N, seq_rows) bytes (may be NULL when that is 0). The size
+ *           never falls as N grows.
  * Sums in a fixed order. N k below 2^31, N E below 2^40, the launch below 2^32 threads (any N below 2^26). N = 0 writes 0
  * to loss. */
 size_t moe_balance_workspace_size(const moe_config* cfg, int64_t N, int64_t seq_rows);

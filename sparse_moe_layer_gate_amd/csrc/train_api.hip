@@ -69,6 +69,20 @@ BalanceLayout balance_layout(const BalancePlan& p, int E) {
   w.total = o;
   return w;
 }
+// What any batch of up to N rows may need: sequences of at most 512 rows, or 256 of them, have a block each, and the others
+// share at most 1,024 chunks of 32 rows and more, the last sequence counted as long as the others.
+size_t balance_bytes(const BalancePlan& p, int64_t N, int E) {
+  BalancePlan most = p;
+  most.S = std::min<int64_t>(p.S, 255);
+  most.chunks = 1;
+  if (p.T <= 512) {
+    most.S = p.S;
+    return balance_layout(most, E).total;
+  }
+  const int64_t parts = 2 * std::min<int64_t>((N + 31) / 32, 1024) + most.S;
+  const size_t shares = 4 * (size_t)std::max(p.S, most.S * p.join_parts);
+  return 2 * align_up(4 * (size_t)parts * E) + align_up(4 * (size_t)parts) + align_up(shares) + 256;
+}
 bool balance_fits(const BalancePlan& p) { return launch_fits(p.S * p.chunks, p.threads); }
 
 // ---- tensor lists ----
@@ -258,7 +272,7 @@ moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t ac
 size_t moe_balance_workspace_size(const moe_config* cfg, int64_t N, int64_t seq_rows) {
   if (check_routing(cfg, N, seq_rows) != MOE_OK) return 0;
   const BalancePlan p = balance_plan(N, seq_rows, cfg->n_routed_experts);
-  return balance_fits(p) ? balance_layout(p, cfg->n_routed_experts).total : 0;
+  return balance_fits(p) ? balance_bytes(p, N, cfg->n_routed_experts) : 0;
 }
 
 moe_status moe_balance_loss(const moe_config* cfg, int64_t N, int64_t seq_rows, float weight, const float* scores,
@@ -279,7 +293,7 @@ moe_status moe_balance_loss(const moe_config* cfg, int64_t N, int64_t seq_rows, 
   if (loss == coef || (counts && (void*)counts == coef) || (void*)counts == loss) return MOE_ERR_INVALID_ARG;
   if (scores == coef || (const void*)scores == counts || scores == loss || topk_idx == counts) return MOE_ERR_INVALID_ARG;
   const BalanceLayout L = balance_layout(p, E);
-  if (!workspace_ok(workspace, ws_bytes, L.total)) return MOE_ERR_WORKSPACE;
+  if (!workspace_ok(workspace, ws_bytes, std::max(L.total, balance_bytes(p, N, E)))) return MOE_ERR_WORKSPACE;
   char* ws = (char*)workspace;
   const BalanceCall c{N, seq_rows, E, cfg->num_experts_per_tok, weight, scores, topk_idx, token_mask, counts, coef, loss,
                       (float*)(ws + L.part_p), (int32_t*)(ws + L.part_c), (int32_t*)(ws + L.part_v),

@@ -111,7 +111,8 @@ BAD = moe.make_config(64, 10, 4, 2, 2, 64)
     (bal, dict(N=I63), UNS), (bal, dict(cfg=WIDE, N=1 << 26), UNS), (bal, dict(N=1 << 27, T=1), UNS),
     (bal, dict(weight=NAN), INV), (bal, dict(weight=INF), INV), (bal, dict(s=None), INV), (bal, dict(idx=None), INV),
     (bal, dict(loss=None), INV), (bal, dict(coef=p(5)), INV), (bal, dict(counts=p(4)), INV), (bal, dict(coef=p(0)), INV),
-    (bal, dict(counts=p(1)), INV), (bal, dict(s=ODD), INV), (bal, dict(ws=None), WS), (bal, dict(n=16), WS),
+    (bal, dict(counts=p(1)), INV), (bal, dict(s=ODD), INV), (bal, dict(N=4000, T=4000, ws=None), WS),
+    (bal, dict(N=4000, T=4000, n=16), WS), (bal, dict(T=1, ws=None), WS),
     (back, dict(cfg=BAD), INV), (back, dict(N=-1), INV), (back, dict(T=0), INV), (back, dict(N=1 << 29), UNS),
     (back, dict(dw=None, coef=None), INV), (back, dict(idx=None), INV), (back, dict(s=None), INV), (back, dict(out=None), INV),
     (back, dict(out=p(2)), INV), (back, dict(out=p(3)), INV), (back, dict(out=ODD), INV), (back, dict(N=0, s=None), OK),
@@ -119,6 +120,14 @@ BAD = moe.make_config(64, 10, 4, 2, 2, 64)
 ])
 def test_balance_errors(fn, kw, status):
     assert fn(**kw) == status
+
+
+@pytest.mark.parametrize("T", [1, 100, 512, 513, 700, 1024, 5000, 100000, 1 << 40])
+def test_balance_workspace_never_falls(T):
+    for cfg in (CFG, WIDE):
+        n = np.unique(np.concatenate([np.arange(0, 2000), 2.0 ** np.arange(11, 22, 0.01)]).astype(np.int64))
+        sizes = np.array([moe.moe_balance_workspace_size(cfg, int(i), T) for i in n], np.int64)
+        assert (np.diff(sizes) >= 0).all() and sizes[0] == 0
 
 
 def tensors(*t):
