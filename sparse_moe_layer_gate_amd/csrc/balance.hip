@@ -8,7 +8,8 @@
 // ds_m = alpha / D (dw_m - sum_l dw_l s_l / D); both meet in dlogit = ds s (1 - s).
 //
 // Both directions read the scores once (N E float32) and are bound by that, or for usual batches, which fit the
-// caches, by latency: a row belongs to a group of 8 to 64 lanes, so that its sums are shuffles.
+// caches, by latency: a row belongs to a group of 8 to 64 lanes, so that its sums are shuffles. 8,192 x 256 in sequences of
+// 1,024: 6 us and 5.5 for the join; gradient of 8,000 x 160: 6; 1 M x 64 53 (5.5 TB/s) and 140 (4.2 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

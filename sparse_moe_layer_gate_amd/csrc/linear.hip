@@ -113,7 +113,8 @@ __device__ inline void wait_steps(int n) {
 //
 // A stream of W: a block holds 16 columns, its waves a run of the reduction each, with a ring of their own and no barrier
 // until the end, where their sums meet in LDS. A step is 128 bytes of every row, whole lines per load, as in the tiles
-// below; of x only the first 8 NX rows are copied, and what the products make of the others is not stored.
+// below; of x only the first 8 NX rows are copied, and what the products make of the others is not stored. Bound by HBM
+// with few rows (1 x 5,120 -> 12,288 in bfloat16: 20 us, 6.3 TB/s of W), with more by x, copied for every 16 columns.
 template <typename T, int NX, int NW, int S>
 struct LinFew {
   static constexpr int STAGE = (2 + NX) * 1024, PER = 2 + NX;
@@ -135,7 +136,7 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
   const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)a.x, (short)0, -1, kRawBufferWord3);
   const __amdgpu_buffer_rsrc_t rb =
       __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + (int64_t)col0 * a.K), (short)0, -1, kRawBufferWord3);
-  auto swz = [](int r) { return (r ^ (r >> 3)) & 7; };
+  auto swz = [](int r) { return (r >> 1) & 7; };
   constexpr int TM = L::TM;
   uint32_t ox[NX], ow[2];
 #pragma unroll
@@ -231,8 +232,7 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
 // ---- tiles of 64 to 256 rows x 64 or 128 columns ----
 //
 // Eight waves, two per SIMD. A step covers 128 bytes of every row of x and of W in the tile (64 k of bfloat16, 32 of
-// float32; whole lines per load), copied global -> LDS by direct loads into a ring of S stages, chunk-swizzled as in
-// gemm_w8.h. Waves 0-3 multiply the first half of each step and waves 4-7 the second, each wave a quarter of the tile,
+// float32; whole lines per load), copied global -> LDS by direct loads into a ring of S stages, chunk-swizzled. Waves 0-3 multiply the first half of each step and waves 4-7 the second, each wave a quarter of the tile,
 // so that a wave's share is as large as the registers allow and LDS is read least; at the end the halves exchange sums.
 //  - One barrier per step: behind it the next step has landed and every wave has read the present one into registers,
 //    so its stage is refilled at once, and the next fragments are read while the present products run.
@@ -242,6 +242,8 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
 //    row. A lane of both operands holds the 16 bytes of one chunk of its row: eight k of v_mfma_f32_16x16x32_bf16, or
 //    four k that four steps of v_mfma_f32_16x16x4_f32 take one by one (which k of a chunk meet in one step does not
 //    matter as long as both operands agree).
+// In bfloat16 bound by the latency of the loads (201 x 12,288 -> 5,120 in six parts: 44 us, matrix cores 27% busy, 2.9 TB/s
+// of W; 7 us for the join), in float32 by the matrix cores (1,000 x 1,536 -> 4,096: 95 us, 77% busy).
 template <typename T, int BM_, int BN_>
 struct LinTile {
   static constexpr int BM = BM_, BN = BN_;
@@ -253,11 +255,10 @@ struct LinTile {
   static constexpr int S = BM == 128 || BN == 64 ? 4 : 3;  // BM = 64: two blocks per CU
   static constexpr int XCH = 8 * (TM * TN / 2) * 1024;  // the exchange of sums
   static constexpr int LDS = S * STAGE > XCH ? S * STAGE : XCH;
-  static_assert(LDS <= 160 * 1024 && TM % 2 == 0 && TN % 2 == 0, "LDS; a wave's tiles start at an even one");
-  __device__ static int swz(int r) {
-    r &= 31;
-    return (r ^ (r >> 3)) & 7;
-  }
+  static_assert(LDS <= 160 * 1024 && TM % 2 == 0, "LDS; the halves end half the tiles each");
+  // Over the 16 rows of a fragment no two of the lanes that LDS serves together share banks (with the pattern of gemm_w8.h,
+  // made for 32 rows, half the cycles of the reads were conflicts).
+  __device__ static int swz(int r) { return (r >> 1) & 7; }
 };
 
 template <typename T, int BM, int BN>
@@ -319,15 +320,9 @@ __global__ __launch_bounds__(512) void linear_tile(LinArgs<T> a) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int r16 = lane & 15, kq = lane >> 4;
-  // fragment addresses: 16-row tiles lie 2 KiB apart, and the swizzle alternates with a tile's parity
-  const int chunk = 4 * half + kq;
-  int fa[2], fb[2];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const int c = 16 * (chunk ^ L::swz(p * 16 + r16));
-    fa[p] = wm * TM * 2048 + r16 * 128 + c;
-    fb[p] = BM * 128 + wn * TN * 2048 + r16 * 128 + c;
-  }
+  // fragment addresses: 16-row tiles lie 2 KiB apart
+  const int fc = r16 * 128 + 16 * ((4 * half + kq) ^ L::swz(r16));
+  const int fa = wm * TM * 2048 + fc, fb = BM * 128 + wn * TN * 2048 + fc;
   typedef typename std::conditional<std::is_same<T, uint16_t>::value, bf16x8, f32x4>::type frag;
   frag av[2][TM], bv[2][TN];
   constexpr int FRAGS = TM + TN;
@@ -336,9 +331,9 @@ __global__ __launch_bounds__(512) void linear_tile(LinArgs<T> a) {
   auto read_one = [&](auto buf, int f) {  // the f-th of a step's FRAGS fragments
     constexpr int b = decltype(buf)::value;
     if (f < TN)
-      bv[b][f] = *(const frag*)(lds + get + fb[f & 1] + f * 2048);
+      bv[b][f] = *(const frag*)(lds + get + fb + f * 2048);
     else
-      av[b][f - TN] = *(const frag*)(lds + get + fa[(f - TN) & 1] + (f - TN) * 2048);
+      av[b][f - TN] = *(const frag*)(lds + get + fa + (f - TN) * 2048);
   };
   auto got = [&] { get = get + L::STAGE == S * L::STAGE ? 0 : get + L::STAGE; };
   auto read = [&](auto buf) {
@@ -499,7 +494,8 @@ __global__ __launch_bounds__(256) void linear_join(LinArgs<T> a) {
 // The tiles cost the same but for the last row tile's, so each block walks them without claiming: per XCD a run of
 // logical ids of nearly equal length (xcd_logical_block), its blocks taking every 32nd. The epilogue goes through LDS
 // in float32, 32 rows of a wave's 64 at a time, so that a lane holds eight consecutive columns of a row: bias, z,
-// activation and residual are applied there, with whole 16-byte loads and stores, and y is rounded once.
+// activation and residual are applied there, with whole 16-byte loads and stores, and y is rounded once. Bound by the
+// matrix cores: 8,191 x 5,120 -> 12,288 with gelu and z 815 us, 1,265 TFLOP/s, 71% busy.
 constexpr int kStagePitch = 128 + 8;  // floats: rows four apart, which one store writes together, lie 32 banks apart
 
 // The K loop of one wave on the ring of Wave8Tile (two stages of x rows, three of W rows): the wave's 64 rows x 128
@@ -787,8 +783,9 @@ hipError_t linear_t(const LinearCall& c, const LinearPlan& p, hipStream_t s) {
 //
 // Eight columns per thread, up to 64 lanes per row, several rows per wave where the rows are narrower. A block takes every
 // runs-th piece of the rows, four rows of a lane in flight; its column sums go to one row of the partial array, which
-// launch_column_sums adds in order.
-// 65,536 x 2,048 in bfloat16: 179 us, with twice the blocks 213; 131,072 x 1,024 in float32 354 and 396.
+// launch_column_sums adds in order. Bound by HBM: 4,096 x 12,288 in bfloat16 with gelu 68 us and 5 for the join, 4.4 TB/s, the
+// vector unit 57% busy.
+// Blocks: 65,536 x 2,048 in bfloat16: 179 us, with twice the blocks 213; 131,072 x 1,024 in float32 354 and 396.
 constexpr int kBackBlocks = 1024;
 
 int back_lanes(int M) {
