@@ -1,7 +1,7 @@
 """MI355X (gfx950) sparse-MoE FFN forward of GLM-4.5 / GLM-5: Python binding of libmoe.so.
 
-Argument marshalling only: every step of the layer runs in the HIP kernels behind the C ABI declared in
-include/moe.h (moe_route, moe_dispatch, moe_forward, moe_workspace_size, moe_status_str). Tensors are
+Argument marshalling only: every step of the layer, of the operators around it and of those of a training step runs
+in the HIP kernels behind the C ABI declared in include/moe.h, under its names. Tensors are
 torch device tensors; the binding checks their device, dtype, shape and contiguity, passes raw pointers
 and the current HIP stream, and raises MoeError on any status other than MOE_OK. There is no fallback:
 without the built library every call raises.
