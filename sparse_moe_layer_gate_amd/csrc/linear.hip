@@ -781,12 +781,14 @@ hipError_t linear_t(const LinearCall& c, const LinearPlan& p, hipStream_t s) {
 
 // ---- the gradients of the epilogue ----
 //
-// Eight columns per thread, up to 64 lanes per row, several rows per wave where the rows are narrower. A block takes every
-// runs-th piece of the rows, four rows of a lane in flight; its column sums go to one row of the partial array, which
-// launch_column_sums adds in order. Bound by HBM: 4,096 x 12,288 in bfloat16 with gelu 68 us and 5 for the join, 4.4 TB/s, the
-// vector unit 57% busy.
-// Blocks: 65,536 x 2,048 in bfloat16: 179 us, with twice the blocks 213; 131,072 x 1,024 in float32 354 and 396.
-constexpr int kBackBlocks = 1024;
+// Eight columns per thread, up to 64 lanes per row, several rows per wave where the rows are narrower. A block takes the
+// rows of every runs-th step, so that the blocks at work lie side by side in memory; its column sums go to one row of the
+// partial array, which launch_column_sums adds in order. One row of a lane in flight and not four, whose unrolled
+// exponentials also made small float32 calls twice as long: 8,192 x 12,288 in bfloat16 134 -> 119 us, 131,072 x 1,024 in
+// float32 355 -> 295. Bound by HBM: 4,096 x 12,288 in bfloat16 with gelu 58 us and 4.5 for the join, 5.2 TB/s.
+// The blocks of a large call have as many bytes in flight in both types (524,288 x 256 with 1,024 blocks: bfloat16
+// 169 us for 160, float32 319 for 300).
+constexpr int kBackBlocks = 1536, kBackBlocksF32 = 768;
 
 int back_lanes(int M) {
   int lanes = 1;
@@ -794,39 +796,30 @@ int back_lanes(int M) {
   return lanes;
 }
 
-// Rows of a piece: a step of the block, four rows of each lane.
-__host__ __device__ inline int back_rows(int lanes) { return 1024 / lanes; }
-
 template <typename T>
 __global__ __launch_bounds__(256) void linear_back(int64_t R, int M, int act, const T* dy, const T* z, T* dz, float* part,
                                                    int64_t runs, int lanes) {
   __shared__ float join[4][512];
-  const int wave = threadIdx.x >> 6, rows = 256 / lanes, piece = back_rows(lanes);  // rows at a time, of a piece
+  const int wave = threadIdx.x >> 6, rows = 256 / lanes;  // of a step
   const int64_t run = blockIdx.x % runs;
   const int first_col = (int)(blockIdx.x / runs) * 512, c8 = (threadIdx.x & (lanes - 1)) * 8, col = first_col + c8;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (col < M) {
-    for (int64_t n = run * piece + threadIdx.x / lanes; n < R; n += runs * piece) {
-      Raw8<T> rd[4], rz[4];
+    for (int64_t n = run * rows + threadIdx.x / lanes; n < R; n += runs * rows) {
+      const int64_t at = n * M + col;
+      const Raw8<T> rd = raw_load8(dy + at);
+      float d[8], v[8];
+      if (act != MOE_ACT_NONE) {
+        const Raw8<T> rz = raw_load8(z + at);
+        widen8(rd, d);
+        widen8(rz, v);
+        act_slope_times<std::is_same<T, uint16_t>::value, 8>(act, v, d);
+      } else {
+        widen8(rd, d);
+      }
+      if (dz) raw_store8<false>(dz + at, d);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (n + u * rows < R) {
-          rd[u] = raw_load8(dy + (n + u * rows) * M + col);
-          if (act != MOE_ACT_NONE) rz[u] = raw_load8(z + (n + u * rows) * M + col);
-        }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (n + u * rows < R) {
-          float d[8], v[8];
-          widen8(rd[u], d);
-          if (act != MOE_ACT_NONE) {
-            widen8(rz[u], v);
-            act_slope_times<std::is_same<T, uint16_t>::value, 8>(act, v, d);
-          }
-          if (dz) raw_store8<false>(dz + (n + u * rows) * M + col, d);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum[i] += d[i];
-        }
+      for (int i = 0; i < 8; ++i) sum[i] += d[i];
     }
   }
   if (!part) return;
@@ -843,8 +836,9 @@ __global__ __launch_bounds__(256) void linear_back(int64_t R, int M, int act, co
 
 template <typename T>
 hipError_t linear_back_t(const LinearBackCall& c, hipStream_t s) {
-  const int64_t pieces = (c.R + back_rows(back_lanes(c.out)) - 1) / back_rows(back_lanes(c.out));
-  const int64_t most = linear_back_runs(c.R, c.out), each = (pieces + most - 1) / most, runs = (pieces + each - 1) / each;
+  const int rows = 256 / back_lanes(c.out);
+  const int64_t steps = (c.R + rows - 1) / rows, most = linear_back_runs(std::is_same<T, float>::value ? MOE_F32 : MOE_BF16, c.R, c.out);
+  const int64_t each = (steps + most - 1) / most, runs = (steps + each - 1) / each;  // as many steps for each block
   hipLaunchKernelGGL(linear_back<T>, dim3((unsigned)(runs * ((c.out + 511) / 512))), dim3(256), 0, s, c.R, c.out, c.act,
                      (const T*)c.dy, (const T*)c.z, (T*)c.dz, c.dbias ? c.part : nullptr, runs, back_lanes(c.out));
   const hipError_t e = hipGetLastError();
@@ -855,10 +849,11 @@ hipError_t linear_back_t(const LinearBackCall& c, hipStream_t s) {
 }  // namespace
 
 int64_t linear_join_blocks(int64_t R, int out) { return (R * (out / 8) + 255) / 256; }
-int64_t linear_back_runs(int64_t R, int out) {
-  const int64_t columns = (out + 511) / 512, most = std::max<int64_t>(64, kBackBlocks / columns);
-  const int piece = back_rows(back_lanes(out));
-  return std::min((R + piece - 1) / piece, most);
+int64_t linear_back_runs(int dtype, int64_t R, int out) {
+  const int64_t columns = (out + 511) / 512, blocks = dtype == MOE_F32 ? kBackBlocksF32 : kBackBlocks;
+  const int64_t most = std::max<int64_t>(64, blocks / columns);
+  const int rows = 256 / back_lanes(out);
+  return std::min((R + rows - 1) / rows, most);
 }
 
 namespace {

@@ -176,7 +176,7 @@ struct LinearBackCall {
   void* dz;
   float *dbias, *part;
 };
-int64_t linear_back_runs(int64_t R, int out);  // most partial rows of dbias
+int64_t linear_back_runs(int dtype, int64_t R, int out);  // most partial rows of dbias
 hipError_t launch_linear_back(int dtype, const LinearBackCall& c, hipStream_t s);
 
 // ---- balance loss and the router's gradient ----

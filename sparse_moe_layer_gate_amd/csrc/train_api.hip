@@ -247,7 +247,7 @@ moe_status moe_linear(int64_t R, int32_t in, int32_t out, int32_t dtype, int32_t
 
 size_t moe_linear_backward_workspace_size(int64_t R, int32_t out, int32_t dtype) {
   if (check_linear(R, 64, out, dtype) != MOE_OK) return 0;
-  return sizeof(float) * (size_t)linear_back_runs(R, out) * out;
+  return sizeof(float) * (size_t)linear_back_runs(dtype, R, out) * out;
 }
 
 moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t activation, const void* dy,
