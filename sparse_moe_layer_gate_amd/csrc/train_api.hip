@@ -254,13 +254,14 @@ moe_status moe_linear_backward(int64_t R, int32_t out, int32_t dtype, int32_t ac
                                const void* z, void* dz, float* dbias, void* workspace, size_t ws_bytes, void* stream) {
   const moe_status st = check_linear(R, 64, out, dtype);
   if (st != MOE_OK) return st;
-  if (!activation_ok(activation) || (!dz && !dbias) || !aligned16(dbias)) return MOE_ERR_INVALID_ARG;
+  if (!activation_ok(activation) || !aligned16(dbias)) return MOE_ERR_INVALID_ARG;
   hipStream_t s = (hipStream_t)stream;
   if (R == 0) {  // a sum over no rows
     MOE_TRY(ST_LINEAR, launch_fill2_i32((int32_t*)dbias, dbias ? out : 0, nullptr, 0, 0, s));
     return MOE_OK;
   }
-  if (!dy || (!z && activation != MOE_ACT_NONE) || !all_aligned16(dy, z, dz)) return MOE_ERR_INVALID_ARG;
+  if (!dy || (!dz && !dbias) || (!z && activation != MOE_ACT_NONE)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned16(dy, z, dz)) return MOE_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, ws_bytes, dbias ? moe_linear_backward_workspace_size(R, out, dtype) : 0))
     return MOE_ERR_WORKSPACE;
   const LinearBackCall c{R, out, activation, dy, z, dz, dbias, (float*)workspace};
@@ -307,8 +308,8 @@ moe_status moe_route_backward(const moe_config* cfg, int64_t N, const float* sco
                               const uint8_t* token_mask, float* dlogits, void* stream) {
   const moe_status st = check_routing(cfg, N, coef ? seq_rows : 1);
   if (st != MOE_OK) return st;
-  if (!dtopk_w && !coef) return MOE_ERR_INVALID_ARG;
   if (N == 0) return MOE_OK;
+  if (!dtopk_w && !coef) return MOE_ERR_INVALID_ARG;
   if (!scores || !dlogits || (dtopk_w && !topk_idx)) return MOE_ERR_INVALID_ARG;
   if (!all_aligned16(scores, topk_idx, dtopk_w, coef, dloss, token_mask, dlogits)) return MOE_ERR_INVALID_ARG;
   if (dlogits == dtopk_w || dlogits == coef || dlogits == dloss || (const void*)dlogits == topk_idx)

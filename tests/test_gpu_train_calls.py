@@ -333,3 +333,91 @@ def test_balance_rows_behind_4_gib():
     last = empty(n, E)
     moe.moe_route_backward(cfg, n, scores[-n:], idx[-n:], dw[-n:], last, seq_rows=n, coef=coef[-1:])
     assert torch.equal(out[-n:], last)
+
+
+# ---------------------------------------------------------------- nothing outside
+class Guarded:
+    """Outputs and workspaces between runs of a known byte, which no call may change."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, shape, dtype=F32):
+        n = torch.empty(shape, dtype=dtype).nbytes
+        buf = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.all.append((buf, n))
+        return buf[4096:4096 + n].view(dtype).view(shape)
+
+    def workspace(self, n):
+        return self((n,), torch.uint8) if n else None
+
+    def check(self):
+        torch.cuda.synchronize()
+        for buf, n in self.all:
+            assert (buf[:4096] == 0xA5).all() and (buf[4096 + n:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,D", [(1, 8), (5, 264), (67, 1032), (301, 2568), (33, 5128), (9, 12296)])
+def test_layer_norm_writes_its_outputs_alone(N, D, dtype):
+    dt, g, out = TYPES[dtype], gen(N + D), Guarded()
+    x, r, dy = (torch.randn(N, D, generator=g).to(dt).cuda() for _ in range(3))
+    w = torch.randn(D, generator=g).to(dt).cuda()
+    h, y, dh, stats, dw, db = out((N, D), dt), out((N, D), dt), out((N, D), dt), out((N, 2)), out((D,)), out((D,))
+    moe.moe_layer_norm(N, x, r, w, w, h, y, stats)
+    moe.moe_layer_norm_backward(N, h, stats, w, r, dy, dh, dw, db,
+                                out.workspace(moe.moe_layer_norm_workspace_size(N, D, dtype)))
+    out.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("R_,K,M", [(1, 64, 8), (13, 704, 40), (45, 512, 136), (66, 1024, 264), (66, 64, 8304), (145, 256, 11000),
+                                    (133, 3456, 5528), (1793, 128, 7000)])
+def test_linear_writes_its_outputs_alone(R_, K, M, dtype):
+    dt, g, out = TYPES[dtype], gen(R_ + M), Guarded()
+    x, w = torch.randn(R_, K, generator=g).to(dt).cuda(), torch.randn(M, K, generator=g).to(dt).cuda()
+    y, z, dz, db = out((R_, M), dt), out((R_, M), dt), out((R_, M), dt), out((M,))
+    moe.moe_linear(x, w, y, out.workspace(moe.moe_linear_workspace_size(R_, K, M, dtype)), act="silu", z=z)
+    moe.moe_linear_backward(y, z, dz, db, out.workspace(moe.moe_linear_backward_workspace_size(R_, M, dtype)), act="silu")
+    out.check()
+
+
+@pytest.mark.parametrize("N,E,k,T", [(1, 1, 1, 1), (77, 6, 2, 20), (100, 60, 8, 100), (1500, 130, 4, 1400), (4000, 256, 8, 1000),
+                                     (9000, 32, 32, 9000), (70000, 64, 6, 1024), (600, 512, 8, 2)])
+def test_balance_writes_its_outputs_alone(N, E, k, T):
+    g, out = gen(N + E), Guarded()
+    scores = torch.rand(N, E, generator=g).cuda()
+    idx = torch.randint(-1, E + 1, (N, k), generator=g, dtype=torch.int32).cuda()
+    cfg, S = moe.make_config(64, E, 1, 1, k, 64), (N + T - 1) // T
+    counts, coef, loss, d = out((S, E), torch.int32), out((S, E)), out((1,)), out((N, E))
+    moe.moe_balance_loss(cfg, N, scores, idx, T, 0.1, counts, coef, loss,
+                         out.workspace(moe.moe_balance_workspace_size(cfg, N, T)))
+    moe.moe_route_backward(cfg, N, scores, idx, torch.randn(N, k, generator=g).cuda(), d, seq_rows=T, coef=coef)
+    out.check()
+
+
+def test_norm_workspace_of_its_size():
+    out = Guarded()
+    for sizes in ([1], [2048] * 3, [5, 70000, 1], [5000000, 9]):
+        grads = [torch.ones(n + 1, device="cuda")[1:] for n in sizes]
+        norm = out((1,))
+        moe.moe_grad_norm(grads, norm, out.workspace(moe.moe_grad_norm_workspace_size(grads)))
+        assert abs(float(norm) / sum(sizes) ** 0.5 - 1) < 1e-6
+    out.check()
+
+
+def test_no_rows():
+    """Calls without rows write the sums over none and nothing else."""
+    out = Guarded()
+    cfg = moe.make_config(64, 16, 1, 1, 2, 64)
+    none, dw, db, dbias, loss = out((0, 64)), out((64,)), out((64,)), out((64,)), out((1,))
+    moe.moe_layer_norm(0, none, None, None, None, None, none)
+    moe.moe_layer_norm_backward(0, none, out((0, 2)), None, None, none, none, dw, db, None)
+    moe.moe_linear(none, torch.ones(64, 64, device="cuda"), none)
+    moe.moe_linear_backward(none, none, none, dbias, None, act="gelu")
+    moe.moe_linear_backward(none, none, none, None, None, act="gelu")
+    moe.moe_balance_loss(cfg, 0, out((0, 16)), out((0, 2), torch.int32), 4, 1.0, None, None, loss, None)
+    moe.moe_route_backward(cfg, 0, out((0, 16)), out((0, 2), torch.int32), out((0, 2)), out((0, 16)))
+    out.check()
+    for t in (dw, db, dbias, loss):
+        assert (t == 0).all()

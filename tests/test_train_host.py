@@ -67,7 +67,7 @@ def lin_bwd(R=4, M=128, dt=moe.MOE_BF16, act=1, dy=p(0), z=p(1), dz=p(2), db=p(3
     (lin_bwd, dict(R=-1), INV), (lin_bwd, dict(M=4), UNS), (lin_bwd, dict(act=9), INV), (lin_bwd, dict(dy=None), INV),
     (lin_bwd, dict(z=None), INV), (lin_bwd, dict(dz=None, db=None), INV), (lin_bwd, dict(db=ODD), INV),
     (lin_bwd, dict(ws=None), WS), (lin_bwd, dict(n=511), WS),
-    (lin_bwd, dict(R=0, db=None), OK),
+    (lin_bwd, dict(R=0, db=None), OK), (lin_bwd, dict(R=0, dy=None, z=None, dz=None, db=None, ws=None), OK),
 ])
 def test_linear_errors(fn, kw, status):
     assert fn(**kw) == status
@@ -116,6 +116,7 @@ BAD = moe.make_config(64, 10, 4, 2, 2, 64)
     (back, dict(cfg=BAD), INV), (back, dict(N=-1), INV), (back, dict(T=0), INV), (back, dict(N=1 << 29), UNS),
     (back, dict(dw=None, coef=None), INV), (back, dict(idx=None), INV), (back, dict(s=None), INV), (back, dict(out=None), INV),
     (back, dict(out=p(2)), INV), (back, dict(out=p(3)), INV), (back, dict(out=ODD), INV), (back, dict(N=0, s=None), OK),
+    (back, dict(N=0, dw=None, coef=None, idx=None, s=None, out=None), OK),
     (back, dict(cfg=WIDE, N=1 << 26), UNS),
 ])
 def test_balance_errors(fn, kw, status):
