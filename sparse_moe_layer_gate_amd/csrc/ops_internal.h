@@ -184,7 +184,7 @@ struct BalancePlan {
   int64_t T, S;           // rows per sequence (at most N), sequences
   int64_t chunk, chunks;  // rows per block, blocks per sequence
   int threads;
-  int join_parts, join_threads;  // blocks per sequence of the second launch, where chunks > 1; S is at most 1024 then
+  int join_parts, join_threads;  // blocks per sequence of the second launch, where chunks > 1; S is below 256 then
 };
 BalancePlan balance_plan(int64_t N, int64_t T, int E);
 struct BalanceCall {
@@ -199,7 +199,7 @@ struct BalanceCall {
   float* part_p;    // [S chunks, E], with more than one chunk
   int32_t* part_c;  // [S chunks, E]
   int32_t* part_v;  // [S chunks]
-  float* part_l;    // [S], with more than one sequence
+  float* part_l;    // [S], with more than one sequence of one chunk; [S join_parts] of several
   int32_t* done;    // [1], with more than one chunk
 };
 hipError_t launch_balance(const BalanceCall& c, hipStream_t s);
