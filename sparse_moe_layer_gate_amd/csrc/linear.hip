@@ -296,7 +296,10 @@ __global__ __launch_bounds__(512) void linear_tile(LinArgs<T> a) {
     const int r = (wave + 8 * i) * 8 + (lane >> 3), c = (lane & 7) ^ L::swz(r);
     ob[i] = (uint32_t)min(r, a.M - 1 - col0) * (uint32_t)(a.K * (int)sizeof(T)) + 16 * c;
   }
-  int put = 0, at = k0 * 128;  // byte offsets: the stage to fill next, the step's place in a row
+  // byte offsets: the stage to fill next, the step's place in a row. The columns' tiles begin at different steps of their
+  // part and go round: where rows of W lie a multiple of 8 KiB apart, all of them would ask the same few memory channels at
+  // one step (12,288 -> 5,120 with 40 rows 36 -> 31 us, with 128 40 -> 37)
+  int put = 0, at = (k0 + (int)((int64_t)nk * ct / a.col_tiles)) * 128;
   auto load = [&](int i) {  // the i-th of a step's PER loads
     char* st = lds + put + wave * 1024 + i * 8192;  // W's rows lie behind x's
     if (i < NA)
@@ -306,7 +309,7 @@ __global__ __launch_bounds__(512) void linear_tile(LinArgs<T> a) {
   };
   auto loaded = [&] {
     put = put + L::STAGE == S * L::STAGE ? 0 : put + L::STAGE;
-    at += 128;
+    at = at + 128 == (k0 + nk) * 128 ? k0 * 128 : at + 128;
   };
   auto issue = [&] {
 #pragma unroll
@@ -913,8 +916,8 @@ LinearPlan linear_plan(int dtype, int64_t R, int in, int out) {
   }
   // Up to 64 rows the tiles and linear_few come close, and the weights of a usual call are not in the caches: tiles draw
   // them at no more than 4.5 TB/s then, linear_few at 5.5; but it reads x again for every 16 columns, at 55 GB/s into a
-  // CU's LDS and 12 TB/s into all. Fitted to 118 shapes of 17 to 64 rows: 0.5% slower than the better one on average (tiles
-  // alone 29%, linear_few alone 8%).
+  // CU's LDS and 12 TB/s into all. Fitted to 118 shapes of 17 to 64 rows; on 160 others 0.5% slower than the better one on
+  // average (tiles alone 32%, linear_few alone 9%).
   if (R <= kMostFewRows) {
     const double size = f32 ? 4.0 : 2.0, weights = size * in * out, blocks = (out + 15) / 16, each = (16.0 + R) * size * in;
     const double stream = std::max({std::ceil(blocks / 256) * each / 5.5e4, blocks * each / 1.2e7, weights / 5.5e6});
