@@ -866,31 +866,33 @@ constexpr int kFewRows = 16, kMostFewRows = 64;
 constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32}, kMostSplits = 32;
 constexpr int64_t kMostPart = (int64_t)1 << 23;  // floats of a split call's parts: 32 MiB of workspace
 
-// What a call takes with tiles of bm x bn, in microseconds, as fitted to 80 bfloat16 shapes (17 to 6,000 rows, 256 to 12,288
-// input and 64 to 16,384 output features) and 44 float32 ones, each timed with every tile and number of parts: rounds of
-// blocks over the CUs, each of a fixed time and a time per step; or the operands from HBM, where that takes longer; and
-// the parts written, read and joined. Its choice is 0.8% (float32 0.2%) slower than the best of them on average, 11% at
-// most. Against always 128 columns and as many parts as fill the CUs once: 2,166 x 640 -> 368 in float32 21 -> 16 us,
-// 1,500 x 2,048 -> 1,400 24 -> 18, 256 x 4,096 -> 4,096 28 -> 23.
+// What a call takes with tiles of bm x bn, in microseconds: rounds of blocks over the CUs, each of a fixed time and a time
+// per step (less in a last round that leaves CUs idle); or the copies of all tiles into LDS, at the 14.3 TB/s that all CUs
+// together reach, where those take longer (the shorter of the two hides all but an eighth); and the parts written, read
+// and joined. Fitted to the timings of every tile and number of parts at 2,122 shapes (66 to 11,585 rows, 128 to 13,312
+// input and 88 to 16,384 output features, a quarter in float32). On 2,139 others its choice is 0.9% slower than the best on
+// average and 34% at most (the rule before, without the copies and the idle CUs: 2.2%; 8,192 x 12,288 -> 5,120 in bfloat16
+// 1,130 us, so 828).
 struct TileCost {
   int bm, bn;
-  double start, step[2];  // bfloat16, float32: 64 k and 32 k
+  double start, idle;  // idle: a step's time with few blocks over that with one on every CU
+  double step[2], both[2];  // bfloat16 and float32, of 64 and 32 k: one block on a CU, two of 64 rows
 };
-constexpr TileCost kTiles[] = {{64, 64, 2.0, {0.27, 0.54}},
-                               {64, 128, 2.0, {0.43, 0.96}},
-                               {128, 128, 3.0, {0.49, 0}},
-                               {256, 128, 3.7, {0.68, 0}},
-                               {256, 256, 3.6, {1.18, 0}}};  // step 0: bfloat16 only (two blocks of 64 rows do as much)
-constexpr double kTwoBlocks = 1.75;  // a step of two 64-row blocks on one CU over that of one
+constexpr TileCost kTiles[] = {{64, 64, 2.2, 0.9, {0.245, 0.67}, {0.615, 1.36}},
+                               {64, 128, 2.0, 0.9, {0.424, 1.39}, {0.72, 2.65}},
+                               {128, 128, 4.0, 0.9, {0.571, 0}, {0, 0}},
+                               {256, 128, 10.0, 0.7, {0.878, 0}, {0, 0}},
+                               {256, 256, 9.5, 0.85, {1.39, 0}, {0, 0}}};  // 0: not for float32, where 64 rows do as much
 
 double tile_cost(const TileCost& c, bool f32, int64_t tiles, int64_t R, int in, int out, int splits) {
-  const int64_t blocks = tiles * splits;
-  const int all = in / (f32 ? 32 : 64), steps = (all + splits - 1) / splits, per_cu = c.bm == 64 ? 2 : 1;
-  const double rounds = (double)(per_cu == 2 ? (blocks + 511) / 512 : (blocks + 255) / 256);
-  const double step = c.step[f32] * (per_cu == 2 && blocks > 256 ? kTwoBlocks : 1.0);
-  const double bytes = (f32 ? 4.0 : 2.0) * in * ((double)out + R);
-  double t = std::max(rounds * (c.start + steps * step), c.start + bytes / 8.5e6);
-  if (splits > 1) t += 2.0 + 0.1 * splits + 8.0 * splits * R * out / 4.0e6;
+  const int64_t blocks = tiles * splits, round = c.bm == 64 ? 512 : 256, rest = blocks % round;
+  const int all = in / (f32 ? 32 : 64), steps = (all + splits - 1) / splits;
+  const double one = c.step[f32], most = c.bm == 64 ? c.both[f32] : one;
+  double work = (double)(blocks / round) * (c.start + steps * most);
+  if (rest > 0) work += c.start + steps * (rest > 256 ? most : one * (c.idle + (1.0 - c.idle) * (double)rest / 256));
+  const double copies = c.start + (double)tiles * (c.bm + c.bn) * in * (f32 ? 4.0 : 2.0) / 1.43e7;
+  double t = std::max(work, copies) + 0.125 * std::min(work, copies);
+  if (splits > 1) t += 2.5 + 0.2 * splits + 1.7e-6 * splits * R * out;
   return t;
 }
 
@@ -915,14 +917,13 @@ LinearPlan linear_plan(int dtype, int64_t R, int in, int out) {
       }
     }
   }
-  // Up to 64 rows the tiles and linear_few come close, and the weights of a usual call are not in the caches: tiles draw
-  // them at no more than 4.5 TB/s then, linear_few at 5.5; but it reads x again for every 16 columns, at 55 GB/s into a
-  // CU's LDS and 12 TB/s into all. Fitted to 118 shapes of 17 to 64 rows; on 160 others 0.5% slower than the better one on
-  // average (tiles alone 32%, linear_few alone 9%).
+  // Up to 64 rows the tiles and linear_few come close. It reads the weights at 5.5 TB/s, but x again for every 16 columns, at
+  // 60 GB/s into a CU's LDS and 12 TB/s into all; and the tiles' cost, fitted to more rows, is a little off. Fitted to 300
+  // shapes of 17 to 64 rows: 0.2% slower than the better one on average (tiles alone 31%, linear_few alone 9%).
   if (R <= kMostFewRows) {
     const double size = f32 ? 4.0 : 2.0, weights = size * in * out, blocks = (out + 15) / 16, each = (16.0 + R) * size * in;
-    const double stream = std::max({std::ceil(blocks / 256) * each / 5.5e4, blocks * each / 1.2e7, weights / 5.5e6});
-    if (2.0 + stream < std::max(1.3 * least, 2.0 + (best.splits > 1 ? 3.0 : 0.0) + weights / 4.5e6)) return few;
+    const double stream = std::max({std::ceil(blocks / 256) * each / 6.0e4, blocks * each / 1.2e7, weights / 5.5e6});
+    if (1.5 + stream < (f32 ? 0.8 : 1.15) * least) return few;
   }
   return best;
 }

@@ -123,6 +123,7 @@ LINEAR_CASES = [
     (65, 640, 136), (128, 2048, 264), (129, 1024, 520), (257, 256, 128), (300, 3008, 64), (1000, 192, 384),
     # tiles of 64 to 256 rows and 64 or 128 columns (256 columns: below), each with one part of the reduction and several
     (66, 64, 8304), (17, 1280, 5472), (145, 256, 11000), (66, 1792, 8352), (325, 64, 11208), (133, 3456, 5528),
+    (73, 2240, 2808), (140, 896, 11120), (65, 4160, 5416), (455, 640, 12680), (1867, 7232, 272), (68, 960, 2872),
     (132, 64, 10960), (18, 768, 11016), (20, 14080, 1800), (50, 896, 72), (40, 704, 328), (64, 64, 8),
 ]
 
@@ -157,15 +158,15 @@ def test_linear(R_, K, M, dtype):
 
 
 @pytest.mark.parametrize("act", list(moe.MOE_ACTIVATIONS))
-@pytest.mark.parametrize("R_,K,M", [(2000, 256, 6152), (1793, 128, 7000)])
+@pytest.mark.parametrize("R_,K,M", [(2000, 256, 6152), (2100, 320, 5640), (3722, 7232, 272)])
 def test_linear_many_tiles(R_, K, M, act):
-    """256 x 256 tiles, the last ones ragged in both directions."""
+    """256 x 256 tiles, the last ones ragged in both directions, and 256 x 128 with several parts of a long reduction."""
     print(f"[linear] R={R_} K={K} M={M} {act}", flush=True)
     check_linear(R_, K, M, act, "bf16", 5, "brz")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("R_,K,M", LINEAR_CASES + [(2100, 192, 5640)])
+@pytest.mark.parametrize("R_,K,M", LINEAR_CASES + [(2100, 256, 6200), (3722, 7232, 272)])
 def test_linear_exact(R_, K, M, dtype):
     """Whole numbers whose sums stay below 2^24 leave no error before the one rounding."""
     dt = TYPES[dtype]

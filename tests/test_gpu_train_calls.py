@@ -372,7 +372,7 @@ def test_layer_norm_writes_its_outputs_alone(N, D, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("R_,K,M", [(1, 64, 8), (13, 704, 40), (45, 512, 136), (66, 1024, 264), (66, 64, 8304), (145, 256, 11000),
-                                    (133, 3456, 5528), (1793, 128, 7000)])
+                                    (133, 3456, 5528), (140, 896, 11120), (2100, 256, 6200), (3722, 7232, 272)])
 def test_linear_writes_its_outputs_alone(R_, K, M, dtype):
     dt, g, out = TYPES[dtype], gen(R_ + M), Guarded()
     x, w = torch.randn(R_, K, generator=g).to(dt).cuda(), torch.randn(M, K, generator=g).to(dt).cuda()
