@@ -243,7 +243,8 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
 //    four k that four steps of v_mfma_f32_16x16x4_f32 take one by one (which k of a chunk meet in one step does not
 //    matter as long as both operands agree).
 // In bfloat16 with few rows bound by the loads into LDS, x's for every BN columns among them (201 x 12,288 -> 5,120 with
-// 128 x 128 tiles in three parts: 45 us, matrix cores 28% busy, 2.8 TB/s of W; 5 us for the join), in float32 by the matrix cores (1,000 x 1,536 -> 4,096: 95 us, 77% busy).
+// 128 x 128 tiles in three parts: 45 us, matrix cores 28% busy, 2.8 TB/s of W; 5 us for the join), in float32
+// by the matrix cores (1,000 x 1,536 -> 4,096: 95 us, 77% busy).
 template <typename T, int BM_, int BN_>
 struct LinTile {
   static constexpr int BM = BM_, BN = BN_;
