@@ -448,8 +448,8 @@ hipError_t launch_balance(const BalanceCall& c, hipStream_t s) {
   const bool few = p.S * p.join_parts <= kCountedBlocks;
   a.done = p.chunks > 1 && few ? c.done : nullptr;
   hipError_t e = with_shape(c.E, [&](auto g, auto pl, auto v) {
-    hipLaunchKernelGGL((balance_chunks<decltype(g)::value, decltype(pl)::value, decltype(v)::value>), dim3((unsigned)(p.S * p.chunks)),
-                       dim3(p.threads), 0, s, a);
+    hipLaunchKernelGGL((balance_chunks<decltype(g)::value, decltype(pl)::value, decltype(v)::value>),
+                       dim3((unsigned)(p.S * p.chunks)), dim3(p.threads), 0, s, a);
     return hipGetLastError();
   });
   if (e == hipSuccess && p.chunks > 1) {

@@ -5,10 +5,10 @@
 // Both operands are contiguous in the reduction index (W is [out, in] row-major). Forms, picked by linear_plan:
 //  - linear_few (both types, up to 16 rows, and up to 64 where x is small): a stream of W, the reduction split over a
 //    block's waves;
-//  - linear_w8 (bfloat16, many rows): 256 x 256 tiles on the eight-wave K loop of the expert GEMMs (gemm_w8.h), a
-//    static walk over the tiles, one block per CU;
-//  - linear_tile (both types): 64 rows (bfloat16: to 256) x 64 or 128 columns, the reduction split over blocks where the tiles alone
-//    would not fill the CUs; linear_join then adds the parts in order and runs the epilogue.
+//  - linear_w8 (bfloat16, many rows): 256 x 256 tiles of eight waves in the expert GEMMs' layout (gemm_w8.h), a static
+//    walk over the tiles, one block per CU;
+//  - linear_tile (both types): 64 rows (bfloat16: to 256) x 64 or 128 columns, the reduction split over blocks where the
+//    tiles alone would not fill the CUs; linear_join then adds the parts in order and runs the epilogue.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -232,7 +232,8 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
 // ---- tiles of 64 to 256 rows x 64 or 128 columns ----
 //
 // Eight waves, two per SIMD. A step covers 128 bytes of every row of x and of W in the tile (64 k of bfloat16, 32 of
-// float32; whole lines per load), copied global -> LDS by direct loads into a ring of S stages, chunk-swizzled. Waves 0-3 multiply the first half of each step and waves 4-7 the second, each wave a quarter of the tile,
+// float32; whole lines per load), copied global -> LDS by direct loads into a ring of S stages, chunk-swizzled. Waves 0-3
+// multiply the first half of each step and waves 4-7 the second, each wave a quarter of the tile,
 // so that a wave's share is as large as the registers allow and LDS is read least; at the end the halves exchange sums.
 //  - One barrier per step: behind it the next step has landed and every wave has read the present one into registers,
 //    so its stage is refilled at once, and the next fragments are read while the present products run.
@@ -842,7 +843,8 @@ __global__ __launch_bounds__(256) void linear_back(int64_t R, int M, int act, co
 template <typename T>
 hipError_t linear_back_t(const LinearBackCall& c, hipStream_t s) {
   const int rows = 256 / back_lanes(c.out);
-  const int64_t steps = (c.R + rows - 1) / rows, most = linear_back_runs(std::is_same<T, float>::value ? MOE_F32 : MOE_BF16, c.R, c.out);
+  const int dtype = std::is_same<T, float>::value ? MOE_F32 : MOE_BF16;
+  const int64_t steps = (c.R + rows - 1) / rows, most = linear_back_runs(dtype, c.R, c.out);
   const int64_t each = (steps + most - 1) / most, runs = (steps + each - 1) / each;  // as many steps for each block
   hipLaunchKernelGGL(linear_back<T>, dim3((unsigned)(runs * ((c.out + 511) / 512))), dim3(256), 0, s, c.R, c.out, c.act,
                      (const T*)c.dy, (const T*)c.z, (T*)c.dz, c.dbias ? c.part : nullptr, runs, back_lanes(c.out));
