@@ -221,8 +221,8 @@ template <int PIECES>
 __global__ __launch_bounds__(kThreads) void clip_chunks(Table t, const float* norm, float max_norm, float eps,
                                                         int in_place) {
   constexpr int64_t CHUNK = kThreads * 8 * PIECES;
-  const float ratio = max_norm / (*norm + eps);
-  const float scale = ratio >= 1.0f ? 1.0f : ratio;  // a NaN stays one
+  const float total = *norm + eps, ratio = max_norm / total;
+  const float scale = ratio >= 1.0f || total == 0.f ? 1.0f : ratio;  // 0 / 0 is not below 1; a NaN in norm stays one
   if (in_place && scale == 1.0f) return;
   const int c = t.first[t.n] - 1 - (int)blockIdx.x, i = tensor_of(t, c);
   const int64_t at = (int64_t)(c - t.first[i]) * CHUNK, n = min(CHUNK, t.numel[i] - at);

@@ -1,4 +1,6 @@
 """Edges of the operators of a training step on the GPU, against float64 references and exact whole-number results."""
+import math
+
 import pytest
 import torch
 
@@ -8,7 +10,8 @@ from tests._ops import check
 
 pytestmark = pytest.mark.gpu
 
-BF = torch.bfloat16
+BF, F32 = torch.bfloat16, torch.float32
+TYPES = {"bf16": BF, "f32": F32}
 
 
 def gen(seed):
@@ -42,3 +45,26 @@ def test_activation_is_float32_before_the_residual(R_, K, M, act):
                    act=act)
     ref = a + res.double()
     check("y", y, ref, (32 + 8 * z * z) * R.U * a.abs() + 2 * R.U * ref.abs())
+
+
+# ---------------------------------------------------------------- gradient norm and clipping
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_clip_of_zeros_to_nothing(dtype):
+    """No ratio below 1 leaves the scale 1, 0 / 0 too: zeros stay zeros. A NaN in the norm still shows."""
+    dt = TYPES[dtype]
+    ts = [torch.zeros(n, dtype=dt, device="cuda") for n in (5, 3000, 5000000)]
+    norm = torch.full((1,), float("nan"), device="cuda")
+    moe.moe_grad_norm(ts, norm, workspace(moe.moe_grad_norm_workspace_size(ts)))
+    assert float(norm) == 0
+    out = [torch.full_like(t, 7.0) for t in ts]
+    moe.moe_grad_clip(ts, norm, 0.0, out=out, eps=0.0)
+    moe.moe_grad_clip(ts, norm, 0.0, eps=0.0)
+    for t, o in zip(ts, out):
+        assert (t == 0).all() and (o == 0).all()
+    ts[0].fill_(3.0)  # a norm above 0: nothing is left
+    norm.fill_(3.0 * math.sqrt(5))
+    moe.moe_grad_clip(ts, norm, 0.0, eps=0.0)
+    assert (ts[0] == 0).all()
+    norm.fill_(float("nan"))
+    moe.moe_grad_clip(ts, norm, 0.0, eps=0.0)
+    assert ts[1].isnan().all()
