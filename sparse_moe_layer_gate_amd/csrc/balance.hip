@@ -90,6 +90,10 @@ struct Row {
   }
 };
 
+// Float32 holds no reciprocal of a sum below 2^-128. Rows whose scores sum to less than kSmallSum are scaled up first, which
+// is exact and leaves the shares p = s / sum as they are.
+constexpr float kSmallSum = 0x1p-100f, kScaleUp = 0x1p64f;
+
 // One chunk of a sequence's rows. Live tokens add to the sums in registers, the slots to a histogram in LDS (whole numbers:
 // the order does not matter). A sequence of one chunk is finished here.
 template <int G, int PL, int V>
@@ -133,6 +137,11 @@ __global__ __launch_bounds__(1024) void balance_chunks(BalanceArgs a) {
 #pragma unroll
       for (int i = 0; i < R::N; ++i) total += v[u][i];
       total = group_sum<G>(total);
+      if (fabsf(total) < kSmallSum) {
+#pragma unroll
+        for (int i = 0; i < R::N; ++i) v[u][i] *= kScaleUp;
+        total *= kScaleUp;
+      }
       const float inv = total != 0.f ? 1.0f / total : 0.f;
 #pragma unroll
       for (int i = 0; i < R::N; ++i) acc[i] += v[u][i] * inv;
@@ -308,8 +317,9 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
   }
   const bool live = !a.mask || a.mask[n] != 0;
   const float g = a.dloss ? *a.dloss : 1.0f;
-  if (co && live) {
-    float sum = 0.f, dot = 0.f;
+  float sum = 1.0f, dot = 0.f, total = 1.0f, dot_w = 0.f, down = 1.0f;
+  auto add_scores = [&] {
+    sum = dot = 0.f;
 #pragma unroll
     for (int i = 0; i < R::N; ++i) {
       sum += s[i];
@@ -317,27 +327,42 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
     }
     sum = group_sum<G>(sum);
     dot = group_sum<G>(dot);
+  };
+  auto add_slots = [&](float eps) {
+    total = dot_w = 0.f;
+#pragma unroll
+    for (int m = 0; m < SPL; ++m) {
+      total += sw[m];
+      dot_w += sw[m] * w[m];
+    }
+    total = group_sum<G>(total) + eps;
+    dot_w = group_sum<G>(dot_w);
+  };
+  if (co && live) add_scores();
+  if (a.dw && a.norm) add_slots(a.eps);
+  if (fminf(fabsf(sum), fabsf(total)) < kSmallSum) {  // ds s is the same with s times kScaleUp and ds over it
+#pragma unroll
+    for (int i = 0; i < R::N; ++i) s[i] *= kScaleUp;
+#pragma unroll
+    for (int m = 0; m < SPL; ++m) sw[m] *= kScaleUp;
+    down = 1.0f / kScaleUp;
+    if (co && live) add_scores();
+    if (a.dw && a.norm) add_slots(a.eps * kScaleUp);
+  }
+  if (co && live) {
     const float inv = sum != 0.f ? 1.0f / sum : 0.f;
 #pragma unroll
     for (int i = 0; i < R::N; ++i) ds[i] = g * inv * (c[i] - dot * inv);
   }
   if (a.dw) {
     if (a.norm) {
-      float total = 0.f, dot = 0.f;
-#pragma unroll
-      for (int m = 0; m < SPL; ++m) {
-        total += sw[m];
-        dot += sw[m] * w[m];
-      }
-      total = group_sum<G>(total) + a.eps;
-      dot = group_sum<G>(dot);
       // divided, not multiplied by a rounded reciprocal: with one slot the two terms are equal
-      const float mean = total != 0.f ? dot / total : 0.f, scale = total != 0.f ? a.alpha / total : 0.f;
+      const float mean = total != 0.f ? dot_w / total : 0.f, scale = total != 0.f ? a.alpha / total : 0.f;
 #pragma unroll
       for (int m = 0; m < SPL; ++m) w[m] = scale * (w[m] - mean);
     } else {
 #pragma unroll
-      for (int m = 0; m < SPL; ++m) w[m] *= a.alpha;
+      for (int m = 0; m < SPL; ++m) w[m] *= a.alpha * down;
     }
     // every slot to the lane and value of its expert (an id may come up twice: each adds)
 #pragma unroll
@@ -353,7 +378,8 @@ __global__ __launch_bounds__(256) void route_backward(RouteBackArgs a) {
   }
   float* out = a.out + n * a.E;
 #pragma unroll
-  for (int i = 0; i < R::N; ++i) ds[i] = ds[i] == 0.f ? 0.f : ds[i] * s[i] * (1.0f - s[i]);  // whatever a dead token holds
+  for (int i = 0; i < R::N; ++i)  // whatever a dead token holds
+    ds[i] = ds[i] == 0.f ? 0.f : ds[i] * s[i] * fmaf(-s[i], down, 1.0f);
 #pragma unroll
   for (int i = 0; i < PL; ++i) {
     const int e = V * (lane + G * i);

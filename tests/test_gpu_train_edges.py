@@ -68,3 +68,50 @@ def test_clip_of_zeros_to_nothing(dtype):
     norm.fill_(float("nan"))
     moe.moe_grad_clip(ts, norm, 0.0, eps=0.0)
     assert ts[1].isnan().all()
+
+
+# ---------------------------------------------------------------- balance loss and the router's gradient
+@pytest.mark.parametrize("eps", [1e-20, 0.0])
+@pytest.mark.parametrize("N,E,k,T", [(12, 6, 2, 5), (40, 32, 4, 40), (40, 160, 8, 10), (40, 130, 8, 13), (1100, 512, 8, 700),
+                                     (9, 257, 1, 9)])
+def test_scores_whose_sum_has_no_float32_reciprocal(N, E, k, T, eps):
+    """Tokens whose scores are subnormal have the shares of any other token, down to one expert's least score above 0."""
+    g = gen(N + E)
+    scores = torch.rand((N, E), generator=g) * 0.9 + 0.05
+    scores[1::4] *= 1e-40 / E
+    scores[2] = 2.0 ** -149
+    scores[3] = 0.0
+    scores[3, E // 2] = 2.0 ** -149
+    scores[4::16] = 0.0
+    scores[5, :] = 2.0 ** -149
+    scores[5, 0] = 0.75
+    idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(N)]).to(torch.int32)
+    idx[3, 0] = E // 2
+    idx[3, 1:] = -1
+    dw = torch.randn((N, k), generator=g)
+    cfg, S = moe.make_config(64, E, 1, 1, k, 64, eps=eps), (N + T - 1) // T
+    s, i = scores.cuda(), idx.cuda()
+    counts, coef, loss = (torch.empty((S, E), dtype=torch.int32, device="cuda"), torch.empty((S, E), device="cuda"),
+                          torch.empty(1, device="cuda"))
+    moe.moe_balance_loss(cfg, N, s, i, T, 0.5, counts, coef, loss, workspace(moe.moe_balance_workspace_size(cfg, N, T)))
+    (rl, rc, rf), (el, ef) = R.balance(scores.double(), idx, T, 0.5, None)
+    assert torch.equal(counts.cpu().long(), rc)
+    check("loss", loss, rl.view(1), el * rl.abs().view(1))
+    check("coef", coef, rf, ef * rf.abs())
+    c = coef.cpu().double()
+    for norm in (True, False):
+        cfg = moe.make_config(64, E, 1, 1, k, 64, eps=eps, norm=norm)
+        e = float(torch.tensor(eps))  # as float32 holds it
+        for wts, co in ((None, c), (dw, None), (dw, c)):
+            if norm and eps == 0 and wts is not None:
+                wts = wts.clone()
+                wts[4::16] = 0.0  # 0 / 0 in the formula
+            out = torch.empty((N, E), device="cuda")
+            moe.moe_route_backward(cfg, N, s, i, None if wts is None else wts.cuda(), out, seq_rows=T,
+                                   coef=None if co is None else coef)
+            ref, bound = R.route_backward(scores.double(), idx, None if wts is None else wts.double(), 1.0, e, norm, T, co)
+            dead = ~ref.isfinite()  # the formula's 0 / 0: weights of scores that sum to 0, without eps
+            assert not dead.any() or (norm and eps == 0 and wts is not None)
+            assert (out.cpu()[dead] == 0).all()
+            ref[dead], bound[dead] = 0.0, 0.0
+            check("dlogits", out, ref, bound)
