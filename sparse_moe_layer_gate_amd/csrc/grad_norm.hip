@@ -33,7 +33,7 @@ struct Table {
   int64_t numel[kTable];
   int32_t first[kTable + 1];  // first chunk of each tensor; [n]: chunks in all
   uint8_t in_bf16[kTable], out_bf16[kTable];
-  uint8_t skip[kTable];  // values in front of the tensor that its first piece leaves out
+  uint8_t skip[kTable];  // clip: values in front of the tensor that its first piece leaves out
   int n;
 };
 static_assert(sizeof(Table) <= 4000, "kernel arguments");
@@ -104,13 +104,15 @@ __device__ inline int tensor_of(const Table& t, int c) {
   return lo;
 }
 
-// skip: the first values of p, up to a line of them, are not the tensor's.
+// Chunks begin at the tensor's first value wherever it lies, so that the order of the sums, and with it the norm's last bit,
+// does not depend on its address. (290 M values of bfloat16 at an odd multiple of 2 bytes: 120 us, at any other address 98;
+// float32: the same anywhere.)
 template <typename T, int PIECES>
-__device__ inline double chunk_squares(const T* p, int64_t n, int skip) {
+__device__ inline double chunk_squares(const T* p, int64_t n) {
   double s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = 0.0;
-  if (n == kThreads * 8 * PIECES && skip == 0) {  // a whole chunk: every load in flight before the first sum
+  if (n == kThreads * 8 * PIECES) {  // a whole chunk: every load in flight before the first sum
     float f[PIECES][8];
 #pragma unroll
     for (int v = 0; v < PIECES; ++v) load8u(p + (threadIdx.x + v * kThreads) * 8, f[v]);
@@ -121,12 +123,12 @@ __device__ inline double chunk_squares(const T* p, int64_t n, int skip) {
   } else {
     for (int64_t at = threadIdx.x * 8; at < n; at += kThreads * 8) {
       float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (at >= skip && at + 8 <= n) {
+      if (at + 8 <= n) {
         load8u(p + at, f);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (at + i >= skip && at + i < n) f[i] = load1(p + at + i);
+          if (at + i < n) f[i] = load1(p + at + i);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] += (double)f[i] * (double)f[i];
@@ -153,9 +155,8 @@ __global__ __launch_bounds__(kThreads) void norm_chunks(Table t, double* part) {
   constexpr int64_t CHUNK = kThreads * 8 * PIECES;
   const int c = blockIdx.x, i = tensor_of(t, c);
   const int64_t at = (int64_t)(c - t.first[i]) * CHUNK, n = min(CHUNK, t.numel[i] - at);
-  const int skip = at == 0 ? t.skip[i] : 0;
-  const double s = t.in_bf16[i] ? chunk_squares<uint16_t, PIECES>((const uint16_t*)t.in[i] + at, n, skip)
-                                : chunk_squares<float, PIECES>((const float*)t.in[i] + at, n, skip);
+  const double s = t.in_bf16[i] ? chunk_squares<uint16_t, PIECES>((const uint16_t*)t.in[i] + at, n)
+                                : chunk_squares<float, PIECES>((const float*)t.in[i] + at, n);
   const double b = block_sum(s, buf);
   if (threadIdx.x == 0) part[c] = b;
 }
@@ -237,9 +238,8 @@ __global__ __launch_bounds__(kThreads) void clip_chunks(Table t, const float* no
     t.out_bf16[i] ? scale_chunk<PIECES>(pf, ob, n, skip, scale) : scale_chunk<PIECES>(pf, of, n, skip, scale);
 }
 
-// A tensor is walked from the start of the 128-byte line that it begins in, so that the blocks' loads and stores cover
-// whole lines (16-byte loads at odd 2-byte addresses run at 4.9 TB/s, others at 5.9; non-temporal stores of float32 that
-// straddle lines made norm and clip of 290 M values 429 us, 391 without).
+// The clip walks a tensor from the start of the 128-byte line that it begins in, so that the blocks' loads and stores cover
+// whole lines (non-temporal stores of float32 that straddle lines made norm and clip of 290 M values 429 us, 391 without).
 int lead_of(const moe_tensor& t) {
   return t.numel == 0 ? 0 : (int)((uintptr_t)t.data & 127) / (t.dtype == MOE_BF16 ? 2 : 4);
 }
@@ -253,11 +253,11 @@ int64_t all_values(const moe_tensor* t, int n) {
 }
 
 // Tables of up to kTable tensors and kMost chunks (a longer tensor is cut); f(table, the chunks of the tables before it).
-// Backwards: from the last tensor to the first.
+// For the clip from the last tensor to the first, each from the start of its line.
 template <typename F>
-hipError_t for_tables(const moe_tensor* in, const moe_tensor* out, int n, int64_t chunk, bool backwards, F f) {
+hipError_t for_tables(const moe_tensor* in, const moe_tensor* out, int n, int64_t chunk, bool clip, F f) {
   constexpr int64_t kMost = (int64_t)1 << 22;
-  int i = backwards ? n - 1 : 0;  // the tensor at hand, and how many of its chunks earlier tables hold
+  int i = clip ? n - 1 : 0;  // the tensor at hand, and how many of its chunks earlier tables hold
   int64_t cut = 0, before = 0;
   Table t;
   while (i >= 0 && i < n) {
@@ -265,12 +265,12 @@ hipError_t for_tables(const moe_tensor* in, const moe_tensor* out, int n, int64_
     t.n = 0;
     for (; i >= 0 && i < n && t.n < kTable && count < kMost; ) {
       const moe_tensor& o = out ? out[i] : in[i];
-      const int64_t lead = lead_of(o), values = in[i].numel + lead;
+      const int64_t lead = clip ? lead_of(o) : 0, values = in[i].numel + lead;
       const int64_t left = chunks_of(in[i], (int)lead, chunk) - cut, take = left < kMost - count ? left : kMost - count;
       if (take > 0) {
         const int j = t.n++;
-        // whole tables leave the end of a tensor to the next one, or backwards its beginning
-        const int64_t at = (backwards ? left - take : cut) * chunk;
+        // whole tables leave the end of a tensor to the next one, or in the clip its beginning
+        const int64_t at = (clip ? left - take : cut) * chunk;
         t.in_bf16[j] = in[i].dtype == MOE_BF16;
         t.out_bf16[j] = o.dtype == MOE_BF16;
         t.in[j] = (const char*)in[i].data + (at - lead) * (t.in_bf16[j] ? 2 : 4);
@@ -285,10 +285,10 @@ hipError_t for_tables(const moe_tensor* in, const moe_tensor* out, int n, int64_
         break;
       }
       cut = 0;
-      i += backwards ? -1 : 1;
+      i += clip ? -1 : 1;
     }
     if (t.n == 0) break;
-    if (backwards) {
+    if (clip) {
       for (int a = 0, b = t.n - 1; a < b; ++a, --b) {
         std::swap(t.in[a], t.in[b]);
         std::swap(t.out[a], t.out[b]);
@@ -310,10 +310,10 @@ hipError_t for_tables(const moe_tensor* in, const moe_tensor* out, int n, int64_
 
 }  // namespace
 
-int64_t most_tensor_chunks(const moe_tensor* t, int n) {
+int64_t tensor_chunks(const moe_tensor* t, int n) {
   const int64_t chunk = chunk_values(all_values(t, n));
   int64_t c = 0;
-  for (int i = 0; i < n; ++i) c += chunks_of(t[i], 63, chunk);
+  for (int i = 0; i < n; ++i) c += chunks_of(t[i], 0, chunk);
   return c;
 }
 

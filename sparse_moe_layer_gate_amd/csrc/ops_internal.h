@@ -218,7 +218,7 @@ int64_t route_backward_blocks(int64_t N, int E);  // of 256 threads
 hipError_t launch_route_backward(const RouteBackCall& c, hipStream_t s);
 
 // ---- gradient norm and clipping ----
-int64_t most_tensor_chunks(const moe_tensor* t, int n);  // partial sums of a list of such lengths, wherever it lies
+int64_t tensor_chunks(const moe_tensor* t, int n);  // partial sums of the norm of a list
 hipError_t launch_grad_norm(const moe_tensor* t, int n, double* part, float* norm, hipStream_t s);
 hipError_t launch_grad_clip(const moe_tensor* t, const moe_tensor* out, int n, const float* norm, float max_norm,
                             float eps, hipStream_t s);

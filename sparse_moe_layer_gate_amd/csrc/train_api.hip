@@ -325,7 +325,7 @@ moe_status moe_route_backward(const moe_config* cfg, int64_t N, const float* sco
 // ---- gradient norm and clipping ----
 size_t moe_grad_norm_workspace_size(const moe_tensor* tensors, int32_t n) {
   if (check_tensors(tensors, n) != MOE_OK) return 0;
-  return align_up(sizeof(double) * std::max<int64_t>(1, most_tensor_chunks(tensors, n)));
+  return align_up(sizeof(double) * std::max<int64_t>(1, tensor_chunks(tensors, n)));
 }
 
 moe_status moe_grad_norm(const moe_tensor* tensors, int32_t n, float* norm, void* workspace, size_t ws_bytes,

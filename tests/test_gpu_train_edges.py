@@ -70,6 +70,25 @@ def test_clip_of_zeros_to_nothing(dtype):
     assert ts[1].isnan().all()
 
 
+def test_norm_does_not_depend_on_the_place():
+    """The same values at any address give the same bits. The sum of these squares lies on the border between two float32
+    norms: two of them, each less than half a step of the sum, add to it only where they meet before the large one."""
+    x = torch.zeros(1900)
+    x[0], x[800], x[1600], x[1200], x[400] = 1.0, 2.0 ** -12, 2.0 ** -12, 2.0 ** -24, 2.0 ** -26
+    x[1] = x[2] = math.sqrt(0.98 * 2.0 ** -53)
+    for dt in (F32, BF):
+        v = x.to(dt).cuda()
+        norms = []
+        for at in range(70):
+            buf = torch.full((x.numel() + 128,), 5.0, dtype=dt, device="cuda")
+            t = buf[at:at + x.numel()]
+            t.copy_(v)
+            norm = torch.empty(1, device="cuda")
+            moe.moe_grad_norm([t], norm, workspace(moe.moe_grad_norm_workspace_size([t])))
+            norms.append(float(norm))
+        assert len(set(norms)) == 1, norms
+
+
 # ---------------------------------------------------------------- balance loss and the router's gradient
 @pytest.mark.parametrize("eps", [1e-20, 0.0])
 @pytest.mark.parametrize("N,E,k,T", [(12, 6, 2, 5), (40, 32, 4, 40), (40, 160, 8, 10), (40, 130, 8, 13), (1100, 512, 8, 700),
