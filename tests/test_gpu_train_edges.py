@@ -47,6 +47,41 @@ def test_activation_is_float32_before_the_residual(R_, K, M, act):
     check("y", y, ref, (32 + 8 * z * z) * R.U * a.abs() + 2 * R.U * ref.abs())
 
 
+def whole_numbers(g, *shape, most=3, dtype=BF):
+    return torch.randint(-most, most + 1, shape, generator=g, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("R_,K,M", [(16400, 64, 32776), (12300, 128, 6152), (6200, 192, 6152), (6200, 256, 6152), (6200, 448, 6152)])
+def test_linear_walks_tiles(R_, K, M):
+    """More tiles than two rounds of CUs, ragged on both sides, with reductions from one step on: what a block stages for
+    one tile is out before the next tile's loads come in. Whole numbers, so every float32 sum is exact."""
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x, w = whole_numbers(g, R_, K), whole_numbers(g, M, K)
+    bias, res = whole_numbers(g, M, most=50), whole_numbers(g, R_, M, most=50)
+    sums = x.float() @ w.float().t() + bias.float()
+    ws = workspace(moe.moe_linear_workspace_size(R_, K, M))
+    for parts in ("", "z", "br", "brz"):
+        y = torch.full((R_, M), float("nan"), dtype=BF, device="cuda")
+        z = torch.full((R_, M), float("nan"), dtype=BF, device="cuda") if "z" in parts else None
+        moe.moe_linear(x, w, y, ws, bias=bias if "b" in parts else None, residual=res if "r" in parts else None, act="relu",
+                       z=z)
+        zz = sums if "b" in parts else sums - bias.float()
+        assert z is None or torch.equal(z, zz.to(BF))
+        ref = torch.relu(zz)
+        assert torch.equal(y, (ref + res.float() if "r" in parts else ref).to(BF))
+
+
+def test_linear_outputs_before_and_behind_4_gib():
+    """4.6 GB of y, every row compared, from an output that held no numbers."""
+    g = torch.Generator(device="cuda").manual_seed(90)
+    R_, K, M = 70000, 192, 32776
+    x, w = whole_numbers(g, R_, K), whole_numbers(g, M, K)
+    y = torch.full((R_, M), float("nan"), dtype=BF, device="cuda")
+    moe.moe_linear(x, w, y, workspace(moe.moe_linear_workspace_size(R_, K, M)), act="relu")
+    for at in range(0, R_, 8192):
+        assert torch.equal(y[at:at + 8192], torch.relu(x[at:at + 8192].float() @ w.float().t()).to(BF))
+
+
 # ---------------------------------------------------------------- gradient norm and clipping
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_clip_of_zeros_to_nothing(dtype):
@@ -87,6 +122,63 @@ def test_norm_does_not_depend_on_the_place():
             moe.moe_grad_norm([t], norm, workspace(moe.moe_grad_norm_workspace_size([t])))
             norms.append(float(norm))
         assert len(set(norms)) == 1, norms
+
+
+def clip_sizes(chunk, at, line):
+    """Lengths of tensors that lie end to end from value `at` on, so that with what precedes each in its line of `line`
+    values they fill whole chunks, miss one by a value or exceed it by one; more than a launch's table holds."""
+    sizes = []
+    for i in range(130):
+        lead = at % line
+        n = [chunk - 1 - lead, chunk - lead, chunk + 1 - lead, 3 * chunk - lead, 1, 2 * chunk - 1 - lead, 7, 4 * chunk + 1 - lead,
+             0, 2 * chunk + 77][i % 10]
+        sizes.append(n)
+        at += n
+    return sizes
+
+
+@pytest.mark.parametrize("flat", [False, True])
+@pytest.mark.parametrize("dtype,to", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("chunk", [2048, 8192])
+def test_clip_around_chunks(chunk, dtype, to, flat):
+    """Both chunk lengths (lists of up to 4 M values and longer ones) at their edges, every value and what lies around."""
+    dt, ot = TYPES[dtype], TYPES[to]
+    line = 128 // (2 if ot == BF else 4)
+    g = torch.Generator(device="cuda").manual_seed(chunk)
+    sizes = clip_sizes(chunk, 5, line if flat else 1)
+    if chunk == 8192:
+        sizes[60] += 3000000
+        assert sum(sizes) > 1 << 22
+    else:
+        assert sum(sizes) < 1 << 22
+    total = sum(sizes)
+    print(f"[clip] {len(sizes)} tensors, {total} values {dtype} -> {to} flat={flat}", flush=True)
+    if flat:
+        whole = torch.randn(total + 100, generator=g, device="cuda").mul_(0.1).to(dt)
+        grads = list(whole[5:5 + total].split(sizes))
+        buf = torch.full((total + 100,), 7.0, dtype=ot, device="cuda")
+        out = list(buf[5:5 + total].split(sizes))
+    else:
+        grads = [torch.randn(n, generator=g, device="cuda").mul_(0.1).to(dt) for n in sizes]
+        out = [torch.full((n,), 7.0, dtype=ot, device="cuda") for n in sizes]
+    before = [t.clone() for t in grads]
+    norm = torch.full((1,), float("nan"), device="cuda")
+    moe.moe_grad_norm(grads, norm, workspace(moe.moe_grad_norm_workspace_size(grads)))
+    rn, scale = R.clip([t.cpu() for t in before], 0.25, 1e-6)
+    assert abs(float(norm) - rn) <= 1.0001 * R.U * rn
+    moe.moe_grad_clip(grads, norm, 0.25, out=out)
+    flat_in, flat_out = torch.cat(before).cpu().double(), torch.cat(out)
+    check("out", flat_out, flat_in * scale, 4 * R.U * (flat_in * scale).abs())
+    for a, b in zip(grads, before):
+        assert torch.equal(a, b)
+    if flat:
+        assert (buf[:5] == 7).all() and (buf[5 + total:] == 7).all()
+    if dt == ot:
+        edge = [whole[:5].clone(), whole[5 + total:].clone()] if flat else []
+        moe.moe_grad_clip(grads, norm, 0.25)
+        assert torch.equal(torch.cat(grads), flat_out)
+        if flat:
+            assert torch.equal(whole[:5], edge[0]) and torch.equal(whole[5 + total:], edge[1])
 
 
 # ---------------------------------------------------------------- balance loss and the router's gradient
