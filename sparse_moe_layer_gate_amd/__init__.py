@@ -736,7 +736,7 @@ def moe_balance_loss(cfg: MoeConfig, N: int, scores, topk_idx, seq_rows: int, we
 
 def _token_mask(t, N):
     torch = _torch or _import_torch()
-    return _ptr(t, "token_mask", torch.bool if t is not None and t.dtype == torch.bool else torch.uint8, (N,),
+    return _ptr(t, "token_mask", torch.bool if getattr(t, "dtype", None) is torch.bool else torch.uint8, (N,),
                 required=False)
 
 
