@@ -242,8 +242,9 @@ __global__ __launch_bounds__(1024) void balance_join(BalanceArgs a, int parts) {
   }
   if (threadIdx.x < 64) loss = wave_sum(loss);
   if (threadIdx.x == 0) {
-    // the one value that another block reads goes past the caches of this XCD and is there before the count rises; a fence
-    // would write back all that they hold (9.4 us for the launch at 8,192 x 256 in sequences of 1,024, 5.8 without)
+    // The one value that another block reads goes past the caches of this XCD (what a store of agent scope does on gfx950)
+    // and, by the wait, is there before the count rises. That order is the chip's: the language's would be a release fence,
+    // which writes back all that the caches hold (9.4 us for the launch at 8,192 x 256 in sequences of 1,024, 5.8 without).
     __hip_atomic_store(a.part_l + blockIdx.x, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (a.done) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

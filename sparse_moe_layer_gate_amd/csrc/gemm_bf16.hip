@@ -39,6 +39,9 @@ namespace {
 #ifndef MOE_PF_GROUP_COLS_DN
 #define MOE_PF_GROUP_COLS_DN 16
 #endif
+
+// ---- eight-wave kernel for 256-row tiles (layout: gemm_w8.h) ----
+//
 // Per K step t a wave issues its A loads of step t + 1 and works through the step's four 16-wide K
 // slices with the fragments double-buffered by slice: the reads of slice s + 1 are in flight while
 // slice s's MFMAs run. It issues its B loads of step t + 2 with the second slice, waits for its

@@ -27,7 +27,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 //    that half and 128 B rows (wn), as 2 x 4 tiles of v_mfma_f32_32x32x16_bf16 (gate_up: 64 gate rows
 //    and the matching 64 up rows, so SwiGLU pairs stay in one wave);
 //  - the waves of half g load rows [128 g, 128 g + 128) of both operands, four direct loads per lane
-//    of each per step (buffer_load_dwordx4 ... lds through raw buffer descriptors);
+//    of each per step (buffer_load_dwordx4 ... lds through raw buffer descriptors).
 template <bool GATE_UP>
 struct Wave8Tile {
   static constexpr int BM = 256, BN = 256, BK = 64;

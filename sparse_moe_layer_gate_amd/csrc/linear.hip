@@ -781,7 +781,7 @@ hipError_t linear_t(const LinearCall& c, const LinearPlan& p, hipStream_t s) {
   }
   if (p.bm == 64) e = p.bn == 64 ? run_tile<T, 64, 64>(a, s) : run_tile<T, 64, 128>(a, s);
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL(linear_join<T>, dim3((unsigned)linear_join_blocks(c.R, c.out)), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(linear_join<T>, dim3((unsigned)((c.R * (c.out / 8) + 255) / 256)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
@@ -855,7 +855,6 @@ hipError_t linear_back_t(const LinearBackCall& c, hipStream_t s) {
 
 }  // namespace
 
-int64_t linear_join_blocks(int64_t R, int out) { return (R * (out / 8) + 255) / 256; }
 int64_t linear_back_runs(int dtype, int64_t R, int out) {
   const int64_t columns = (out + 511) / 512, blocks = dtype == MOE_F32 ? kBackBlocksF32 : kBackBlocks;
   const int64_t most = std::max<int64_t>(64, blocks / columns);

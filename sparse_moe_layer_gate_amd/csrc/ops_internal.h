@@ -167,7 +167,6 @@ struct LinearPlan {
 };
 LinearPlan linear_plan(int dtype, int64_t R, int in, int out);
 size_t linear_part_bytes(int64_t R, int out);  // workspace; never falls as R grows
-int64_t linear_join_blocks(int64_t R, int out);
 hipError_t launch_linear(int dtype, const LinearCall& c, hipStream_t s);
 struct LinearBackCall {
   int64_t R;
