@@ -21,7 +21,7 @@ __device__ inline float act_sigmoid(float z) {
 // Phi(-a) / exp(-a^2 / 2) for a >= 0: the mass beyond a of the normal distribution over its density's exponential, as a
 // polynomial in 1 / (1 + c a) fitted to erfcx(a / sqrt 2) / 2 by relative error up to a = 14, where the exponential
 // leaves float32: 1.6e-7 with eight terms. (Five terms, 3.2e-5, round 0.3% of bfloat16 results otherwise, with a residual
-// or without, and take 0.3% less time at 8,191 x 5,120 -> 12,288 and 3% less at 6,517 x 320 -> 7,472.)
+// or without, and take 0.3% less time at 8,191 x 5,120 -> 12,288 and 3 to 4% less at 6,517 x 320 -> 7,472.)
 __device__ inline float normal_tail_ratio(float a) {
   const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, a, 1.0f));
   float p = fmaf(0.0354239674f, t, -0.156159341f);

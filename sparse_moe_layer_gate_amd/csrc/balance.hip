@@ -9,7 +9,7 @@
 //
 // Both directions read the scores once (N E float32) and are bound by that, or for usual batches, which fit the
 // caches, by latency: a row belongs to a group of 8 to 64 lanes, so that its sums are shuffles. 8,192 x 256 in sequences of
-// 1,024: 6 us and 5.5 for the join; gradient of 8,000 x 160: 6; 1 M x 64 53 (5.5 TB/s) and 140 (4.2 TB/s).
+// 1,024: 6 us and 5.5 for the join; gradient of 8,000 x 160: 6; 1 M x 64 54 (5.4 TB/s) and 143 (4.1 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -70,7 +70,7 @@ __device__ inline float block_total(float v, float* buf) {
 
 // The scores of a row lie with a group of G lanes: piece i of lane j holds the V experts from V (j + G i) on, one load of V
 // floats. V = 4 needs E to be a multiple of 4; 16 lanes then take a row of up to 64 experts in one load and a wave four
-// rows (one row of 64 lanes and single floats: 1 M rows of 64 experts, gradient 407 us, so 140).
+// rows (one row of 64 lanes and single floats: 1 M rows of 64 experts, gradient 407 us, so 143).
 template <int G, int PL, int V>
 struct Row {
   static constexpr int N = PL * V;  // values per lane
@@ -429,7 +429,7 @@ hipError_t with_shape(int E, F f) {
 }  // namespace
 
 // Rows of a block: a few per group of lanes, with two to four blocks per CU in a large batch (1 M rows of 64 experts in
-// sequences of 512: 57 us, with 32 rows per block 299). One block takes a sequence of up to 512 rows, or one of 256
+// sequences of 512: 59 us, with 32 rows per block 299). One block takes a sequence of up to 512 rows, or one of 256
 // sequences and more (65,536 x 256 in sequences of 512: 17 us, with 64 rows per block 42). A sequence is never shared by
 // more than 512 blocks.
 BalancePlan balance_plan(int64_t N, int64_t T, int E) {

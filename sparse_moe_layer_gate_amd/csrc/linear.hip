@@ -245,7 +245,7 @@ __global__ __launch_bounds__(64 * NW) void linear_few(LinArgs<T> a) {
 //    matter as long as both operands agree).
 // In bfloat16 with few rows bound by the loads into LDS, x's for every BN columns among them (201 x 12,288 -> 5,120 with
 // 128 x 128 tiles in three parts: 45 us, matrix cores 28% busy, 2.8 TB/s of W; 5 us for the join), in float32
-// by the matrix cores (1,000 x 1,536 -> 4,096: 95 us, 77% busy).
+// by the matrix cores (1,000 x 1,536 -> 4,096: 96 us back to back, 103 in a kernel trace, 78% busy).
 template <typename T, int BM_, int BN_>
 struct LinTile {
   static constexpr int BM = BM_, BN = BN_;
@@ -500,8 +500,8 @@ __global__ __launch_bounds__(256) void linear_join(LinArgs<T> a) {
 // logical ids of nearly equal length (xcd_logical_block), its blocks taking every 32nd. The epilogue goes through LDS
 // in float32, 32 rows of a wave's 64 at a time, so that a lane holds eight consecutive columns of a row: bias, z,
 // activation and residual are applied there, with whole 16-byte loads and stores, and y is rounded once. Bound by the
-// matrix cores: 8,191 x 5,120 -> 12,288 with gelu and z 807 to 837 us, 1,230 to 1,280 TFLOP/s,
-// 72% busy.
+// matrix cores: 8,191 x 5,120 -> 12,288 with gelu and z 814 to 823 us, 1,250 to 1,270 TFLOP/s,
+// 71% busy.
 constexpr int kStagePitch = 128 + 8;  // floats: rows four apart, which one store writes together, lie 32 banks apart
 
 // The K loop of one wave on the ring of Wave8Tile (two stages of x rows, three of W rows): the wave's 64 rows x 128
