@@ -460,8 +460,8 @@ typedef struct {
 } moe_tensor;
 
 /* The 2-norm over all values of n tensors: norm[0] = sqrt(sum of squares), float32 on the device. Squares and sums are
- * float64, in an order that the lengths alone fix (the same values give the same bits at any address), so neither overflows
- * nor vanishes where the norm itself is a float32; a NaN gives NaN, an infinity without one infinity. n = 0 or no values: 0.
+ * float64, so neither overflows nor vanishes where the norm itself is a float32, in an order that the lengths alone fix (the
+ * same values give the same bits at any address); a NaN gives NaN, an infinity without one infinity. n = 0 or no values: 0.
  *   workspace: at least moe_grad_norm_workspace_size(tensors, n) bytes, 16-byte aligned; the size depends on the tensors'
  *           lengths alone
  * n up to 65536, 2^40 values in all. */
@@ -469,10 +469,10 @@ size_t moe_grad_norm_workspace_size(const moe_tensor* tensors, int32_t n);
 moe_status moe_grad_norm(const moe_tensor* tensors, int32_t n, float* norm, void* workspace, size_t ws_bytes,
                          void* stream);
 
-/* Clipping by that norm: out = tensor * scale with scale = max_norm / (norm[0] + eps) where that is below 1, else 1,
- * in float32, rounded once (norm and eps both 0: 1). norm is read on the device. out: n tensors of the same numel, each of its own dtype, or NULL:
- * in place (with a scale of 1 the tensors are then left as they are). A norm of infinity gives the scale 0 and a NaN the
- * scale NaN: look at norm before the optimizer's step. No tensor written overlaps norm or another of either list, but
+/* Clipping by that norm: out = tensor * scale with scale = max_norm / (norm[0] + eps) where that is below 1, else 1 (0 / 0
+ * too), in float32, rounded once. norm is read on the device. out: n tensors of the same numel, each of its own dtype, or
+ * NULL: in place (with a scale of 1 the tensors are then left as they are). A norm of infinity gives the scale 0 and a NaN
+ * the scale NaN: look at norm before the optimizer's step. No tensor written overlaps norm or another of either list, but
  * out[i] may be tensors[i] exactly. max_norm >= 0 and eps >= 0, finite. */
 moe_status moe_grad_clip(const moe_tensor* tensors, const moe_tensor* out, int32_t n, const float* norm, float max_norm,
                          float eps, void* stream);
